@@ -9,6 +9,9 @@ Calls (same names as the C ABI in include/fsdpshard.h):
   reduce_shard      fp32 rank-order sum of F bf16 contributions (GPU)
   adamw_shard_step  fused reduce + AdamW + bf16 unflatten of one slice (GPU)
   unflatten_bf16    bf16 copy of an fp32 master slice into the flat layout (GPU)
+and in include/fsdpshard_logits.h:
+  token_logprobs    log probabilities of given tokens, entropies, top alternatives (GPU)
+  distill_topk      divergence from a teacher's top logits (GPU); both with their gradients
 bf16 tensors may be torch.bfloat16, torch.int16 or torch.uint16 (bit patterns); fp32 tensors
 are torch.float32.  All device tensors must be contiguous.
 """
@@ -44,6 +47,16 @@ class _AdamW(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
                 ("grad_scale", ctypes.c_double), ("step", c_i64),
                 ("max_grad_norm", ctypes.c_double), ("grad_sumsq", c_vp)]
+
+
+class _Logits(ctypes.Structure):
+    _fields_ = [("data", c_vp), ("rows", c_i64), ("vocab", c_i64), ("row_stride", c_i64),
+                ("dtype", c_i32), ("scale", ctypes.c_float)]
+
+
+class _Teacher(ctypes.Structure):
+    _fields_ = [("ids", c_vp), ("values", c_vp), ("row_stride", c_i64), ("k", c_i32),
+                ("tail", c_i32)]
 
 
 class _Piece(ctypes.Structure):
@@ -122,6 +135,16 @@ def lib():
                                ctypes.POINTER(_Piece), c_i32, ctypes.POINTER(c_i32)]
     h.reshard_copy.argtypes = [ctypes.POINTER(c_vp), ctypes.POINTER(c_i64), c_i32, c_vp, c_i64,
                                ctypes.POINTER(_Piece), c_i32, c_i32, c_vp]
+    pl, pt = ctypes.POINTER(_Logits), ctypes.POINTER(_Teacher)
+    h.token_logprobs_workspace_bytes.argtypes = [c_i64, c_i64, c_i32]
+    h.token_logprobs_workspace_bytes.restype = c_i64
+    h.token_logprobs.argtypes = [pl, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp]
+    h.token_logprobs_grad.argtypes = [pl, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]
+    h.distill_topk_workspace_bytes.argtypes = [c_i64, c_i64]
+    h.distill_topk_workspace_bytes.restype = c_i64
+    h.distill_topk.argtypes = [pl, pt, c_vp, c_vp, c_vp, c_i64, c_vp]
+    h.distill_topk_grad.argtypes = [pl, pt, c_vp, c_vp, c_vp, c_i64, c_vp]
+    h.distill_topk_loss_grad.argtypes = [pl, pt, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]
     h.fsdpshard_strerror.argtypes = [ctypes.c_int]
     h.fsdpshard_strerror.restype = ctypes.c_char_p
     h.fsdpshard_abi_version.argtypes = []
@@ -146,7 +169,9 @@ def lib():
                  "adamw_shard_step_interleaved", "grads_to_interleaved",
                  "grad_sumsq_shard_interleaved", "reduce_shard_interleaved",
                  "reduce_shard_sumsq_interleaved",
-                 "state_to_blocked", "state_from_blocked"):
+                 "state_to_blocked", "state_from_blocked",
+                 "token_logprobs", "token_logprobs_grad",
+                 "distill_topk", "distill_topk_grad", "distill_topk_loss_grad"):
         getattr(h, name).restype = ctypes.c_int
     _lib_handle = h
     return h
@@ -576,6 +601,211 @@ def unflatten_bf16(master, flat, flat_index0=0, lo=0, segs=None, n_segments=0, n
         _ptr(master, "master", {torch.float32}, n), n, _segs(segs, n_segments), int(n_segments),
         _ptr(flat, "flat"), int(flat_index0), int(lo), _stream(stream, master)))
 
+
+# ------------------------------------------------------------------------------ logits
+
+MAX_TOP = 128                 # alternatives of token_logprobs, places of a teacher's list
+_LOGITS_DTYPES = None
+
+
+def _logits_dtypes():
+    global _LOGITS_DTYPES
+    if _LOGITS_DTYPES is None:
+        import torch
+        _LOGITS_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    return _LOGITS_DTYPES
+
+
+def _matrix(t, what, dtypes):
+    """(pointer, rows, columns, elements between rows) of a 2-D device tensor whose rows are
+    contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions, rows and columns")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} has dtype {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _logits(t, scale):
+    ptr, rows, vocab, stride = _matrix(t, "logits", _logits_dtypes())
+    return _Logits(ptr, rows, vocab, stride, _logits_dtypes()[t.dtype], float(scale))
+
+
+def _teacher(ids, values, rows, tail):
+    import torch
+    ip, ir, ik, istride = _matrix(ids, "teacher_ids", {torch.int32})
+    vp, vr, vk, vstride = _matrix(values, "teacher_values", {torch.float32})
+    if (ir, ik) != (rows, vk) or vr != rows:
+        raise ValueError("teacher_ids and teacher_values need one row for each row of the logits "
+                         "and the same number of places")
+    if istride != vstride:
+        raise ValueError("teacher_ids and teacher_values must have the same row stride")
+    return _Teacher(ip, vp, istride, ik, 1 if tail else 0)
+
+
+def _dlogits(t, logits):
+    ptr, rows, vocab, stride = _matrix(t, "dlogits", {logits.dtype})
+    if tuple(t.shape) != tuple(logits.shape):
+        raise ValueError("dlogits must have the shape of the logits")
+    return ptr, stride
+
+
+def _of(t, what, dtype, numel):
+    """Pointer of a contiguous device tensor of exactly ``numel`` elements (None stays None)."""
+    if t is not None and not isinstance(t, int) and t.numel() != numel:
+        raise ValueError(f"{what} holds {t.numel()} elements, {numel} expected")
+    return _ptr(t, what, {dtype})
+
+
+def _row_workspace(workspace, need, logits, stream):
+    """(pointer, bytes) of a call's workspace; allocated through PyTorch when omitted."""
+    if need < 0:
+        raise ValueError("vocabulary or list size out of range")
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _call_workspace(need, logits.device, stream)
+    return (_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace)
+
+
+def _on_device_of(call, logits, others, stream, run):
+    """run(stream handle) with the logits' device current; all tensors must be on it."""
+    import torch
+    dev = logits.device
+    for t in others:
+        if t is not None and not isinstance(t, int) and t.device != dev:
+            raise ValueError("all tensors of a call must be on one device")
+    handle = _stream(stream, logits)
+    if torch.cuda.current_device() == dev.index:
+        _check(call, run(handle))
+    else:
+        with torch.cuda.device(dev):
+            _check(call, run(handle))
+
+
+def token_logprobs_workspace_bytes(rows, vocab, top_k=0):
+    return int(lib().token_logprobs_workspace_bytes(int(rows), int(vocab), int(top_k)))
+
+
+def token_logprobs(logits, ids=None, logprob=None, entropy=None, stats=None, top_ids=None,
+                   top_logprobs=None, scale=1.0, workspace=None, stream=None):
+    """For every row of ``logits`` ([rows, vocab], bf16, fp16 or fp32, rows contiguous but any
+    distance apart): the log probability of its token into ``logprob`` (float32), the entropy into
+    ``entropy`` (float32), the maximum and log-sum the gradient needs into ``stats`` (float32
+    [rows, 2]) and the K largest into ``top_ids`` (int32 [rows, K]) and ``top_logprobs`` (float32
+    [rows, K]).  Outputs left out are not computed.  ``ids`` (int64): below 0 is a position
+    without a token.  ``scale``: inverse temperature.  ``workspace``: device tensor of at least
+    token_logprobs_workspace_bytes(rows, vocab, K) bytes (allocated here through PyTorch when
+    omitted, and then safe to use with any ``stream``)."""
+    import torch
+    x = _logits(logits, scale)
+    f32, rows, k = torch.float32, x.rows, 0
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("give both of top_ids and top_logprobs, or neither")
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != rows:
+            raise ValueError("top_ids must be [rows, K]")
+        k = top_ids.shape[1]
+    if (ids is None) != (logprob is None):
+        raise ValueError("give both of ids and logprob, or neither")
+    wp, wbytes, workspace = _row_workspace(
+        workspace, lib().token_logprobs_workspace_bytes(rows, x.vocab, k), logits, stream)
+    _on_device_of("token_logprobs", logits,
+                  (ids, logprob, entropy, stats, top_ids, top_logprobs, workspace), stream,
+                  lambda s: lib().token_logprobs(
+                      ctypes.byref(x), _of(ids, "ids", torch.int64, rows),
+                      _of(logprob, "logprob", f32, rows), _of(entropy, "entropy", f32, rows),
+                      _of(stats, "stats", f32, 2 * rows), k,
+                      _of(top_ids, "top_ids", torch.int32, k * rows) if k else None,
+                      _of(top_logprobs, "top_logprobs", f32, k * rows) if k else None,
+                      wp, wbytes, s))
+
+
+def token_logprobs_grad(logits, ids, stats, dlogits, dlogprob=None, entropy=None, dentropy=None,
+                        scale=1.0, stream=None):
+    """Gradient of the logits into ``dlogits`` (their type and shape; may be ``logits`` itself)
+    for gradients ``dlogprob`` of token_logprobs' logprob and ``dentropy`` of its entropy (at
+    least one of them).  ``stats`` and ``entropy`` are what token_logprobs wrote."""
+    import torch
+    x = _logits(logits, scale)
+    f32, rows = torch.float32, x.rows
+    out, ostride = _dlogits(dlogits, logits)
+    if dlogprob is None and dentropy is None:
+        raise ValueError("give dlogprob, dentropy or both")
+    _on_device_of("token_logprobs_grad", logits,
+                  (ids, stats, dlogits, dlogprob, entropy, dentropy), stream,
+                  lambda s: lib().token_logprobs_grad(
+                      ctypes.byref(x), _of(ids, "ids", torch.int64, rows),
+                      _of(stats, "stats", f32, 2 * rows), _of(entropy, "entropy", f32, rows),
+                      _of(dlogprob, "dlogprob", f32, rows), _of(dentropy, "dentropy", f32, rows),
+                      out, ostride, s))
+
+
+def distill_topk_workspace_bytes(rows, vocab):
+    return int(lib().distill_topk_workspace_bytes(int(rows), int(vocab)))
+
+
+def distill_topk(logits, teacher_ids, teacher_values, loss, stats=None, tail=False, scale=1.0,
+                 workspace=None, stream=None):
+    """Loss of every row of the student's ``logits`` against a teacher's top logits, into ``loss``
+    (float32).  ``teacher_ids`` (int32 [rows, K], below 0: empty place) and ``teacher_values``
+    (float32 [rows, K]).  With ``tail`` false the list is renormalised (values: logits or log
+    probabilities, scaled like the student's); with ``tail`` true the values are log probabilities
+    and the mass outside the list is one more place.  ``stats`` (float32 [rows, 4]) receives what
+    the gradient needs.  ``workspace``: at least distill_topk_workspace_bytes(rows, vocab) bytes
+    (allocated here through PyTorch when omitted)."""
+    import torch
+    x = _logits(logits, scale)
+    t = _teacher(teacher_ids, teacher_values, x.rows, tail)
+    wp, wbytes, workspace = _row_workspace(
+        workspace, lib().distill_topk_workspace_bytes(x.rows, x.vocab), logits, stream)
+    _on_device_of("distill_topk", logits, (teacher_ids, teacher_values, loss, stats, workspace),
+                  stream,
+                  lambda s: lib().distill_topk(
+                      ctypes.byref(x), ctypes.byref(t), _of(loss, "loss", torch.float32, x.rows),
+                      _of(stats, "stats", torch.float32, 4 * x.rows), wp, wbytes, s))
+
+
+def distill_topk_grad(logits, teacher_ids, teacher_values, stats, dloss, dlogits, tail=False,
+                      scale=1.0, stream=None):
+    """Gradient of the logits into ``dlogits`` (their type and shape; may be ``logits`` itself)
+    for the gradient ``dloss`` (float32) of distill_topk's loss; ``stats`` is what it wrote."""
+    import torch
+    x = _logits(logits, scale)
+    t = _teacher(teacher_ids, teacher_values, x.rows, tail)
+    out, ostride = _dlogits(dlogits, logits)
+    _on_device_of("distill_topk_grad", logits,
+                  (teacher_ids, teacher_values, stats, dloss, dlogits), stream,
+                  lambda s: lib().distill_topk_grad(
+                      ctypes.byref(x), ctypes.byref(t),
+                      _of(stats, "stats", torch.float32, 4 * x.rows),
+                      _of(dloss, "dloss", torch.float32, x.rows), out, ostride, s))
+
+
+def distill_topk_loss_grad(logits, teacher_ids, teacher_values, dloss, loss, stats, dlogits,
+                           tail=False, scale=1.0, workspace=None, stream=None):
+    """distill_topk and distill_topk_grad in one call, for loss weights that are known before."""
+    import torch
+    x = _logits(logits, scale)
+    t = _teacher(teacher_ids, teacher_values, x.rows, tail)
+    out, ostride = _dlogits(dlogits, logits)
+    f32 = torch.float32
+    wp, wbytes, workspace = _row_workspace(
+        workspace, lib().distill_topk_workspace_bytes(x.rows, x.vocab), logits, stream)
+    _on_device_of("distill_topk_loss_grad", logits,
+                  (teacher_ids, teacher_values, dloss, loss, stats, dlogits, workspace), stream,
+                  lambda s: lib().distill_topk_loss_grad(
+                      ctypes.byref(x), ctypes.byref(t), _of(dloss, "dloss", f32, x.rows),
+                      _of(loss, "loss", f32, x.rows), _of(stats, "stats", f32, 4 * x.rows), out,
+                      ostride, wp, wbytes, s))
+
+
+# ------------------------------------------------------------------------------ measurement aids
 
 def stream_copy(src, dst, nbytes=None, stream=None):
     """Measurement aid: plain 16-byte-vector device copy (bandwidth reference)."""
