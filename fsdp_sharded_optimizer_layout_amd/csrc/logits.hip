@@ -11,6 +11,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "fsdpshard_logits.h"
 #include "stream_common.h"
@@ -25,10 +26,19 @@ using fsdpshard_detail::overlaps;
 constexpr float kInf = __builtin_huge_valf();
 
 // ------------------------------------------------------------------------------------------------
-// Elements.
+// Elements and vectors.  A row is read as 16-byte aligned vectors: the first and the last may reach
+// into a neighbour's elements (the same 16 bytes, hence the same page), which are masked out.
 
 struct Bf16 { uint16_t bits; };
 struct Fp16 { uint16_t bits; };
+
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+
+template <typename T>
+constexpr int kElems = 16 / static_cast<int>(sizeof(T));   // elements of a vector: 8 or 4
+constexpr int kBatch = 32;                                 // elements a thread loads at once
+template <typename T>
+constexpr int kLoads = kBatch / kElems<T>;                 // in 4 or 8 vectors, kBlock apart
 
 __device__ __forceinline__ float widen(Bf16 h) {
     return __uint_as_float(static_cast<uint32_t>(h.bits) << 16);
@@ -37,6 +47,33 @@ __device__ __forceinline__ float widen(Fp16 h) {
     return static_cast<float>(__builtin_bit_cast(_Float16, h.bits));
 }
 __device__ __forceinline__ float widen(float x) { return x; }
+
+template <typename T>
+__device__ __forceinline__ void unpack(u32x4 v, float* x);
+template <>
+__device__ __forceinline__ void unpack<Bf16>(u32x4 v, float* x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(v[i] << 16);
+        x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    }
+}
+template <>
+__device__ __forceinline__ void unpack<Fp16>(u32x4 v, float* x) {
+    using h2 = _Float16 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = v[i];    // by value: a bit_cast of the element itself takes element 0
+        const h2 h = __builtin_bit_cast(h2, w);
+        x[2 * i] = static_cast<float>(h.x);
+        x[2 * i + 1] = static_cast<float>(h.y);
+    }
+}
+template <>
+__device__ __forceinline__ void unpack<float>(u32x4 v, float* x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(v[i]);
+}
 
 // Round to nearest even, once; NaN stays NaN.
 template <typename T>
@@ -52,36 +89,336 @@ __device__ __forceinline__ Bf16 narrow<Bf16>(float x) {
     return Bf16{__builtin_bit_cast(uint16_t, static_cast<__bf16>(x))};
 }
 
-// ------------------------------------------------------------------------------------------------
-// Work-group reductions (kBlock threads); the result is in every thread.
+template <typename T>
+struct Row {
+    const char* base;   // first vector (16-byte aligned, at or before the row)
+    int phase;          // elements of the first vector that belong to the row before
+    int nvec;           // vectors
+    int vocab;
 
-template <typename V, typename Op>
-__device__ V block_reduce(V x, Op op, V* scratch) {
-    const int t = threadIdx.x;
-    __syncthreads();
-    scratch[t] = x;
-    __syncthreads();
-    for (int w = kBlock / 2; w > 0; w >>= 1) {
-        if (t < w) scratch[t] = op(scratch[t], scratch[t + w]);
-        __syncthreads();
+    __device__ __forceinline__ Row(const void* data, int64_t r, int64_t stride, int64_t v) {
+        const char* p = static_cast<const char*>(data) + r * stride * static_cast<int64_t>(sizeof(T));
+        const uintptr_t off = reinterpret_cast<uintptr_t>(p) & 15u;
+        base = p - off;
+        phase = static_cast<int>(off / sizeof(T));
+        vocab = static_cast<int>(v);
+        nvec = (phase + vocab + kElems<T> - 1) / kElems<T>;
     }
-    return scratch[0];
-}
-
-struct Scratch {
-    double d[kBlock];
-    unsigned long long u[kBlock];
+    __device__ __forceinline__ u32x4 load(int v) const {
+        return *reinterpret_cast<const u32x4*>(base + static_cast<int64_t>(v) * 16);
+    }
+    __device__ __forceinline__ float at(int i) const {
+        return widen(*reinterpret_cast<const T*>(base + static_cast<int64_t>(i + phase) *
+                                                            static_cast<int64_t>(sizeof(T))));
+    }
+    // Vector v as floats; elements that are not the row's become -inf.
+    __device__ __forceinline__ void get_masked(int v, float* x) const {
+        unpack<T>(load(v), x);
+#pragma unroll
+        for (int e = 0; e < kElems<T>; ++e) {
+            const int i = v * kElems<T> + e - phase;
+            if (i < 0 || i >= vocab) x[e] = -kInf;
+        }
+    }
+    __device__ __forceinline__ bool first_partial() const { return phase != 0; }
+    __device__ __forceinline__ bool last_partial() const {
+        return (phase + vocab) % kElems<T> != 0;
+    }
 };
 
-__device__ double block_sum(double x, Scratch& sh) {
-    return block_reduce(x, [](double a, double b) { return a + b; }, sh.d);
+// A work-group's part of a row: vectors [lo, hi), of which [va, vb) are whole.  A partial first
+// vector belongs to thread 0, a partial last one to thread 1; the whole ones are dealt in turn.
+struct Part {
+    int lo, hi, va, vb;
+    bool first, last;
+
+    template <typename T>
+    __device__ __forceinline__ Part(const Row<T>& row, int split, int part_vecs) {
+        lo = split * part_vecs;
+        hi = lo + part_vecs < row.nvec ? lo + part_vecs : row.nvec;
+        if (lo > hi) lo = hi;
+        first = lo == 0 && hi > 0 && row.first_partial();
+        last = hi == row.nvec && hi > lo && row.last_partial() && !(first && hi - lo == 1);
+        va = lo + (first ? 1 : 0);
+        vb = hi - (last ? 1 : 0);
+    }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Reductions over a wave through DPP (row shifts, then row broadcasts): lane 63 has the result,
+// which every lane then reads.  The order is fixed.
+
+template <int Ctrl, int RowMask>
+__device__ __forceinline__ float dpp(float identity, float x) {
+    return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        static_cast<int>(__float_as_uint(identity)), static_cast<int>(__float_as_uint(x)), Ctrl,
+        RowMask, 0xF, false)));
 }
-__device__ unsigned long long block_max(unsigned long long x, Scratch& sh) {
-    return block_reduce(x, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; },
-                        sh.u);
+__device__ __forceinline__ float lane63(float x) {
+    return __uint_as_float(static_cast<uint32_t>(
+        __builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(x)), 63)));
 }
 
-// A float's bits as an unsigned integer that grows with the value; -0 and +0 are equal.
+#define WAVE_STEPS(STEP)                                                            \
+    STEP(0x111, 0xF) STEP(0x112, 0xF) STEP(0x114, 0xF) STEP(0x118, 0xF) STEP(0x142, 0xA) \
+    STEP(0x143, 0xC)
+
+__device__ __forceinline__ float wave_max(float x) {
+#define STEP(C, R) x = fmaxf(x, dpp<C, R>(-kInf, x));
+    WAVE_STEPS(STEP)
+#undef STEP
+    return lane63(x);
+}
+__device__ __forceinline__ float wave_sum(float x) {
+#define STEP(C, R) x += dpp<C, R>(0.0f, x);
+    WAVE_STEPS(STEP)
+#undef STEP
+    return lane63(x);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int w = 1; w < kWave; w <<= 1) x += __shfl_xor(x, w);
+    return x;
+}
+
+constexpr int kMaxWaves = 16;
+struct BlockScratch {
+    float f[3][kMaxWaves];
+    double d[2][kMaxWaves];
+    int n;
+    int owner;
+};
+
+// ------------------------------------------------------------------------------------------------
+// Running statistics.  In units of log 2, u = c2 (x - m) with c2 = c log2(e): s = sum 2^u and
+// t = sum 2^u u of the elements seen, m their maximum.  m starts at the lowest float instead of
+// -inf, so that no difference of infinities arises: a -inf element adds 2^-inf = 0, a NaN or +inf
+// makes s NaN, and s = 0 means that nothing unmasked was seen.
+
+constexpr float kLowest = -3.402823466e+38f;
+constexpr float kNegligible = -200.0f;      // 2^-200 is 0 in float32
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct Acc {
+    float m = kLowest, s = 0.0f, t = 0.0f;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The largest of three in one instruction (a plain fmaxf would first quiet each loaded value).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const float* x) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) m = max3(m, x[i], x[i + 1]);
+    return m;
+}
+
+// Move the reference of an accumulator up to m.
+template <bool Entropy>
+__device__ __forceinline__ void rebase(Acc& a, float m, float c2) {
+    const float delta = fmaxf(c2 * (a.m - m), kNegligible);
+    const float f = exp2_fast(delta);
+    if (Entropy) a.t = f * __builtin_fmaf(delta, a.s, a.t);
+    a.s *= f;
+    a.m = m;
+}
+
+// One batch, with its maximum.  Its terms are added up by themselves first: fewer additions at the size of the
+// whole sum.
+template <int N, bool Entropy>
+__device__ __forceinline__ void add_batch(Acc& a, const float* x, float top, float c2) {
+    rebase<Entropy>(a, fmaxf(a.m, top), c2);
+    float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float u0 = c2 * (x[i] - a.m), u1 = c2 * (x[i + 1] - a.m);
+        const float e0 = exp2_fast(u0), e1 = exp2_fast(u1);
+        s0 += e0;
+        s1 += e1;
+        if (Entropy) {
+            t0 = __builtin_fmaf(e0, fmaxf(u0, kNegligible), t0);
+            t1 = __builtin_fmaf(e1, fmaxf(u1, kNegligible), t1);
+        }
+    }
+    a.s += s0 + s1;
+    if (Entropy) a.t += t0 + t1;
+}
+
+// What is known of a set of elements: maximum m, r = sum 2^u - 1 (the maximum's own term left
+// out; -1: no unmasked element, NaN: a NaN or +inf), t = sum 2^u u.
+struct Set {
+    float m, r, t;
+};
+
+// Below this r, the sum of the thread that saw the maximum is taken again without the maximum.
+// Its partial sums were rounded at the size of 1, at most about 48 times, which is no more than
+// 200 roundings of r for any larger r.
+constexpr float kPeaked = 0.25f;
+
+// The sum over the threads of x in a fixed order, in every thread.
+__device__ __forceinline__ float block_sum(float x, BlockScratch& sh, int slot, int waves) {
+    const int wave = threadIdx.x / kWave;
+    const float w = wave_sum(x);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) sh.f[slot][wave] = w;
+    __syncthreads();
+    float total = sh.f[slot][0];
+    for (int i = 1; i < waves; ++i) total += sh.f[slot][i];
+    return total;
+}
+
+// Joins the threads' accumulators.  rest_of(j) is called by all threads and returns this thread's
+// share of sum 2^u over the elements of thread j other than its maximum.
+template <bool Entropy, int Waves, typename RestOf>
+__device__ Set join_threads(Acc a, float c2, BlockScratch& sh, RestOf rest_of) {
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const float wm = wave_max(a.m);
+    __syncthreads();
+    if (lane == 0) sh.f[0][wave] = wm;
+    if (threadIdx.x == 0) sh.owner = -1;
+    __syncthreads();
+    float m = sh.f[0][0];
+#pragma unroll
+    for (int i = 1; i < Waves; ++i) m = fmaxf(m, sh.f[0][i]);
+    const bool top = a.m == m && a.s != 0.0f;      // a NaN sum counts: it must reach the result
+    if (top) sh.owner = threadIdx.x;               // any of several: used only if there is one
+    rebase<Entropy>(a, m, c2);
+    const float wr = wave_sum(top ? a.s - 1.0f : a.s);
+    const float wt = Entropy ? wave_sum(a.t) : 0.0f;
+    const int wn = __popcll(__ballot(top));
+    if (lane == 0) {
+        sh.f[1][wave] = wr;
+        sh.f[2][wave] = wt;
+        sh.d[0][wave] = wn;
+    }
+    __syncthreads();
+    float r = sh.f[1][0], t = sh.f[2][0], n = static_cast<float>(sh.d[0][0]);
+#pragma unroll
+    for (int i = 1; i < Waves; ++i) {
+        r += sh.f[1][i];
+        t += sh.f[2][i];
+        n += static_cast<float>(sh.d[0][i]);
+    }
+    r += n - 1.0f;
+    if (n == 1.0f && r < kPeaked)
+        r = block_sum((top ? 0.0f : a.s) + rest_of(sh.owner, m), sh, 1, Waves);
+    return Set{m, r, t};
+}
+
+// Joins sets (the parts of a row): every wave does the same, a lane takes every 64th set.
+template <typename Get>
+__device__ Set join_sets(int count, float c2, Get get) {
+    const int lane = threadIdx.x % kWave;
+    float m = kLowest;
+    for (int i = lane; i < count; i += kWave) m = fmaxf(m, get(i).m);
+    m = wave_max(m);
+    float r = 0.0f, t = 0.0f, n = 0.0f;
+    for (int i = lane; i < count; i += kWave) {
+        const Set p = get(i);
+        if (p.r == -1.0f) continue;
+        const float delta = fmaxf(c2 * (p.m - m), kNegligible), f = exp2_fast(delta);
+        if (p.m == m) {
+            n += 1.0f;
+            r += p.r;
+        } else {
+            r += f * (1.0f + p.r);
+        }
+        t += f * __builtin_fmaf(delta, 1.0f + p.r, p.t);
+    }
+    r = wave_sum(r) + (wave_sum(n) - 1.0f);
+    return Set{m, r, wave_sum(t)};
+}
+
+struct RowStats {
+    float m, L;      // maximum and log-sum (m = L = -inf: all masked; both NaN: NaN or +inf inside)
+    float entropy;
+};
+
+__device__ __forceinline__ RowStats finish(const Set& x) {
+    if (x.r != x.r) return {x.r, x.r, x.r};
+    if (x.r < 0.0f) return {-kInf, -kInf, 0.0f};
+    const float L = log1pf(x.r);
+    return {x.m, L, L - kLn2 * x.t / (1.0f + x.r)};
+}
+
+__device__ __forceinline__ float log_p(float x, float m, float L, float c) {
+    return x == -kInf ? (m != m ? m : -kInf) : c * (x - m) - L;
+}
+
+// Streams a part: calls batch(x, b) with kBatch floats of this thread's b-th batch of whole
+// vectors (-inf past the end), and edge(x, v) with the kElems floats of a partial vector v.
+template <typename T, typename Batch, typename Edge>
+__device__ __forceinline__ void stream(const Row<T>& row, const Part& part, Batch batch,
+                                       Edge edge) {
+    constexpr int E = kElems<T>, U = kLoads<T>;
+    const int tid = threadIdx.x;
+    int b = 0;
+    for (int v0 = part.va; v0 < part.vb; v0 += U * kBlock, ++b) {
+        u32x4 raw[U];
+        const bool whole = v0 + U * kBlock <= part.vb;
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int v = v0 + q * kBlock + tid;
+            raw[q] = row.load(whole || v < part.vb ? v : part.va);
+        }
+        float x[kBatch];
+#pragma unroll
+        for (int q = 0; q < U; ++q) unpack<T>(raw[q], x + q * E);
+        if (!whole) {
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (v0 + q * kBlock + tid >= part.vb) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[q * E + e] = -kInf;
+                }
+        }
+        batch(x, b);
+    }
+    if ((part.first && tid == 0) || (part.last && tid == 1)) {
+        const int v = tid == 0 ? part.lo : part.hi - 1;
+        float x[E];
+        row.get_masked(v, x);
+        edge(x, v);
+    }
+}
+
+// Calls f(x, v) for the vectors of thread j of a part, dealt over the threads of the work-group.
+template <typename T, typename F>
+__device__ __forceinline__ void vectors_of(const Row<T>& row, const Part& part, int j, F f) {
+    float x[kElems<T>];
+    for (int64_t v = part.va + j + static_cast<int64_t>(threadIdx.x) * kBlock; v < part.vb;
+         v += static_cast<int64_t>(kBlock) * kBlock) {
+        unpack<T>(row.load(static_cast<int>(v)), x);
+        f(x, static_cast<int>(v));
+    }
+    if (threadIdx.x == 0 && ((j == 0 && part.first) || (j == 1 && part.last))) {
+        const int v = j == 0 ? part.lo : part.hi - 1;
+        row.get_masked(v, x);
+        f(x, v);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ float rest_sum(const float* x, float m, float c2) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) s += x[e] == m ? 0.0f : exp2_fast(c2 * (x[e] - m));
+    return s;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Top alternatives.  A candidate is one 64-bit key: the value's bits as an unsigned integer that
+// grows with the value (-0 and +0 equal), then the reversed index.  Keys of a row are distinct, so
+// the K largest and their order do not depend on the order in which candidates are found.
+
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
@@ -89,63 +426,151 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float from_key(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
-constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t order_key16(float x) { return order_key(x) >> 16; }
+constexpr uint32_t kKey16Finite = 0x0080;   // the lowest finite value; -inf is below
 
-struct RowStats {
-    float m, L;      // maximum and log-sum (m = L = -inf: all masked; both NaN: NaN or +inf inside)
-    float entropy;
-};
-
-// Statistics of the elements of a row for which keep(i) holds.
-template <typename T, typename Keep>
-__device__ RowStats row_stats(const T* x, int64_t vocab, float c, Keep keep, Scratch& sh) {
-    double top = -HUGE_VAL, bad = 0.0;
-    for (int64_t i = threadIdx.x; i < vocab; i += kBlock) {
-        if (!keep(i)) continue;
-        const float v = widen(x[i]);
-        if (!(v < kInf)) bad = 1.0;
-        top = fmax(top, static_cast<double>(v));
-    }
-    bad = block_sum(bad, sh);
-    top = block_reduce(top, [](double a, double b) { return fmax(a, b); }, sh.d);
-    RowStats r;
-    if (bad > 0.0) {
-        r.m = r.L = r.entropy = __builtin_nanf("");
-        return r;
-    }
-    if (top == -HUGE_VAL) {
-        r.m = r.L = -kInf;
-        r.entropy = 0.0f;
-        return r;
-    }
-    double s = 0.0, w = 0.0, ones = 0.0;   // terms of the maximum are exactly 1, counted apart
-    for (int64_t i = threadIdx.x; i < vocab; i += kBlock) {
-        if (!keep(i)) continue;
-        const double d = c * (static_cast<double>(widen(x[i])) - top);
-        if (d == 0.0) {
-            ones += 1.0;
-            continue;
-        }
-        const double e = exp(d);
-        s += e;
-        if (e > 0.0) w += e * d;
-    }
-    s = block_sum(s, sh);
-    w = block_sum(w, sh);
-    s += block_sum(ones, sh) - 1.0;
-    const double L = log1p(s);
-    r.m = static_cast<float>(top);
-    r.L = static_cast<float>(L);
-    r.entropy = static_cast<float>(L - w / (1.0 + s));
-    return r;
+__device__ __forceinline__ unsigned long long candidate(float x, int i) {
+    return (static_cast<unsigned long long>(order_key(x)) << 32) |
+           (0xFFFFFFFFu - static_cast<uint32_t>(i));
 }
 
-__device__ __forceinline__ float log_p(float x, float m, float L, float c) {
-    return x == -kInf ? (m != m ? m : -kInf) : c * (x - m) - L;
+constexpr int kMaxPartVecs = 16384;                        // vectors of a part
+constexpr int kMaxBatches = kMaxPartVecs / (kBlock * 4) + 1;
+constexpr int kCandidates = 1024;
+
+struct TopScratch {
+    uint16_t batch_max[kMaxBatches * kBlock];              // 16-bit keys of the batches' maxima
+    uint16_t thread_max[kBlock];
+    alignas(16) unsigned long long cand[kCandidates];
+    uint32_t threshold;
+    int count;
+    int wave_count[kMaxWaves];
+};
+
+// The largest 16-bit value that at least k of the work-group's 256 keys reach (by one wave).
+__device__ uint32_t kth_of_keys16(const uint16_t* keys, int k) {
+    const int lane = threadIdx.x % kWave;
+    uint32_t own[kBlock / kWave];
+#pragma unroll
+    for (int i = 0; i < kBlock / kWave; ++i) own[i] = keys[lane + i * kWave];
+    uint32_t best = 0;
+    for (int bit = 15; bit >= 0; --bit) {
+        const uint32_t probe = best | (1u << bit);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kBlock / kWave; ++i) n += __popcll(__ballot(own[i] >= probe));
+        if (n >= k) best = probe;
+    }
+    return best;
+}
+
+// Writes the `want` largest of the candidates found, in falling order, through put(place, key);
+// places beyond the candidates get key 0.
+template <typename Put>
+__device__ void rank_candidates(const TopScratch& sh, int found, int want, Put put) {
+    for (int i = threadIdx.x; i < found; i += kBlock) {
+        const unsigned long long own = sh.cand[i];
+        int place = 0;
+        for (int j = 0; j < found; ++j) place += sh.cand[j] > own;
+        if (place < want) put(place, own);
+    }
+    for (int i = found + static_cast<int>(threadIdx.x); i < want; i += kBlock) put(i, 0ull);
+}
+
+// Number of elements over the work-group (all threads return it).
+__device__ int block_count(int n, TopScratch& sh) {
+#pragma unroll
+    for (int w = 1; w < kWave; w <<= 1) n += __shfl_xor(n, w);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) sh.wave_count[threadIdx.x / kWave] = n;
+    __syncthreads();
+    int total = 0;
+    for (int i = 0; i < kBlock / kWave; ++i) total += sh.wave_count[i];
+    return total;
+}
+
+// More candidates than fit (many equal values, or the best ones in few threads): find the k-th
+// largest value's key by bisection with counting passes over the part, then take what is above it
+// and, of the equal ones, the lowest indices.  Slow and exact.
+template <typename T>
+__device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint32_t lo_key,
+                                float top, TopScratch& sh) {
+    constexpr int E = kElems<T>;
+    float x[E];
+    // Largest key `at` with count(key >= at) >= k; holds for lo_key, not above the maximum's key.
+    uint32_t at = lo_key, end = order_key(top);
+    while (at < end) {
+        const uint32_t probe = at + (end - at) / 2 + 1;
+        int n = 0;
+        for (int v = part.lo + static_cast<int>(threadIdx.x); v < part.hi; v += kBlock) {
+            row.get_masked(v, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) n += order_key(x[e]) >= probe;
+        }
+        if (block_count(n, sh) >= k) at = probe;
+        else end = probe - 1;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    for (int v = part.lo + static_cast<int>(threadIdx.x); v < part.hi; v += kBlock) {
+        row.get_masked(v, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (order_key(x[e]) > at) {              // fewer than k
+                const int n = atomicAdd(&sh.count, 1);
+                sh.cand[n] = candidate(x[e], v * E + e - row.phase);
+            }
+    }
+    __syncthreads();
+    int have = sh.count;
+    for (int v0 = part.lo; v0 < part.hi && have < k; v0 += kBlock) {
+        const int v = v0 + static_cast<int>(threadIdx.x);
+        int n = 0;
+        if (v < part.hi) {
+            row.get_masked(v, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) n += order_key(x[e]) == at;
+        }
+        int before = n;                              // inclusive prefix over the wave
+        const int lane = threadIdx.x % kWave;
+#pragma unroll
+        for (int w = 1; w < kWave; w <<= 1) {
+            const int y = __shfl_up(before, w);
+            if (lane >= w) before += y;
+        }
+        __syncthreads();
+        if (lane == kWave - 1) sh.wave_count[threadIdx.x / kWave] = before;
+        __syncthreads();
+        int total = 0;
+        for (int i = 0; i < kBlock / kWave; ++i) {
+            if (i < static_cast<int>(threadIdx.x / kWave)) before += sh.wave_count[i];
+            total += sh.wave_count[i];
+        }
+        int place = have + before - n;
+        if (n > 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (order_key(x[e]) == at) {
+                    if (place < k) sh.cand[place] = candidate(x[e], v * E + e - row.phase);
+                    ++place;
+                }
+        }
+        have += total;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = have < k ? have : k;
+    __syncthreads();
 }
 
 // ------------------------------------------------------------------------------------------------
 // Token log probabilities.
+//
+// One work-group streams one part of a row (a whole row when there are enough rows) and joins its
+// threads' running statistics.  For the alternatives it keeps, for each batch of 32 elements of a
+// thread, only the 16-bit key of the maximum.  The k-th largest of the 256 threads' maxima is a
+// lower bound of the k-th largest element, so only batches that reach it are read again (about k
+// of them), and the few elements that reach it are ranked.  The stream itself has no branch.
 
 struct LogprobParams {
     const void* x;
@@ -155,51 +580,289 @@ struct LogprobParams {
     float *logprob, *entropy, *stats;
     int32_t* top_ids;
     float* top_logprobs;
-    int32_t k;
+    int32_t k, splits, part_vecs;
+    float4* part_sets;                 // [rows][splits]: m, r, t
+    unsigned long long* part_keys;     // [rows][splits][k]
 };
 
-template <typename T>
+__device__ __forceinline__ void write_row(const LogprobParams& p, int64_t r, const RowStats& st,
+                                          float token_logit, int64_t y) {
+    if (p.stats) {
+        p.stats[2 * r] = st.m;
+        p.stats[2 * r + 1] = st.L;
+    }
+    if (p.entropy) p.entropy[r] = st.entropy;
+    if (p.logprob)
+        p.logprob[r] = y < 0 ? 0.0f
+                       : y >= p.vocab ? __builtin_nanf("")
+                                      : log_p(token_logit, st.m, st.L, p.c);
+}
+
+__device__ __forceinline__ void write_top(const LogprobParams& p, int64_t r, int place,
+                                          unsigned long long key, const RowStats& st) {
+    const int64_t o = r * p.k + place;
+    p.top_ids[o] = key ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key)) : -1;
+    p.top_logprobs[o] = key ? log_p(from_key(static_cast<uint32_t>(key >> 32)), st.m, st.L, p.c)
+                            : (st.m != st.m ? st.m : -kInf);
+}
+
+template <typename T, bool Top>
 __global__ __launch_bounds__(kBlock) void logprobs_kernel(LogprobParams p) {
-    __shared__ Scratch sh;
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const T* x = static_cast<const T*>(p.x) + r * p.stride;
-        const RowStats st = row_stats(x, p.vocab, p.c, [](int64_t) { return true; }, sh);
-        if (threadIdx.x == 0) {
-            if (p.stats) {
-                p.stats[2 * r] = st.m;
-                p.stats[2 * r + 1] = st.L;
-            }
-            if (p.entropy) p.entropy[r] = st.entropy;
-            if (p.logprob) {
-                const int64_t y = p.ids[r];
-                p.logprob[r] = y < 0 ? 0.0f
-                               : y >= p.vocab ? __builtin_nanf("")
-                                              : log_p(widen(x[y]), st.m, st.L, p.c);
-            }
+    constexpr int E = kElems<T>, U = kLoads<T>;
+    __shared__ BlockScratch bs;
+    __shared__ typename std::conditional<Top, TopScratch, int>::type top_sh;
+    const float c2 = p.c * kLog2e;
+    const int tid = threadIdx.x;
+    const int64_t units = p.rows * p.splits;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t r = unit / p.splits;
+        const int split = static_cast<int>(unit - r * p.splits);
+        const Row<T> row(p.x, r, p.stride, p.vocab);
+        const Part part(row, split, p.part_vecs);
+        int64_t y = -1;
+        float token_logit = 0.0f;
+        if (tid == 0 && p.splits == 1 && p.logprob) {
+            y = p.ids[r];
+            if (y >= 0 && y < p.vocab) token_logit = row.at(static_cast<int>(y));
         }
-        unsigned long long last = ~0ull;
-        for (int k = 0; k < p.k; ++k) {
-            unsigned long long best = 0;
-            if (st.m == st.m && last > 0) {
-                for (int64_t i = threadIdx.x; i < p.vocab; i += kBlock) {
-                    const uint32_t key = order_key(widen(x[i]));
-                    const unsigned long long q =
-                        (static_cast<unsigned long long>(key) << 32) |
-                        (0xFFFFFFFFu - static_cast<uint32_t>(i));
-                    if (key > kKeyMinusInf && q < last && q > best) best = q;
+        Acc a;
+        stream(
+            row, part,
+            [&](const float* x, int b) {
+                const float top = max_of<kBatch>(x);
+                if constexpr (Top)
+                    top_sh.batch_max[b * kBlock + tid] = static_cast<uint16_t>(order_key16(top));
+                add_batch<kBatch, true>(a, x, top, c2);
+            },
+            [&](const float* x, int) { add_batch<E, true>(a, x, max_of<E>(x), c2); });
+        const Set set = join_threads<true, kBlock / kWave>(
+            a, c2, bs, [&](int j, float m) {
+                float s = 0.0f;
+                vectors_of(row, part, j,
+                           [&](const float* x, int) { s += rest_sum<E>(x, m, c2); });
+                return s;
+            });
+        const RowStats st = finish(set);
+        if (p.splits == 1) {
+            if (tid == 0) write_row(p, r, st, token_logit, y);
+        } else if (tid == 0) {
+            p.part_sets[unit] = make_float4(set.m, set.r, set.t, 0.0f);
+        }
+        if constexpr (Top) {
+            const auto put = [&](int place, unsigned long long key) {
+                if (p.splits == 1) write_top(p, r, place, key, st);
+                else p.part_keys[unit * p.k + place] = key;
+            };
+            if (!(set.r >= 0.0f)) {                      // nothing unmasked, or NaN
+                for (int i = tid; i < p.k; i += kBlock) put(i, 0ull);
+                continue;
+            }
+            const uint32_t own = order_key16(a.m);
+            top_sh.thread_max[tid] = static_cast<uint16_t>(own);
+            if (tid == 0) top_sh.count = 0;
+            __syncthreads();
+            if (tid < kWave) {
+                const uint32_t t = kth_of_keys16(top_sh.thread_max, p.k);
+                if (tid == 0) top_sh.threshold = t > kKey16Finite ? t : kKey16Finite;
+            }
+            __syncthreads();
+            const uint32_t threshold = top_sh.threshold;
+            const auto collect = [&](const float* x, int v) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (order_key16(x[e]) >= threshold) {
+                        const int n = atomicAdd(&top_sh.count, 1);
+                        if (n < kCandidates)
+                            top_sh.cand[n] = candidate(x[e], v * E + e - row.phase);
+                    }
+            };
+            if (own >= threshold) {
+                int b = 0;
+                float x[E];
+                for (int v0 = part.va; v0 < part.vb; v0 += U * kBlock, ++b) {
+                    if (top_sh.batch_max[b * kBlock + tid] < threshold) continue;
+#pragma unroll
+                    for (int q = 0; q < U; ++q) {
+                        const int v = v0 + q * kBlock + tid;
+                        if (v < part.vb) {
+                            unpack<T>(row.load(v), x);
+                            collect(x, v);
+                        }
+                    }
                 }
-                best = block_max(best, sh);
+                if ((part.first && tid == 0) || (part.last && tid == 1)) {
+                    const int v = tid == 0 ? part.lo : part.hi - 1;
+                    row.get_masked(v, x);
+                    collect(x, v);
+                }
             }
-            if (threadIdx.x == 0) {
-                p.top_ids[r * p.k + k] =
-                    best ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best)) : -1;
-                p.top_logprobs[r * p.k + k] =
-                    best ? log_p(from_key(static_cast<uint32_t>(best >> 32)), st.m, st.L, p.c)
-                         : (st.m != st.m ? st.m : -kInf);
+            __syncthreads();
+            if (top_sh.count > kCandidates)
+                collect_exactly(row, part, p.k, threshold << 16, set.m, top_sh);
+            rank_candidates(top_sh, top_sh.count, p.k, put);
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the parts of a row.
+template <typename T, bool Top>
+__global__ __launch_bounds__(kBlock) void logprobs_join_kernel(LogprobParams p) {
+    __shared__ typename std::conditional<Top, TopScratch, int>::type sh;
+    const float c2 = p.c * kLog2e;
+    const int tid = threadIdx.x;
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        const float4* sets = p.part_sets + r * p.splits;
+        const Set set = join_sets(p.splits, c2, [&](int i) {
+            return Set{sets[i].x, sets[i].y, sets[i].z};
+        });
+        const RowStats st = finish(set);
+        if (tid == 0) {
+            int64_t y = -1;
+            float token_logit = 0.0f;
+            if (p.logprob) {
+                y = p.ids[r];
+                if (y >= 0 && y < p.vocab)
+                    token_logit = Row<T>(p.x, r, p.stride, p.vocab).at(static_cast<int>(y));
             }
-            last = best;
+            write_row(p, r, st, token_logit, y);
+        }
+        if constexpr (Top) {
+            const unsigned long long* keys = p.part_keys + r * p.splits * p.k;
+            const int n = p.splits * p.k;
+            const auto put = [&](int place, unsigned long long key) {
+                write_top(p, r, place, st.m == st.m ? key : 0ull, st);
+            };
+            uint32_t own = 0;
+            for (int i = tid; i < n; i += kBlock) {
+                const uint32_t key = static_cast<uint32_t>(keys[i] >> 48);
+                own = key > own ? key : own;
+            }
+            sh.thread_max[tid] = static_cast<uint16_t>(own);
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            if (tid < kWave) {
+                const uint32_t t = kth_of_keys16(sh.thread_max, p.k);
+                if (tid == 0) sh.threshold = t > kKey16Finite ? t : kKey16Finite;
+            }
+            __syncthreads();
+            unsigned long long least = static_cast<unsigned long long>(sh.threshold) << 48;
+            const auto collect = [&]() {
+                for (int i = tid; i < n; i += kBlock)
+                    if (keys[i] >= least) {
+                        const int at = atomicAdd(&sh.count, 1);
+                        if (at < kCandidates) sh.cand[at] = keys[i];
+                    }
+                __syncthreads();
+            };
+            collect();
+            if (sh.count > kCandidates) {
+                // Too many: find the k-th key exactly (keys are distinct), bit by bit.
+                least = 0;
+                for (int bit = 63; bit >= 0; --bit) {
+                    const unsigned long long probe = least | (1ull << bit);
+                    int above = 0;
+                    for (int i = tid; i < n; i += kBlock) above += keys[i] >= probe;
+                    if (block_count(above, sh) >= p.k) least = probe;
+                }
+                __syncthreads();
+                if (tid == 0) sh.count = 0;
+                __syncthreads();
+                collect();
+            }
+            rank_candidates(sh, sh.count, p.k, put);
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Gradients.  Element-wise streams: a work-group writes one part of a row, each vector from one
+// exponential an element.
+
+// The vectors of a gradient's row, which may start at another phase of 16 bytes than the logits'.
+template <typename T>
+struct OutRow {
+    char* base;         // where the logits' vector 0 goes
+    bool aligned;
+
+    __device__ __forceinline__ OutRow(void* data, int64_t r, int64_t stride, const Row<T>& row) {
+        base = static_cast<char*>(data) + (r * stride - row.phase) * static_cast<int64_t>(sizeof(T));
+        aligned = (reinterpret_cast<uintptr_t>(base) & 15u) == 0;
+    }
+    __device__ __forceinline__ void put(int v, const float* x) const {
+        u32x4 out;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = __float_as_uint(x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                out[i] = narrow<T>(x[2 * i]).bits |
+                         (static_cast<uint32_t>(narrow<T>(x[2 * i + 1]).bits) << 16);
+        }
+        char* at = base + static_cast<int64_t>(v) * 16;
+        if (aligned) {
+            __builtin_nontemporal_store(out, reinterpret_cast<u32x4*>(at));
+        } else {
+            // An unaligned 16-byte store: the hardware takes any alignment of the element.
+            typedef u32x4 loose __attribute__((aligned(2)));
+            *reinterpret_cast<loose*>(at) = out;
         }
     }
+    // The elements of vector v that are the row's.
+    __device__ __forceinline__ void put_masked(const Row<T>& row, int v, const float* x) const {
+        T* at = reinterpret_cast<T*>(base + static_cast<int64_t>(v) * 16);
+#pragma unroll
+        for (int e = 0; e < kElems<T>; ++e) {
+            const int i = v * kElems<T> + e - row.phase;
+            if (i >= 0 && i < row.vocab) at[e] = narrow<T>(x[e]);
+        }
+    }
+};
+
+// Streams a part and writes it: f(x, v) turns the floats of vector v into the gradient's.
+template <typename T, typename F>
+__device__ __forceinline__ void stream_through(const Row<T>& row, const OutRow<T>& out,
+                                               const Part& part, F f) {
+    constexpr int E = kElems<T>, U = kLoads<T>;
+    const int tid = threadIdx.x;
+    for (int v0 = part.va; v0 < part.vb; v0 += U * kBlock) {
+        u32x4 raw[U];
+        const bool whole = v0 + U * kBlock <= part.vb;
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int v = v0 + q * kBlock + tid;
+            raw[q] = row.load(whole || v < part.vb ? v : part.va);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int v = v0 + q * kBlock + tid;
+            float x[E];
+            unpack<T>(raw[q], x);
+            f(x, v);
+            if (whole || v < part.vb) out.put(v, x);
+        }
+    }
+    if ((part.first && tid == 0) || (part.last && tid == 1)) {
+        const int v = tid == 0 ? part.lo : part.hi - 1;
+        float x[E];
+        row.get_masked(v, x);
+        f(x, v);
+        out.put_masked(row, v, x);
+    }
+}
+
+// Writes one value to a part.
+template <typename T>
+__device__ __forceinline__ void fill_part(const Row<T>& row, const OutRow<T>& out,
+                                          const Part& part, float value) {
+    float x[kElems<T>];
+#pragma unroll
+    for (int e = 0; e < kElems<T>; ++e) x[e] = value;
+    for (int v = part.va + static_cast<int>(threadIdx.x); v < part.vb; v += kBlock) out.put(v, x);
+    if ((part.first && threadIdx.x == 0) || (part.last && threadIdx.x == 1))
+        out.put_masked(row, threadIdx.x == 0 ? part.lo : part.hi - 1, x);
 }
 
 struct LogprobGradParams {
@@ -210,36 +873,83 @@ struct LogprobGradParams {
     const float *stats, *entropy, *g, *h;
     void* out;
     int64_t ostride;
+    int32_t splits, part_vecs;
 };
 
 template <typename T>
 __global__ __launch_bounds__(kBlock) void logprobs_grad_kernel(LogprobGradParams p) {
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const T* x = static_cast<const T*>(p.x) + r * p.stride;
-        T* out = static_cast<T*>(p.out) + r * p.ostride;
+    constexpr int E = kElems<T>;
+    const float c2 = p.c * kLog2e;
+    const int64_t units = p.rows * p.splits;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t r = unit / p.splits;
+        const Row<T> row(p.x, r, p.stride, p.vocab);
+        const OutRow<T> out(p.out, r, p.ostride, row);
+        const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
         const int64_t y = p.ids ? p.ids[r] : -1;
         const float g = p.g && y >= 0 ? p.g[r] : 0.0f;
         const float h = p.h ? p.h[r] : 0.0f;
         const float m = p.stats[2 * r], L = p.stats[2 * r + 1];
-        const float H = p.h ? p.entropy[r] : 0.0f;
-        const bool zero = (g == 0.0f && h == 0.0f) || (m == -kInf && y < p.vocab);
-        const bool nan = y >= p.vocab || m != m;
-        for (int64_t i = threadIdx.x; i < p.vocab; i += kBlock) {
-            float v = 0.0f;
-            if (!zero) {
-                const float lp = log_p(widen(x[i]), m, L, p.c);
-                const float e = expf(lp);
-                const float slope = e > 0.0f && h != 0.0f ? h * (e * (lp + H)) : 0.0f;
-                v = p.c * ((i == y && g != 0.0f ? -g * expm1f(lp) : -g * e) - slope);
-                if (nan) v = __builtin_nanf("");
-            }
-            out[i] = narrow<T>(v);
+        const float H = h != 0.0f ? p.entropy[r] : 0.0f;
+        if (g == 0.0f && h == 0.0f) {
+            fill_part(row, out, part, 0.0f);
+            continue;
+        }
+        if (y >= p.vocab || m != m) {
+            fill_part(row, out, part, __builtin_nanf(""));
+            continue;
+        }
+        if (m == -kInf) {
+            fill_part(row, out, part, 0.0f);
+            continue;
+        }
+        // The token's entry: g (1 - p) through expm1, precise also where p is near 1.  Each thread
+        // forms it from its own load; in place, the one that stores it has then loaded it already.
+        const float gc = g * p.c, hc = h * p.c, L2 = L * kLog2e;
+        int token_vec = -1, token_elem = 0;
+        float token = 0.0f;
+        if (y >= 0) {
+            token_vec = (static_cast<int>(y) + row.phase) / E;
+            token_elem = (static_cast<int>(y) + row.phase) % E;
+            const float lp = log_p(row.at(static_cast<int>(y)), m, L, p.c);
+            const float e = exp2_fast(lp * kLog2e);
+            token = -gc * expm1f(lp) - (hc != 0.0f && e > 0.0f ? hc * (e * (lp + H)) : 0.0f);
+        }
+        const auto set_token = [&](float* x) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[i] = i == token_elem ? token : x[i];
+        };
+        if (h == 0.0f) {
+            stream_through(row, out, part, [&](float* x, int v) {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    x[i] = -gc * exp2_fast(__builtin_fmaf(c2, x[i] - m, -L2));
+                if (v == token_vec) set_token(x);
+            });
+        } else {
+            // -p (g + h (log p + H)) with log p in units of log 2; the clamp keeps 0 times -inf
+            // out (p is 0 there).
+            const float h2 = hc * kLn2, base = __builtin_fmaf(hc, H, gc);
+            stream_through(row, out, part, [&](float* x, int v) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const float u = __builtin_fmaf(c2, x[i] - m, -L2);
+                    x[i] = -exp2_fast(u) * __builtin_fmaf(h2, fmaxf(u, kNegligible), base);
+                }
+                if (v == token_vec) set_token(x);
+            });
         }
     }
 }
 
 // ------------------------------------------------------------------------------------------------
 // Distillation.
+//
+// The stream takes only the tokens outside the teacher's list (their maximum and sum); the at most
+// 128 listed ones are added in float64 from their own loads.  So the mass outside the list is a
+// sum of its own and no difference, and a row whose likeliest token is listed, the usual case,
+// keeps the precision of a small L with no second look.  A byte for each vector of the part says
+// whether it holds listed tokens, and which slot describes them.
 
 struct DistillParams {
     const void* x;
@@ -253,130 +963,384 @@ struct DistillParams {
     const float* g;
     void* out;
     int64_t ostride;
+    int32_t splits, part_vecs;
+    float2* part_sets;             // [rows][splits]: m, r of the tokens outside the list
 };
 
-// A row's list: ids (below 0: empty), log q and q of the places, all in float64, since the mass
-// left over (1 - sum q) and p - q are small differences.
+constexpr int kTop = FSDPSHARD_MAX_TOP;
+
+// A row's list.  q, log q and their sums are float64: 1 - sum q and p - q are small differences.
 struct Teacher {
-    int32_t id[FSDPSHARD_MAX_TOP];
-    double logq[FSDPSHARD_MAX_TOP], q[FSDPSHARD_MAX_TOP];
-    double mass, rest;
-    int some, bad;
+    int32_t id[kTop];              // -1: empty place (or past it)
+    double q[kTop];
+    double mass, rest;             // sum q, and with a tail 1 - sum q
+    int some, bad, repeats;
 };
 
-__device__ void load_teacher(const DistillParams& p, int64_t r, Teacher& t) {
+// What the listed tokens of a part's vectors do: slot j belongs to the vector of place j's token
+// if no lower place has its token there.
+template <typename T>
+struct Slots {
+    uint32_t mask[kTop];           // elements of the vector that are listed
+    float value[kTop][kElems<T>];  // their gradients
+};
+
+// Loads the list of row r (threads 0..127 take one place each).  In those threads `logq` and `x`
+// are the place's log q and logit, and `leads` tells the first place of its token.
+template <typename T>
+__device__ void load_teacher(const DistillParams& p, int64_t r, const Row<T>& row, Teacher& t,
+                             BlockScratch& sh, double& logq, float& x, bool& leads) {
+    const int j = threadIdx.x;
+    int id = -1;
+    float v = 0.0f;
+    if (j < p.k) {
+        id = p.ids[r * p.tstride + j];
+        v = p.values[r * p.tstride + j];
+    }
+    const bool valid = id >= 0, inside = valid && id < p.vocab;
+    x = inside ? row.at(id) : -kInf;
     __syncthreads();
-    if (threadIdx.x < p.k) {
-        t.id[threadIdx.x] = p.ids[r * p.tstride + threadIdx.x];
-        const double v = p.values[r * p.tstride + threadIdx.x];
-        t.logq[threadIdx.x] = p.tail ? v : v * p.c;
+    if (j == 0) t.some = t.bad = t.repeats = 0;
+    if (j < kTop) t.id[j] = valid ? id : -1;
+    float top = wave_max(valid ? v : -kInf);
+    __syncthreads();
+    if (j < kTop && j % kWave == 0) sh.f[0][j / kWave] = top;
+    if (valid) t.some = 1;
+    if (valid && (!inside || v != v || v == kInf)) t.bad = 1;
+    leads = valid;
+    for (int i = 0; i < p.k; ++i)
+        if (i < j && t.id[i] == id) leads = false;
+    if (valid && !leads) t.repeats = 1;
+    __syncthreads();
+    logq = valid ? static_cast<double>(v) : -HUGE_VAL;
+    double q = 0.0;
+    if (j < kTop) {
+        if (!p.tail) {
+            top = fmaxf(sh.f[0][0], sh.f[0][1]);
+            if (valid) logq = top == -kInf ? -HUGE_VAL
+                                           : static_cast<double>(p.c) *
+                                                 (static_cast<double>(v) - static_cast<double>(top));
+        }
+        q = logq > -HUGE_VAL ? exp(logq) : 0.0;
+        const double s = wave_sum(q);
+        if (j % kWave == 0) sh.d[0][j / kWave] = s;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double top = -HUGE_VAL, sum = 0.0;
-        t.some = t.bad = 0;
-        for (int j = 0; j < p.k; ++j) {
-            if (t.id[j] < 0) continue;
-            t.some = 1;
-            if (t.id[j] >= p.vocab || t.logq[j] != t.logq[j] || t.logq[j] == HUGE_VAL) t.bad = 1;
-            top = fmax(top, t.logq[j]);
+    double sum = sh.d[0][0] + sh.d[0][1];
+    if (!p.tail) {
+        if (sum > 0.0) {
+            q /= sum;
+            logq -= log(sum);
+            sum = 1.0;
         }
-        if (!p.tail && top > -HUGE_VAL) {
-            for (int j = 0; j < p.k; ++j)
-                if (t.id[j] >= 0) sum += exp(t.logq[j] - top);
-            const double ls = log(sum);
-            for (int j = 0; j < p.k; ++j) t.logq[j] = t.logq[j] - top - ls;
-        }
-        sum = 0.0;
-        for (int j = 0; j < p.k; ++j) {
-            t.q[j] = t.id[j] >= 0 ? exp(t.logq[j]) : 0.0;
-            sum += t.q[j];
-        }
+    }
+    if (j < kTop) t.q[j] = q;
+    if (j == 0) {
         t.mass = sum;
         t.rest = p.tail ? fmax(0.0, 1.0 - sum) : 0.0;
     }
     __syncthreads();
 }
 
-__device__ __forceinline__ bool listed(const Teacher& t, int k, int64_t i) {
-    for (int j = 0; j < k; ++j)
-        if (t.id[j] == i) return true;
-    return false;
+// Fills the part's map: map[v - lo] is 0, or 1 + the slot of vector v.
+template <typename T>
+__device__ void map_list(const DistillParams& p, const Row<T>& row, const Part& part,
+                         const Teacher& t, uint8_t* map, Slots<T>& slots) {
+    constexpr int E = kElems<T>;
+    const int j = threadIdx.x, bytes = part.hi - part.lo;
+    for (int i = j * 16; i < bytes; i += kBlock * 16)
+        *reinterpret_cast<u32x4*>(map + i) = u32x4{0, 0, 0, 0};
+    if (j < kTop) slots.mask[j] = 0;
+    __syncthreads();
+    if (j < p.k) {
+        const int id = t.id[j];
+        const int at = id + row.phase, v = at / E;
+        if (id >= 0 && id < p.vocab && v >= part.lo && v < part.hi) {
+            int slot = j;
+            for (int i = p.k - 1; i >= 0; --i)
+                if (i < j && t.id[i] >= 0 && (t.id[i] + row.phase) / E == v) slot = i;
+            if (slot == j) map[v - part.lo] = static_cast<uint8_t>(1 + j);
+            atomicOr(&slots.mask[slot], 1u << (at % E));
+        }
+    }
+    __syncthreads();
 }
 
+// Statistics of the tokens of a part that are outside the list.
 template <typename T>
-__global__ __launch_bounds__(kBlock) void distill_kernel(DistillParams p) {
-    __shared__ Scratch sh;
-    __shared__ Teacher t;
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        load_teacher(p, r, t);
-        const T* x = static_cast<const T*>(p.x) + r * p.stride;
-        RowStats st = {0.0f, 0.0f, 0.0f}, ts = {0.0f, 0.0f, 0.0f};
-        double loss = 0.0;
-        if (t.some) {
-            st = row_stats(x, p.vocab, p.c, [](int64_t) { return true; }, sh);
-            if (p.tail)
-                ts = row_stats(x, p.vocab, p.c,
-                               [&](int64_t i) { return !listed(t, p.k, i); }, sh);
-            if (p.tail && st.m != st.m) ts = st;
-            for (int j = 0; j < p.k; ++j) {
-                if (t.q[j] == 0.0 || t.id[j] >= p.vocab) continue;
-                loss += t.q[j] * (t.logq[j] - log_p(widen(x[t.id[j]]), st.m, st.L, p.c));
-            }
-            if (p.tail && t.rest > 0.0 && ts.m != -kInf)
-                loss += t.rest * (log(t.rest) - (static_cast<double>(p.c) *
-                                                     (static_cast<double>(ts.m) - st.m) +
-                                                 ts.L - st.L));
-            if (t.bad || st.m != st.m) loss = __builtin_nan("");
+__device__ Set outside_set(const Row<T>& row, const Part& part, float c2, const uint8_t* map,
+                           const Slots<T>& slots, BlockScratch& sh) {
+    constexpr int E = kElems<T>, U = kLoads<T>;
+    const int tid = threadIdx.x;
+    const auto drop = [&](float* x, int v) {
+        const int slot = map[v - part.lo];
+        if (slot != 0) {
+            const uint32_t mask = slots.mask[slot - 1];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if ((mask >> e) & 1u) x[e] = -kInf;
         }
-        if (threadIdx.x == 0) {
-            if (p.loss) p.loss[r] = static_cast<float>(loss);
-            if (p.stats) {
-                p.stats[4 * r] = st.m;
-                p.stats[4 * r + 1] = st.L;
-                p.stats[4 * r + 2] = ts.m;
-                p.stats[4 * r + 3] = ts.L;
+    };
+    Acc a;
+    stream(
+        row, part,
+        [&](float* x, int b) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const int v = part.va + (b * U + q) * kBlock + tid;
+                if (v < part.vb) drop(x + q * E, v);
             }
+            add_batch<kBatch, false>(a, x, max_of<kBatch>(x), c2);
+        },
+        [&](float* x, int v) {
+            drop(x, v);
+            add_batch<E, false>(a, x, max_of<E>(x), c2);
+        });
+    return join_threads<false, kBlock / kWave>(a, c2, sh, [&](int j, float m) {
+        float s = 0.0f;
+        vectors_of(row, part, j, [&](float* x, int v) {
+            drop(x, v);
+            s += rest_sum<E>(x, m, c2);
+        });
+        return s;
+    });
+}
+
+// A row's statistics from the set outside the list and the listed tokens' logits.
+struct DistillRow {
+    double m, L;            // of the whole row (m = -inf: all masked)
+    double mt, Lt;          // outside the list (-inf: nothing unmasked there)
+    bool nan;
+};
+
+__device__ DistillRow join_list(const Set& outside, float x, bool leads, float c,
+                                BlockScratch& sh) {
+    const int j = threadIdx.x;
+    const float own = leads ? x : -kInf;
+    const float wm = wave_max(own);
+    const unsigned long long odd = __ballot(leads && !(x < kInf));
+    __syncthreads();
+    if (j < kTop && j % kWave == 0) {
+        sh.f[0][j / kWave] = wm;
+        sh.f[1][j / kWave] = odd ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    const bool none = outside.r < 0.0f;
+    const float mt = none ? -kInf : outside.m;
+    const float m = fmaxf(fmaxf(sh.f[0][0], sh.f[0][1]), mt);
+    const bool nan = outside.r != outside.r || sh.f[1][0] + sh.f[1][1] != 0.0f;
+    double s = 0.0;
+    int ones = 0;
+    if (j < kTop) {
+        if (own == m) ones = 1;
+        else if (own > -kInf) s = exp(static_cast<double>(c) * (static_cast<double>(own) - m));
+        s = wave_sum(s);
+        if (j % kWave == 0) sh.d[0][j / kWave] = s;
+    }
+    const int n = __popcll(__ballot(ones));
+    if (j < kTop && j % kWave == 0) sh.d[1][j / kWave] = n;
+    __syncthreads();
+    DistillRow d;
+    d.nan = nan;
+    d.m = m;
+    d.mt = mt;
+    if (m == -kInf) {
+        d.L = d.Lt = -HUGE_VAL;
+        return d;
+    }
+    double rest = sh.d[0][0] + sh.d[0][1], count = sh.d[1][0] + sh.d[1][1];
+    d.Lt = none ? -HUGE_VAL : log1p(static_cast<double>(outside.r));
+    if (!none) {
+        if (mt == m) {
+            count += 1.0;
+            rest += outside.r;
+        } else {
+            rest += (1.0 + outside.r) * exp(static_cast<double>(c) * (static_cast<double>(mt) - m));
+        }
+    }
+    d.L = log1p(rest + (count - 1.0));
+    return d;
+}
+
+__device__ __forceinline__ double list_logp(float x, const DistillRow& d, float c) {
+    return x == -kInf ? -HUGE_VAL : static_cast<double>(c) * (x - d.m) - d.L;
+}
+
+// Loss and statistics of a row (all threads).
+__device__ void write_loss(const DistillParams& p, int64_t r, const Teacher& t,
+                           const DistillRow& d, double logq, float x, BlockScratch& sh) {
+    const int j = threadIdx.x;
+    __syncthreads();
+    if (j < kTop) {
+        const double q = t.q[j];
+        const double s = wave_sum(q > 0.0 ? q * (logq - list_logp(x, d, p.c)) : 0.0);
+        if (j % kWave == 0) sh.d[0][j / kWave] = s;
+    }
+    __syncthreads();
+    if (j == 0) {
+        double loss = sh.d[0][0] + sh.d[0][1];
+        if (t.rest > 0.0 && d.mt != -HUGE_VAL)
+            loss += t.rest * (log(t.rest) -
+                              (static_cast<double>(p.c) * (d.mt - d.m) + d.Lt - d.L));
+        const float nan = __builtin_nanf("");
+        if (p.loss) p.loss[r] = t.bad || d.nan ? nan : static_cast<float>(loss);
+        if (p.stats) {
+            p.stats[4 * r] = d.nan ? nan : static_cast<float>(d.m);
+            p.stats[4 * r + 1] = d.nan ? nan : static_cast<float>(d.L);
+            p.stats[4 * r + 2] = !p.tail ? 0.0f : d.nan ? nan : static_cast<float>(d.mt);
+            p.stats[4 * r + 3] = !p.tail ? 0.0f : d.nan ? nan : static_cast<float>(d.Lt);
         }
     }
 }
 
+__device__ __forceinline__ void write_no_list(const DistillParams& p, int64_t r) {
+    if (threadIdx.x == 0) {
+        p.loss[r] = 0.0f;
+        if (p.stats)
+            for (int i = 0; i < 4; ++i) p.stats[4 * r + i] = 0.0f;
+    }
+}
+
 template <typename T>
-__global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
+__global__ __launch_bounds__(kBlock) void distill_kernel(DistillParams p) {
+    extern __shared__ __align__(16) uint8_t map[];
+    __shared__ BlockScratch sh;
+    __shared__ Teacher t;
+    __shared__ Slots<T> slots;
+    const float c2 = p.c * kLog2e;
+    const int64_t units = p.rows * p.splits;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t r = unit / p.splits;
+        const Row<T> row(p.x, r, p.stride, p.vocab);
+        const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
+        double logq;
+        float x;
+        bool leads;
+        load_teacher(p, r, row, t, sh, logq, x, leads);
+        if (!t.some) {
+            if (p.splits == 1) write_no_list(p, r);
+            continue;
+        }
+        map_list(p, row, part, t, map, slots);
+        const Set set = outside_set(row, part, c2, map, slots, sh);
+        if (p.splits == 1) {
+            const DistillRow d = join_list(set, x, leads, p.c, sh);
+            write_loss(p, r, t, d, logq, x, sh);
+        } else if (threadIdx.x == 0) {
+            p.part_sets[unit] = make_float2(set.m, set.r);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
+    __shared__ BlockScratch sh;
     __shared__ Teacher t;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        load_teacher(p, r, t);
-        const T* x = static_cast<const T*>(p.x) + r * p.stride;
-        T* out = static_cast<T*>(p.out) + r * p.ostride;
-        const float m = p.stats[4 * r], L = p.stats[4 * r + 1];
-        const float mt = p.stats[4 * r + 2], Lt = p.stats[4 * r + 3];
-        const float g = p.g[r];
-        const bool zero = !t.some || g == 0.0f || (m == -kInf && !t.bad);
-        const bool nan = t.bad || m != m;
-        const double rest = mt == -kInf ? 0.0 : t.rest;
-        for (int64_t i = threadIdx.x; i < p.vocab; i += kBlock) {
-            float v = 0.0f;
-            if (!zero) {
-                const float xi = widen(x[i]);
-                double q = 0.0;
-                bool in = false;
-                for (int j = 0; j < p.k; ++j)
-                    if (t.id[j] == i) {
-                        q += t.q[j];
-                        in = true;
-                    }
-                double dx = (t.mass + rest) * exp(static_cast<double>(log_p(xi, m, L, p.c))) - q;
-                if (!in && rest > 0.0) dx -= rest * expf(log_p(xi, mt, Lt, p.c));
-                v = g * p.c * static_cast<float>(dx);
-                if (nan) v = __builtin_nanf("");
-            }
-            out[i] = narrow<T>(v);
+        const Row<T> row(p.x, r, p.stride, p.vocab);
+        double logq;
+        float x;
+        bool leads;
+        load_teacher(p, r, row, t, sh, logq, x, leads);
+        if (!t.some) {
+            write_no_list(p, r);
+            continue;
         }
+        const float2* sets = p.part_sets + r * p.splits;
+        const Set set = join_sets(p.splits, p.c * kLog2e,
+                                  [&](int i) { return Set{sets[i].x, sets[i].y, 0.0f}; });
+        const DistillRow d = join_list(set, x, leads, p.c, sh);
+        write_loss(p, r, t, d, logq, x, sh);
+        __syncthreads();
+    }
+}
+
+// The factors of a row's gradient: listed tokens get value[][], the others coef 2^(c2 (x - ref)).
+template <typename T>
+__device__ void grad_values(const DistillParams& p, const Row<T>& row, const Part& part,
+                            const Teacher& t, const DistillRow& d, float g, float x, bool leads,
+                            const uint8_t* map, Slots<T>& slots, float& ref, float& coef) {
+    constexpr int E = kElems<T>;
+    const int j = threadIdx.x;
+    const double gc = static_cast<double>(g) * p.c;
+    const double rest = d.mt == -HUGE_VAL ? 0.0 : t.rest, mass = t.mass + rest;
+    if (j < kTop && leads) {
+        double q = t.q[j];
+        if (t.repeats)
+            for (int i = j + 1; i < p.k; ++i)
+                if (t.id[i] == t.id[j]) q += t.q[i];
+        const int at = t.id[j] + row.phase, v = at / E;
+        if (v >= part.lo && v < part.hi)
+            slots.value[map[v - part.lo] - 1][at % E] =
+                static_cast<float>(gc * (mass * exp(list_logp(x, d, p.c)) - q));
+    }
+    if (p.tail && d.mt != -HUGE_VAL) {
+        ref = static_cast<float>(d.mt);
+        coef = static_cast<float>(gc * (mass * exp(static_cast<double>(p.c) * (d.mt - d.m) - d.L) -
+                                        rest * exp(-d.Lt)));
+    } else {
+        ref = static_cast<float>(d.m);
+        coef = static_cast<float>(gc * mass * exp(-d.L));
+    }
+    __syncthreads();
+}
+
+template <typename T>
+__global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
+    constexpr int E = kElems<T>;
+    extern __shared__ __align__(16) uint8_t map[];
+    __shared__ BlockScratch sh;
+    __shared__ Teacher t;
+    __shared__ Slots<T> slots;
+    const float c2 = p.c * kLog2e;
+    const int64_t units = p.rows * p.splits;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t r = unit / p.splits;
+        const Row<T> row(p.x, r, p.stride, p.vocab);
+        const OutRow<T> out(p.out, r, p.ostride, row);
+        const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
+        const float g = p.g[r];
+        if (g == 0.0f) {
+            fill_part(row, out, part, 0.0f);
+            continue;
+        }
+        double logq;
+        float x;
+        bool leads;
+        load_teacher(p, r, row, t, sh, logq, x, leads);
+        DistillRow d;
+        d.m = p.stats[4 * r];
+        d.L = p.stats[4 * r + 1];
+        d.mt = p.tail ? p.stats[4 * r + 2] : 0.0;
+        d.Lt = p.tail ? p.stats[4 * r + 3] : 0.0;
+        if (!t.some || t.bad || d.m != d.m || d.m == -HUGE_VAL) {
+            const bool nan = t.some && (t.bad || d.m != d.m);
+            fill_part(row, out, part, nan ? __builtin_nanf("") : 0.0f);
+            continue;
+        }
+        map_list(p, row, part, t, map, slots);
+        float ref, coef;
+        grad_values(p, row, part, t, d, g, x, leads, map, slots, ref, coef);
+        stream_through(row, out, part, [&](float* y, int v) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - ref));
+            const int slot = v < part.hi ? map[v - part.lo] : 0;
+            if (slot != 0) {
+                const uint32_t mask = slots.mask[slot - 1];
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if ((mask >> e) & 1u) y[e] = slots.value[slot - 1][e];
+            }
+        });
+        __syncthreads();
     }
 }
 
 // ------------------------------------------------------------------------------------------------
 // Host side.
+
+constexpr int64_t kMaxRows = int64_t{1} << 44;   // keeps every size below within int64
 
 int element_bytes(int32_t dtype) { return dtype == FSDPSHARD_FP32 ? 4 : 2; }
 
@@ -419,8 +1383,7 @@ int check_logits(const fsdpshard_logits* x, int64_t* bytes) {
     if (x->vocab > FSDPSHARD_MAX_VOCAB) return FSDPSHARD_ERR_UNSUPPORTED;
     if (!aligned_to(x->data, element_bytes(x->dtype))) return FSDPSHARD_ERR_ALIGNMENT;
     *bytes = extent(x->rows, x->vocab, x->row_stride, element_bytes(x->dtype));
-    return *bytes < 0 || x->rows > INT64_MAX / (4 * 8 * FSDPSHARD_MAX_TOP) ? FSDPSHARD_ERR_OVERFLOW
-                                                                            : FSDPSHARD_OK;
+    return *bytes < 0 || x->rows > kMaxRows ? FSDPSHARD_ERR_OVERFLOW : FSDPSHARD_OK;
 }
 
 int check_teacher(const fsdpshard_logits* x, const fsdpshard_teacher* t, int64_t* bytes) {
@@ -446,17 +1409,52 @@ int check_dlogits(const fsdpshard_logits* x, const void* out, int64_t ostride, i
     return FSDPSHARD_OK;
 }
 
-constexpr int64_t kMaxGroups = 1 << 20;   // work-groups of a launch; each loops over its rows
+constexpr int64_t kMaxGroups = 1 << 20;   // work-groups of a launch; each loops over its units
 
-int launch_rows(const void* kernel, int64_t rows, void* params, void* stream) {
-    return fsdpshard_detail::launch(
-        kernel, static_cast<unsigned>(rows < kMaxGroups ? rows : kMaxGroups), params, stream);
+int launch_units(const void* kernel, int64_t units, void* params, int64_t lds, void* stream) {
+    void* args[] = {params};
+    const hipError_t e = hipLaunchKernel(
+        kernel, dim3(static_cast<unsigned>(units < kMaxGroups ? units : kMaxGroups)), dim3(kBlock),
+        args, static_cast<size_t>(lds), static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? FSDPSHARD_OK : FSDPSHARD_ERR_HIP;
 }
 
-#define BY_DTYPE(dtype, kernel)                                             \
-    ((dtype) == FSDPSHARD_BF16   ? reinterpret_cast<const void*>(&kernel<Bf16>) \
-     : (dtype) == FSDPSHARD_FP16 ? reinterpret_cast<const void*>(&kernel<Fp16>) \
-                                 : reinterpret_cast<const void*>(&kernel<float>))
+template <typename Get>
+const void* by_dtype(int32_t dtype, Get get) {
+    if (dtype == FSDPSHARD_BF16) return get(Bf16{});
+    if (dtype == FSDPSHARD_FP16) return get(Fp16{});
+    return get(float{});
+}
+#define KERNEL(...) reinterpret_cast<const void*>(&__VA_ARGS__)
+
+// How rows are cut into parts.  Vectors a row may have, whatever its phase: ceil((vocab + E - 1) /
+// E).  A part has at most kMaxPartVecs (what a work-group keeps for its part in LDS is sized for
+// that), and where rows are few they are cut further, for about kWantUnits work-groups, but not
+// below kMinPartVecs vectors.
+constexpr int64_t kWantUnits = 1024;
+constexpr int64_t kMinPartVecs = 512;
+
+struct Cut {
+    int32_t splits, part_vecs;
+};
+
+Cut cut_rows(int64_t rows, int64_t vocab, int elem) {
+    const int64_t per = 16 / elem, vecs = (vocab + 2 * per - 2) / per;
+    int64_t splits = (vecs + kMaxPartVecs - 1) / kMaxPartVecs;
+    const int64_t want = rows > 0 ? kWantUnits / rows : 1;
+    const int64_t most = vecs / kMinPartVecs;
+    if (want > splits && most > splits) splits = want < most ? want : most;
+    const int64_t part = (vecs + splits - 1) / splits;
+    return {static_cast<int32_t>((vecs + part - 1) / part), static_cast<int32_t>(part)};
+}
+
+// The most parts of any type's rows (their workspace does not depend on the type).
+int64_t most_splits(int64_t rows, int64_t vocab) {
+    const int64_t a = cut_rows(rows, vocab, 2).splits, b = cut_rows(rows, vocab, 4).splits;
+    return a > b ? a : b;
+}
+
+int64_t map_bytes(const Cut& cut) { return (cut.part_vecs + 15) / 16 * 16; }
 
 bool workspace_ok(const void* ws, int64_t have, int64_t need, int* rc) {
     if (have < 0 || (ws == nullptr && have > 0)) *rc = FSDPSHARD_ERR_INVALID_ARG;
@@ -478,16 +1476,42 @@ DistillParams distill_params(const fsdpshard_logits* x, const fsdpshard_teacher*
     p.tstride = t->row_stride;
     p.k = t->k;
     p.tail = t->tail;
+    const Cut cut = cut_rows(x->rows, x->vocab, element_bytes(x->dtype));
+    p.splits = cut.splits;
+    p.part_vecs = cut.part_vecs;
     return p;
+}
+
+int launch_distill(DistillParams& p, int32_t dtype, void* workspace, void* stream) {
+    p.part_sets = static_cast<float2*>(workspace);
+    const void* kernel = by_dtype(
+        dtype, [](auto t) { return KERNEL(distill_kernel<decltype(t)>); });
+    const int rc = launch_units(kernel, p.rows * p.splits, &p,
+                                map_bytes({p.splits, p.part_vecs}), stream);
+    if (rc != FSDPSHARD_OK || p.splits == 1) return rc;
+    kernel = by_dtype(dtype, [](auto t) { return KERNEL(distill_join_kernel<decltype(t)>); });
+    return launch_units(kernel, p.rows, &p, 0, stream);
+}
+
+int launch_distill_grad(DistillParams& p, int32_t dtype, const float* dloss, void* dlogits,
+                        int64_t dlogits_stride, void* stream) {
+    p.g = dloss;
+    p.out = dlogits;
+    p.ostride = dlogits_stride;
+    const void* kernel = by_dtype(
+        dtype, [](auto t) { return KERNEL(distill_grad_kernel<decltype(t)>); });
+    return launch_units(kernel, p.rows * p.splits, &p, map_bytes({p.splits, p.part_vecs}),
+                        stream);
 }
 
 }  // namespace
 
 extern "C" int64_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t top_k) {
     if (rows < 0 || vocab < 1 || vocab > FSDPSHARD_MAX_VOCAB || top_k < 0 ||
-        top_k > FSDPSHARD_MAX_TOP)
+        top_k > FSDPSHARD_MAX_TOP || rows > kMaxRows)
         return -1;
-    return 0;
+    const int64_t splits = most_splits(rows, vocab);
+    return splits > 1 ? rows * splits * (16 + 8 * static_cast<int64_t>(top_k)) : 0;
 }
 
 extern "C" int token_logprobs(const fsdpshard_logits* logits, const int64_t* ids, float* logprob,
@@ -516,9 +1540,36 @@ extern "C" int token_logprobs(const fsdpshard_logits* logits, const int64_t* ids
     const Span in[] = {{logits->data, xbytes}, {ids, 8 * rows}};
     if (!disjoint(out, 6, in, 2)) return FSDPSHARD_ERR_INVALID_ARG;
     if (rows == 0) return FSDPSHARD_OK;
-    LogprobParams p{logits->data, rows,  logits->vocab, logits->row_stride, logits->scale, ids,
-                    logprob,      entropy, stats,       top_ids,            top_logprobs,  top_k};
-    return launch_rows(BY_DTYPE(logits->dtype, logprobs_kernel), rows, &p, stream);
+    const Cut cut = cut_rows(rows, logits->vocab, element_bytes(logits->dtype));
+    LogprobParams p{};
+    p.x = logits->data;
+    p.rows = rows;
+    p.vocab = logits->vocab;
+    p.stride = logits->row_stride;
+    p.c = logits->scale;
+    p.ids = ids;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.stats = stats;
+    p.top_ids = top_ids;
+    p.top_logprobs = top_logprobs;
+    p.k = top_k;
+    p.splits = cut.splits;
+    p.part_vecs = cut.part_vecs;
+    p.part_sets = static_cast<float4*>(workspace);
+    p.part_keys = reinterpret_cast<unsigned long long*>(p.part_sets + rows * cut.splits);
+    const void* kernel = by_dtype(logits->dtype, [&](auto t) {
+        using T = decltype(t);
+        return top_k > 0 ? KERNEL(logprobs_kernel<T, true>) : KERNEL(logprobs_kernel<T, false>);
+    });
+    rc = launch_units(kernel, rows * cut.splits, &p, 0, stream);
+    if (rc != FSDPSHARD_OK || cut.splits == 1) return rc;
+    kernel = by_dtype(logits->dtype, [&](auto t) {
+        using T = decltype(t);
+        return top_k > 0 ? KERNEL(logprobs_join_kernel<T, true>)
+                         : KERNEL(logprobs_join_kernel<T, false>);
+    });
+    return launch_units(kernel, rows, &p, 0, stream);
 }
 
 extern "C" int token_logprobs_grad(const fsdpshard_logits* logits, const int64_t* ids,
@@ -545,15 +1596,21 @@ extern "C" int token_logprobs_grad(const fsdpshard_logits* logits, const int64_t
                        {dentropy, 4 * rows}};
     if (!disjoint(out, 1, in, 6)) return FSDPSHARD_ERR_INVALID_ARG;
     if (rows == 0) return FSDPSHARD_OK;
+    const Cut cut = cut_rows(rows, logits->vocab, element_bytes(logits->dtype));
     LogprobGradParams p{logits->data, rows,     logits->vocab, logits->row_stride,
                         logits->scale, ids,     stats,         entropy,
-                        dlogprob,     dentropy, dlogits,       dlogits_stride};
-    return launch_rows(BY_DTYPE(logits->dtype, logprobs_grad_kernel), rows, &p, stream);
+                        dlogprob,     dentropy, dlogits,       dlogits_stride,
+                        cut.splits,   cut.part_vecs};
+    const void* kernel = by_dtype(logits->dtype, [](auto t) {
+        return KERNEL(logprobs_grad_kernel<decltype(t)>);
+    });
+    return launch_units(kernel, rows * cut.splits, &p, 0, stream);
 }
 
 extern "C" int64_t distill_topk_workspace_bytes(int64_t rows, int64_t vocab) {
-    if (rows < 0 || vocab < 1 || vocab > FSDPSHARD_MAX_VOCAB) return -1;
-    return 0;
+    if (rows < 0 || vocab < 1 || vocab > FSDPSHARD_MAX_VOCAB || rows > kMaxRows) return -1;
+    const int64_t splits = most_splits(rows, vocab);
+    return splits > 1 ? (rows * splits * 8 + 15) / 16 * 16 : 0;
 }
 
 extern "C" int distill_topk(const fsdpshard_logits* logits, const fsdpshard_teacher* teacher,
@@ -577,7 +1634,7 @@ extern "C" int distill_topk(const fsdpshard_logits* logits, const fsdpshard_teac
     DistillParams p = distill_params(logits, teacher);
     p.loss = loss;
     p.stats = stats;
-    return launch_rows(BY_DTYPE(logits->dtype, distill_kernel), rows, &p, stream);
+    return launch_distill(p, logits->dtype, workspace, stream);
 }
 
 extern "C" int distill_topk_grad(const fsdpshard_logits* logits, const fsdpshard_teacher* teacher,
@@ -600,11 +1657,8 @@ extern "C" int distill_topk_grad(const fsdpshard_logits* logits, const fsdpshard
     if (!disjoint(out, 1, in, 5)) return FSDPSHARD_ERR_INVALID_ARG;
     if (rows == 0) return FSDPSHARD_OK;
     DistillParams p = distill_params(logits, teacher);
-    p.stats = const_cast<float*>(stats);
-    p.g = dloss;
-    p.out = dlogits;
-    p.ostride = dlogits_stride;
-    return launch_rows(BY_DTYPE(logits->dtype, distill_grad_kernel), rows, &p, stream);
+    p.stats = const_cast<float*>(stats);       // read only by this kernel
+    return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
 }
 
 extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
@@ -637,10 +1691,7 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
     DistillParams p = distill_params(logits, teacher);
     p.loss = loss;
     p.stats = stats;
-    rc = launch_rows(BY_DTYPE(logits->dtype, distill_kernel), rows, &p, stream);
+    rc = launch_distill(p, logits->dtype, workspace, stream);
     if (rc != FSDPSHARD_OK) return rc;
-    p.g = dloss;
-    p.out = dlogits;
-    p.ostride = dlogits_stride;
-    return launch_rows(BY_DTYPE(logits->dtype, distill_grad_kernel), rows, &p, stream);
+    return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
 }

@@ -35,7 +35,7 @@ extern "C" {
 #endif
 
 #define FSDPSHARD_MAX_TOP 128                  /* alternatives, and places of a teacher's list */
-#define FSDPSHARD_MAX_VOCAB ((int64_t)1 << 30)
+#define FSDPSHARD_MAX_VOCAB ((int64_t)1 << 21)
 
 typedef enum fsdpshard_dtype {
     FSDPSHARD_BF16 = 0,
@@ -45,7 +45,7 @@ typedef enum fsdpshard_dtype {
 
 typedef struct fsdpshard_logits {
     const void* data;      /* device, aligned to its element                                  */
-    int64_t rows;          /* >= 0; 0 is a successful no-op                                   */
+    int64_t rows;          /* >= 0 (0 is a successful no-op), up to 2^44                      */
     int64_t vocab;         /* 1 .. FSDPSHARD_MAX_VOCAB                                        */
     int64_t row_stride;    /* elements from a row to the next, >= vocab (any when rows <= 1)  */
     int32_t dtype;         /* fsdpshard_dtype                                                 */
