@@ -126,6 +126,13 @@ struct Row {
     }
 };
 
+// The row of a unit of work; a 64-bit division is a long routine, and most launches need none.
+__device__ __forceinline__ int64_t row_of(int64_t unit, int splits) {
+    if (splits == 1) return unit;
+    if ((unit >> 32) == 0) return static_cast<uint32_t>(unit) / static_cast<uint32_t>(splits);
+    return unit / splits;
+}
+
 // A work-group's part of a row: vectors [lo, hi), of which [va, vb) are whole.  A partial first
 // vector belongs to thread 0, a partial last one to thread 1; the whole ones are dealt in turn.
 struct Part {
@@ -355,18 +362,18 @@ __device__ __forceinline__ float log_p(float x, float m, float L, float c) {
 
 // Streams a part: calls batch(x, b) with kBatch floats of this thread's b-th batch of whole
 // vectors (-inf past the end), and edge(x, v) with the kElems floats of a partial vector v.
-template <typename T, typename Batch, typename Edge>
+template <int Threads, typename T, typename Batch, typename Edge>
 __device__ __forceinline__ void stream(const Row<T>& row, const Part& part, Batch batch,
                                        Edge edge) {
     constexpr int E = kElems<T>, U = kLoads<T>;
     const int tid = threadIdx.x;
     int b = 0;
-    for (int v0 = part.va; v0 < part.vb; v0 += U * kBlock, ++b) {
+    for (int v0 = part.va; v0 < part.vb; v0 += U * Threads, ++b) {
         u32x4 raw[U];
-        const bool whole = v0 + U * kBlock <= part.vb;
+        const bool whole = v0 + U * Threads <= part.vb;
 #pragma unroll
         for (int q = 0; q < U; ++q) {
-            const int v = v0 + q * kBlock + tid;
+            const int v = v0 + q * Threads + tid;
             raw[q] = row.load(whole || v < part.vb ? v : part.va);
         }
         float x[kBatch];
@@ -375,7 +382,7 @@ __device__ __forceinline__ void stream(const Row<T>& row, const Part& part, Batc
         if (!whole) {
 #pragma unroll
             for (int q = 0; q < U; ++q)
-                if (v0 + q * kBlock + tid >= part.vb) {
+                if (v0 + q * Threads + tid >= part.vb) {
 #pragma unroll
                     for (int e = 0; e < E; ++e) x[q * E + e] = -kInf;
                 }
@@ -391,11 +398,11 @@ __device__ __forceinline__ void stream(const Row<T>& row, const Part& part, Batc
 }
 
 // Calls f(x, v) for the vectors of thread j of a part, dealt over the threads of the work-group.
-template <typename T, typename F>
+template <int Threads, typename T, typename F>
 __device__ __forceinline__ void vectors_of(const Row<T>& row, const Part& part, int j, F f) {
     float x[kElems<T>];
-    for (int64_t v = part.va + j + static_cast<int64_t>(threadIdx.x) * kBlock; v < part.vb;
-         v += static_cast<int64_t>(kBlock) * kBlock) {
+    for (int64_t v = part.va + j + static_cast<int64_t>(threadIdx.x) * Threads; v < part.vb;
+         v += static_cast<int64_t>(Threads) * Threads) {
         unpack<T>(row.load(static_cast<int>(v)), x);
         f(x, static_cast<int>(v));
     }
@@ -434,67 +441,115 @@ __device__ __forceinline__ unsigned long long candidate(float x, int i) {
            (0xFFFFFFFFu - static_cast<uint32_t>(i));
 }
 
-constexpr int kMaxPartVecs = 16384;                        // vectors of a part
-constexpr int kMaxBatches = kMaxPartVecs / (kBlock * 4) + 1;
+constexpr int kMaxPartVecs = 17408;    // vectors of a part: 131,072 16-bit elements at any phase
 constexpr int kCandidates = 1024;
+constexpr int kListed = 1024;
+constexpr int kMaxima = 256;           // maxima of thread groups that the threshold is taken from
 
+template <int Threads>
 struct TopScratch {
-    uint16_t batch_max[kMaxBatches * kBlock];              // 16-bit keys of the batches' maxima
-    uint16_t thread_max[kBlock];
+    // 16-bit keys of the batches' maxima
+    uint16_t batch_max[(kMaxPartVecs + 4 * Threads - 1) / (4 * Threads) * Threads];
+    uint16_t maxima[kMaxima];
+    uint16_t list[kListed];            // batches that reach the threshold: batch * Threads + thread
+    int listed;
+    int place[kBlock];
     alignas(16) unsigned long long cand[kCandidates];
     uint32_t threshold;
     int count;
     int wave_count[kMaxWaves];
 };
 
-// The largest 16-bit value that at least k of the work-group's 256 keys reach (by one wave).
-__device__ uint32_t kth_of_keys16(const uint16_t* keys, int k) {
+// A 16-bit value that at least k of the 256 keys reach, and not many more: the largest one, or the
+// first that the bisection meets with at most k + k / 16 + 2 (by one wave; 16 steps at most).
+__device__ uint32_t near_kth(const uint16_t* keys, int k) {
     const int lane = threadIdx.x % kWave;
-    uint32_t own[kBlock / kWave];
+    uint32_t own[kMaxima / kWave];
 #pragma unroll
-    for (int i = 0; i < kBlock / kWave; ++i) own[i] = keys[lane + i * kWave];
+    for (int i = 0; i < kMaxima / kWave; ++i) own[i] = keys[lane + i * kWave];
     uint32_t best = 0;
     for (int bit = 15; bit >= 0; --bit) {
         const uint32_t probe = best | (1u << bit);
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < kBlock / kWave; ++i) n += __popcll(__ballot(own[i] >= probe));
-        if (n >= k) best = probe;
+        for (int i = 0; i < kMaxima / kWave; ++i) n += __popcll(__ballot(own[i] >= probe));
+        if (n >= k) {
+            best = probe;
+            if (n <= k + k / 16 + 2) break;
+        }
     }
     return best;
 }
 
-// Writes the `want` largest of the candidates found, in falling order, through put(place, key);
-// places beyond the candidates get key 0.
-template <typename Put>
-__device__ void rank_candidates(const TopScratch& sh, int found, int want, Put put) {
-    for (int i = threadIdx.x; i < found; i += kBlock) {
-        const unsigned long long own = sh.cand[i];
-        int place = 0;
-        for (int j = 0; j < found; ++j) place += sh.cand[j] > own;
-        if (place < want) put(place, own);
+// Sets the threshold from every thread's largest key (0: none).
+template <int Threads>
+__device__ void set_threshold(uint32_t own, int k, TopScratch<Threads>& sh) {
+    if constexpr (Threads > kMaxima) {       // the maximum of each four lanes
+        static_assert(Threads == 4 * kMaxima);
+        uint32_t y = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(own), 0xB1, 0xF, 0xF, true));
+        own = own > y ? own : y;
+        y = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(own), 0x4E, 0xF, 0xF, true));
+        own = own > y ? own : y;
+        if (threadIdx.x % 4 == 0) sh.maxima[threadIdx.x / 4] = static_cast<uint16_t>(own);
+    } else {
+        sh.maxima[threadIdx.x] = static_cast<uint16_t>(own);
     }
-    for (int i = found + static_cast<int>(threadIdx.x); i < want; i += kBlock) put(i, 0ull);
+    if (threadIdx.x == 0) sh.count = sh.listed = 0;
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        const uint32_t t = near_kth(sh.maxima, k);
+        if (threadIdx.x == 0) sh.threshold = t > kKey16Finite ? t : kKey16Finite;
+    }
+    __syncthreads();
+}
+
+// Writes the `want` largest of the candidates found, in falling order, through put(place, key);
+// places beyond the candidates get key 0.  A candidate's place is the number of larger ones; up to
+// kBlock candidates, the threads share the comparisons of each.
+template <int Threads, typename Put>
+__device__ void rank_candidates(TopScratch<Threads>& sh, int found, int want, Put put) {
+    const int tid = threadIdx.x;
+    for (int i = found + tid; i < want; i += Threads) put(i, 0ull);
+    if (found > kBlock) {
+        for (int i = tid; i < found; i += Threads) {
+            const unsigned long long own = sh.cand[i];
+            int place = 0;
+            for (int j = 0; j < found; ++j) place += sh.cand[j] > own;
+            if (place < want) put(place, own);
+        }
+        return;
+    }
+    const int lanes = found <= 64 ? 64 : found <= 128 ? 128 : 256;   // threads side by side
+    const int shares = Threads / lanes, share = tid / lanes, i = tid % lanes;
+    if (tid < kBlock) sh.place[tid] = 0;
+    __syncthreads();
+    const unsigned long long own = i < found ? sh.cand[i] : ~0ull;
+    int place = 0;
+    for (int j = share; j < found; j += shares) place += sh.cand[j] > own;
+    if (i < found && place) atomicAdd(&sh.place[i], place);
+    __syncthreads();
+    if (tid < found && sh.place[tid] < want) put(sh.place[tid], own);
 }
 
 // Number of elements over the work-group (all threads return it).
-__device__ int block_count(int n, TopScratch& sh) {
+template <int Threads>
+__device__ int block_count(int n, TopScratch<Threads>& sh) {
 #pragma unroll
     for (int w = 1; w < kWave; w <<= 1) n += __shfl_xor(n, w);
     __syncthreads();
     if (threadIdx.x % kWave == 0) sh.wave_count[threadIdx.x / kWave] = n;
     __syncthreads();
     int total = 0;
-    for (int i = 0; i < kBlock / kWave; ++i) total += sh.wave_count[i];
+    for (int i = 0; i < Threads / kWave; ++i) total += sh.wave_count[i];
     return total;
 }
 
 // More candidates than fit (many equal values, or the best ones in few threads): find the k-th
 // largest value's key by bisection with counting passes over the part, then take what is above it
 // and, of the equal ones, the lowest indices.  Slow and exact.
-template <typename T>
+template <typename T, int Threads>
 __device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint32_t lo_key,
-                                float top, TopScratch& sh) {
+                                float top, TopScratch<Threads>& sh) {
     constexpr int E = kElems<T>;
     float x[E];
     // Largest key `at` with count(key >= at) >= k; holds for lo_key, not above the maximum's key.
@@ -502,7 +557,7 @@ __device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint
     while (at < end) {
         const uint32_t probe = at + (end - at) / 2 + 1;
         int n = 0;
-        for (int v = part.lo + static_cast<int>(threadIdx.x); v < part.hi; v += kBlock) {
+        for (int v = part.lo + static_cast<int>(threadIdx.x); v < part.hi; v += Threads) {
             row.get_masked(v, x);
 #pragma unroll
             for (int e = 0; e < E; ++e) n += order_key(x[e]) >= probe;
@@ -513,7 +568,7 @@ __device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint
     __syncthreads();
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
-    for (int v = part.lo + static_cast<int>(threadIdx.x); v < part.hi; v += kBlock) {
+    for (int v = part.lo + static_cast<int>(threadIdx.x); v < part.hi; v += Threads) {
         row.get_masked(v, x);
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -524,7 +579,7 @@ __device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint
     }
     __syncthreads();
     int have = sh.count;
-    for (int v0 = part.lo; v0 < part.hi && have < k; v0 += kBlock) {
+    for (int v0 = part.lo; v0 < part.hi && have < k; v0 += Threads) {
         const int v = v0 + static_cast<int>(threadIdx.x);
         int n = 0;
         if (v < part.hi) {
@@ -543,7 +598,7 @@ __device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint
         if (lane == kWave - 1) sh.wave_count[threadIdx.x / kWave] = before;
         __syncthreads();
         int total = 0;
-        for (int i = 0; i < kBlock / kWave; ++i) {
+        for (int i = 0; i < Threads / kWave; ++i) {
             if (i < static_cast<int>(threadIdx.x / kWave)) before += sh.wave_count[i];
             total += sh.wave_count[i];
         }
@@ -606,16 +661,16 @@ __device__ __forceinline__ void write_top(const LogprobParams& p, int64_t r, int
                             : (st.m != st.m ? st.m : -kInf);
 }
 
-template <typename T, bool Top>
-__global__ __launch_bounds__(kBlock) void logprobs_kernel(LogprobParams p) {
+template <typename T, bool Top, int Threads>
+__global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
     constexpr int E = kElems<T>, U = kLoads<T>;
     __shared__ BlockScratch bs;
-    __shared__ typename std::conditional<Top, TopScratch, int>::type top_sh;
+    __shared__ typename std::conditional<Top, TopScratch<Threads>, int>::type top_sh;
     const float c2 = p.c * kLog2e;
     const int tid = threadIdx.x;
     const int64_t units = p.rows * p.splits;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t r = unit / p.splits;
+        const int64_t r = row_of(unit, p.splits);
         const int split = static_cast<int>(unit - r * p.splits);
         const Row<T> row(p.x, r, p.stride, p.vocab);
         const Part part(row, split, p.part_vecs);
@@ -626,19 +681,19 @@ __global__ __launch_bounds__(kBlock) void logprobs_kernel(LogprobParams p) {
             if (y >= 0 && y < p.vocab) token_logit = row.at(static_cast<int>(y));
         }
         Acc a;
-        stream(
+        stream<Threads>(
             row, part,
             [&](const float* x, int b) {
                 const float top = max_of<kBatch>(x);
                 if constexpr (Top)
-                    top_sh.batch_max[b * kBlock + tid] = static_cast<uint16_t>(order_key16(top));
+                    top_sh.batch_max[b * Threads + tid] = static_cast<uint16_t>(order_key16(top));
                 add_batch<kBatch, true>(a, x, top, c2);
             },
             [&](const float* x, int) { add_batch<E, true>(a, x, max_of<E>(x), c2); });
-        const Set set = join_threads<true, kBlock / kWave>(
+        const Set set = join_threads<true, Threads / kWave>(
             a, c2, bs, [&](int j, float m) {
                 float s = 0.0f;
-                vectors_of(row, part, j,
+                vectors_of<Threads>(row, part, j,
                            [&](const float* x, int) { s += rest_sum<E>(x, m, c2); });
                 return s;
             });
@@ -654,50 +709,51 @@ __global__ __launch_bounds__(kBlock) void logprobs_kernel(LogprobParams p) {
                 else p.part_keys[unit * p.k + place] = key;
             };
             if (!(set.r >= 0.0f)) {                      // nothing unmasked, or NaN
-                for (int i = tid; i < p.k; i += kBlock) put(i, 0ull);
+                for (int i = tid; i < p.k; i += Threads) put(i, 0ull);
                 continue;
             }
             const uint32_t own = order_key16(a.m);
-            top_sh.thread_max[tid] = static_cast<uint16_t>(own);
-            if (tid == 0) top_sh.count = 0;
-            __syncthreads();
-            if (tid < kWave) {
-                const uint32_t t = kth_of_keys16(top_sh.thread_max, p.k);
-                if (tid == 0) top_sh.threshold = t > kKey16Finite ? t : kKey16Finite;
+            set_threshold(own, p.k, top_sh);
+            const uint32_t threshold = top_sh.threshold;
+            const float least = from_key(threshold << 16);   // key16(x) >= threshold: x >= least
+            if (own >= threshold) {
+                int b = 0;
+                for (int v0 = part.va; v0 < part.vb; v0 += U * Threads, ++b)
+                    if (top_sh.batch_max[b * Threads + tid] >= threshold) {
+                        const int n = atomicAdd(&top_sh.listed, 1);
+                        if (n < kListed)
+                            top_sh.list[n] = static_cast<uint16_t>(b * Threads + tid);
+                    }
             }
             __syncthreads();
-            const uint32_t threshold = top_sh.threshold;
             const auto collect = [&](const float* x, int v) {
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (order_key16(x[e]) >= threshold) {
+                    if (x[e] >= least) {
                         const int n = atomicAdd(&top_sh.count, 1);
                         if (n < kCandidates)
                             top_sh.cand[n] = candidate(x[e], v * E + e - row.phase);
                     }
             };
-            if (own >= threshold) {
-                int b = 0;
-                float x[E];
-                for (int v0 = part.va; v0 < part.vb; v0 += U * kBlock, ++b) {
-                    if (top_sh.batch_max[b * kBlock + tid] < threshold) continue;
-#pragma unroll
-                    for (int q = 0; q < U; ++q) {
-                        const int v = v0 + q * kBlock + tid;
-                        if (v < part.vb) {
-                            unpack<T>(row.load(v), x);
-                            collect(x, v);
-                        }
-                    }
-                }
-                if ((part.first && tid == 0) || (part.last && tid == 1)) {
-                    const int v = tid == 0 ? part.lo : part.hi - 1;
-                    row.get_masked(v, x);
+            // A lane for each vector of the listed batches, so that one round of loads, or few,
+            // brings them all.
+            const int listed = top_sh.listed;
+            float x[E];
+            for (int i = tid; i < (listed < kListed ? listed : kListed) * U; i += Threads) {
+                const int entry = top_sh.list[i / U];
+                const int v = part.va + (entry / Threads * U + i % U) * Threads + entry % Threads;
+                if (v < part.vb) {
+                    unpack<T>(row.load(v), x);
                     collect(x, v);
                 }
             }
+            if ((part.first && tid == 0) || (part.last && tid == 1)) {
+                const int v = tid == 0 ? part.lo : part.hi - 1;
+                row.get_masked(v, x);
+                collect(x, v);
+            }
             __syncthreads();
-            if (top_sh.count > kCandidates)
+            if (listed > kListed || top_sh.count > kCandidates)
                 collect_exactly(row, part, p.k, threshold << 16, set.m, top_sh);
             rank_candidates(top_sh, top_sh.count, p.k, put);
         }
@@ -708,7 +764,7 @@ __global__ __launch_bounds__(kBlock) void logprobs_kernel(LogprobParams p) {
 // Joins the parts of a row.
 template <typename T, bool Top>
 __global__ __launch_bounds__(kBlock) void logprobs_join_kernel(LogprobParams p) {
-    __shared__ typename std::conditional<Top, TopScratch, int>::type sh;
+    __shared__ typename std::conditional<Top, TopScratch<kBlock>, int>::type sh;
     const float c2 = p.c * kLog2e;
     const int tid = threadIdx.x;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
@@ -728,30 +784,30 @@ __global__ __launch_bounds__(kBlock) void logprobs_join_kernel(LogprobParams p) 
             write_row(p, r, st, token_logit, y);
         }
         if constexpr (Top) {
-            const unsigned long long* keys = p.part_keys + r * p.splits * p.k;
+            // Key i is place i / splits of part i % splits: the parts' best keys, taken in turn by
+            // the threads, make maxima close to the row's best.
+            const unsigned long long* part_keys = p.part_keys + r * p.splits * p.k;
             const int n = p.splits * p.k;
+            const auto key_at = [&](int i) {
+                const int place = static_cast<int>(static_cast<unsigned>(i) /
+                                                   static_cast<unsigned>(p.splits));
+                return part_keys[(i - place * p.splits) * p.k + place];
+            };
             const auto put = [&](int place, unsigned long long key) {
                 write_top(p, r, place, st.m == st.m ? key : 0ull, st);
             };
             uint32_t own = 0;
             for (int i = tid; i < n; i += kBlock) {
-                const uint32_t key = static_cast<uint32_t>(keys[i] >> 48);
+                const uint32_t key = static_cast<uint32_t>(key_at(i) >> 48);
                 own = key > own ? key : own;
             }
-            sh.thread_max[tid] = static_cast<uint16_t>(own);
-            if (tid == 0) sh.count = 0;
-            __syncthreads();
-            if (tid < kWave) {
-                const uint32_t t = kth_of_keys16(sh.thread_max, p.k);
-                if (tid == 0) sh.threshold = t > kKey16Finite ? t : kKey16Finite;
-            }
-            __syncthreads();
+            set_threshold(own, p.k, sh);
             unsigned long long least = static_cast<unsigned long long>(sh.threshold) << 48;
             const auto collect = [&]() {
                 for (int i = tid; i < n; i += kBlock)
-                    if (keys[i] >= least) {
+                    if (const unsigned long long key = key_at(i); key >= least) {
                         const int at = atomicAdd(&sh.count, 1);
-                        if (at < kCandidates) sh.cand[at] = keys[i];
+                        if (at < kCandidates) sh.cand[at] = key;
                     }
                 __syncthreads();
             };
@@ -762,7 +818,7 @@ __global__ __launch_bounds__(kBlock) void logprobs_join_kernel(LogprobParams p) 
                 for (int bit = 63; bit >= 0; --bit) {
                     const unsigned long long probe = least | (1ull << bit);
                     int above = 0;
-                    for (int i = tid; i < n; i += kBlock) above += keys[i] >= probe;
+                    for (int i = tid; i < n; i += kBlock) above += key_at(i) >= probe;
                     if (block_count(above, sh) >= p.k) least = probe;
                 }
                 __syncthreads();
@@ -882,7 +938,7 @@ __global__ __launch_bounds__(kBlock) void logprobs_grad_kernel(LogprobGradParams
     const float c2 = p.c * kLog2e;
     const int64_t units = p.rows * p.splits;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t r = unit / p.splits;
+        const int64_t r = row_of(unit, p.splits);
         const Row<T> row(p.x, r, p.stride, p.vocab);
         const OutRow<T> out(p.out, r, p.ostride, row);
         const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
@@ -965,6 +1021,7 @@ struct DistillParams {
     int64_t ostride;
     int32_t splits, part_vecs;
     float2* part_sets;             // [rows][splits]: m, r of the tokens outside the list
+    int64_t row0;                  // first row of a launch (rows in registers)
 };
 
 constexpr int kTop = FSDPSHARD_MAX_TOP;
@@ -1082,7 +1139,7 @@ __device__ Set outside_set(const Row<T>& row, const Part& part, float c2, const 
         }
     };
     Acc a;
-    stream(
+    stream<kBlock>(
         row, part,
         [&](float* x, int b) {
 #pragma unroll
@@ -1098,7 +1155,7 @@ __device__ Set outside_set(const Row<T>& row, const Part& part, float c2, const 
         });
     return join_threads<false, kBlock / kWave>(a, c2, sh, [&](int j, float m) {
         float s = 0.0f;
-        vectors_of(row, part, j, [&](float* x, int v) {
+        vectors_of<kBlock>(row, part, j, [&](float* x, int v) {
             drop(x, v);
             s += rest_sum<E>(x, m, c2);
         });
@@ -1210,7 +1267,7 @@ __global__ __launch_bounds__(kBlock) void distill_kernel(DistillParams p) {
     const float c2 = p.c * kLog2e;
     const int64_t units = p.rows * p.splits;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t r = unit / p.splits;
+        const int64_t r = row_of(unit, p.splits);
         const Row<T> row(p.x, r, p.stride, p.vocab);
         const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
         double logq;
@@ -1296,7 +1353,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     const float c2 = p.c * kLog2e;
     const int64_t units = p.rows * p.splits;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t r = unit / p.splits;
+        const int64_t r = row_of(unit, p.splits);
         const Row<T> row(p.x, r, p.stride, p.vocab);
         const OutRow<T> out(p.out, r, p.ostride, row);
         const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
@@ -1334,6 +1391,331 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
             }
         });
         __syncthreads();
+    }
+}
+
+// Whole rows in registers.  Each thread holds Vecs vectors of the row: loads are issued before the
+// list is worked out and arrive meanwhile, the maximum and the sum are taken from registers, and
+// with Grad the gradient is written from them, so that the row is read once.
+
+template <typename T>
+constexpr uint32_t kMinusInfBits = 0;
+template <>
+constexpr uint32_t kMinusInfBits<Bf16> = 0xFF80FF80u;
+template <>
+constexpr uint32_t kMinusInfBits<Fp16> = 0xFC00FC00u;
+template <>
+constexpr uint32_t kMinusInfBits<float> = 0xFF800000u;
+
+// Elements of `raw` whose bit is set become -inf.
+template <typename T>
+__device__ __forceinline__ void mask_out(u32x4& raw, uint32_t mask) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t drop;
+        if constexpr (sizeof(T) == 4)
+            drop = (mask >> i) & 1u ? ~0u : 0u;
+        else
+            drop = ((mask >> (2 * i)) & 1u ? 0xFFFFu : 0u) |
+                   ((mask >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+        raw[i] = (raw[i] & ~drop) | (kMinusInfBits<T> & drop);
+    }
+}
+
+// Keeps the compiler from holding the floats of an earlier unpacking of the row (two registers for
+// each one of 16-bit elements) instead of unpacking it again.
+template <int Vecs>
+__device__ __forceinline__ void forget_floats(u32x4 (&raw)[Vecs]) {
+#pragma unroll
+    for (int i = 0; i < Vecs; ++i) asm volatile("" : "+v"(raw[i]));
+}
+
+struct WholeScratch {
+    float list_top[2], list_max[2];
+    int list_some[2], list_bad[2], list_repeats[2];
+    double q_sum[2], list_sum[2], loss[2];
+    int list_ones[2];
+    float wave_top[kMaxWaves], wave_rest[kMaxWaves];
+    int wave_ones[kMaxWaves];
+    float coef;
+    int zero;
+    int32_t id[kTop];
+    double q[kTop];
+};
+
+template <typename T, int Threads, int Vecs, bool Grad>
+__global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams p) {
+    constexpr int E = kElems<T>, W = Threads / kWave;
+    __shared__ __align__(16) uint8_t map[Threads * Vecs];
+    __shared__ Slots<T> slots;
+    __shared__ WholeScratch sh;
+    __shared__ BlockScratch bs;
+    const float c2 = p.c * kLog2e;
+    const double c = p.c;
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    // One row for each work-group (the host cuts longer launches): in a loop over rows the compiler
+    // would keep the constants of the float64 functions in registers.
+    const int64_t r = p.row0 + blockIdx.x;
+    {
+        const Row<T> row(p.x, r, p.stride, p.vocab);
+        // The list's places and the row.
+        int id = -1;
+        float value = 0.0f;
+        if (tid < p.k) {
+            id = p.ids[r * p.tstride + tid];
+            value = p.values[r * p.tstride + tid];
+        }
+        const float g = Grad ? p.g[r] : 0.0f;
+        u32x4 raw[Vecs];
+#pragma unroll
+        for (int i = 0; i < Vecs; ++i) {
+            const int v = tid + i * Threads;
+            if (v < row.nvec) raw[i] = row.load(v);
+            else raw[i] = u32x4{kMinusInfBits<T>, kMinusInfBits<T>, kMinusInfBits<T>,
+                                kMinusInfBits<T>};
+        }
+#pragma unroll
+        for (int i = 0; i < (Vecs + 15) / 16; ++i)
+            if ((i * Threads + tid) * 16 < Threads * Vecs)
+                reinterpret_cast<u32x4*>(map)[i * Threads + tid] = u32x4{0, 0, 0, 0};
+        const bool valid = id >= 0, inside = valid && id < p.vocab;
+        float x = -kInf;
+        if (tid < kTop) {
+            if (inside) x = row.at(id);
+            sh.id[tid] = valid ? id : -1;
+            slots.mask[tid] = 0;
+            const float top = wave_max(valid ? value : -kInf);
+            const bool some = __ballot(valid) != 0;
+            const bool bad =
+                __ballot(valid && (!inside || value != value || value == kInf)) != 0;
+            if (lane == 0) {
+                sh.list_top[wave] = top;
+                sh.list_some[wave] = some;
+                sh.list_bad[wave] = bad;
+            }
+        }
+        __syncthreads();
+        const bool some = sh.list_some[0] || sh.list_some[1];
+        const bool bad = sh.list_bad[0] || sh.list_bad[1];
+        double logq = -HUGE_VAL, q = 0.0;
+        bool leads = valid;
+        if (tid < kTop) {
+            int slot = tid;
+            const int vec = (id + row.phase) / E;
+            for (int i = 0; i < p.k; ++i) {
+                const int other = sh.id[i];
+                if (i < tid) {
+                    if (other == id) leads = false;
+                    if (slot == tid && other >= 0 && (other + row.phase) / E == vec) slot = i;
+                }
+            }
+            if (inside) {
+                if (slot == tid) map[vec] = static_cast<uint8_t>(1 + tid);
+                atomicOr(&slots.mask[slot], 1u << ((id + row.phase) % E));
+            }
+            const float top = fmaxf(sh.list_top[0], sh.list_top[1]);
+            if (valid) {
+                logq = value;
+                if (!p.tail) logq = top == -kInf ? -HUGE_VAL : c * (logq - static_cast<double>(top));
+            }
+            q = logq > -HUGE_VAL ? exp(logq) : 0.0;
+            const double sum = wave_sum(q);
+            const bool repeats = __ballot(valid && !leads) != 0;
+            if (lane == 0) {
+                sh.q_sum[wave] = sum;
+                sh.list_repeats[wave] = repeats;
+            }
+        }
+        __syncthreads();
+        double mass = sh.q_sum[0] + sh.q_sum[1];
+        double rest = p.tail ? fmax(0.0, 1.0 - mass) : 0.0;
+        if (tid < kTop) {
+            if (!p.tail && mass > 0.0) {
+                q /= mass;
+                logq -= log(mass);
+            }
+            sh.q[tid] = q;
+            const float top = wave_max(leads ? x : -kInf);
+            const bool odd = __ballot(leads && !(x < kInf)) != 0;
+            if (lane == 0) sh.list_max[wave] = odd ? __builtin_nanf("") : top;
+        }
+        if (!p.tail && mass > 0.0) mass = 1.0;
+        // Only what is outside the list stays in the registers.
+        float own_top = kLowest;
+#pragma unroll
+        for (int i = 0; i < Vecs; ++i) {
+            const int v = tid + i * Threads;
+            uint32_t mask = 0;
+            const int slot = map[v];
+            if (slot != 0) mask = slots.mask[slot - 1];
+            if (v == 0) mask |= (1u << row.phase) - 1u;
+            const int end = (row.phase + row.vocab) - v * E;      // elements before the row's end
+            if (v == row.nvec - 1 && end < E) mask |= ~0u << end;
+            if (mask != 0) mask_out<T>(raw[i], mask);
+            float y[E];
+            unpack<T>(raw[i], y);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) own_top = max3(own_top, y[e], y[e + 1]);
+        }
+        forget_floats(raw);
+        const float wave_top = wave_max(own_top);
+        if (lane == 0) sh.wave_top[wave] = wave_top;
+        __syncthreads();
+        float mt = sh.wave_top[0];
+#pragma unroll
+        for (int i = 1; i < W; ++i) mt = fmaxf(mt, sh.wave_top[i]);
+        const float list_max = fmaxf(sh.list_max[0], sh.list_max[1]);
+        const bool list_nan = sh.list_max[0] != sh.list_max[0] || sh.list_max[1] != sh.list_max[1];
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Vecs; i += kBatch / E) {
+            float part = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kBatch / E; ++j) {
+                if (i + j < Vecs) {
+                    float y[E];
+                    unpack<T>(raw[i + j], y);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) part += exp2_fast(c2 * (y[e] - mt));
+                }
+            }
+            s += part;
+        }
+        forget_floats(raw);
+        const bool is_top = own_top == mt && s != 0.0f;
+        {
+            const float w = wave_sum(is_top ? s - 1.0f : s);
+            const int ones = __popcll(__ballot(is_top));
+            if (lane == 0) {
+                sh.wave_rest[wave] = w;
+                sh.wave_ones[wave] = ones;
+            }
+        }
+        // The maximum of the whole row, unless nothing outside the list is unmasked (then the
+        // list's alone, found below).
+        if (tid < kTop) {
+            const float m = fmaxf(list_max, mt);
+            const float own = leads ? x : -kInf;
+            double e = 0.0;
+            if (own > -kInf && own != m) e = exp(c * (static_cast<double>(own) - m));
+            const double sum = wave_sum(e);
+            const int ones = __popcll(__ballot(own > -kInf && own == m));
+            if (lane == 0) {
+                sh.list_sum[wave] = sum;
+                sh.list_ones[wave] = ones;
+            }
+        }
+        __syncthreads();
+        float rt = sh.wave_rest[0];
+        int ones = sh.wave_ones[0];
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            rt += sh.wave_rest[i];
+            ones += sh.wave_ones[i];
+        }
+        rt += static_cast<float>(ones) - 1.0f;
+        if (ones == 1 && rt < kPeaked) {
+            if (is_top) {
+                s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < Vecs; ++i) {
+                    float y[E];
+                    unpack<T>(raw[i], y);
+                    s += rest_sum<E>(y, mt, c2);
+                }
+            }
+            forget_floats(raw);
+            rt = block_sum(s, bs, 0, W);
+        }
+        const bool none = rt == -1.0f;              // nothing unmasked outside the list
+        const bool nan = rt != rt || list_nan;
+        DistillRow d;                               // in the threads of the list
+        if (none) rest = 0.0;
+        mass += rest;
+        if (tid < kTop) {
+            d.m = none ? list_max : fmaxf(list_max, mt);
+            d.mt = none ? -HUGE_VAL : mt;
+            d.Lt = none ? -HUGE_VAL : log1p(static_cast<double>(rt));
+            double sum = sh.list_sum[0] + sh.list_sum[1];
+            int count = sh.list_ones[0] + sh.list_ones[1];
+            if (!none) {
+                if (mt >= list_max) {
+                    count += 1;
+                    sum += rt;
+                } else {
+                    sum += (1.0 + rt) * exp(c * (static_cast<double>(mt) - list_max));
+                }
+            }
+            const bool empty = none && list_max == -kInf;
+            d.L = empty ? -HUGE_VAL : log1p(sum + (count - 1.0));
+            const double logp = list_logp(x, d, p.c);
+            sum = wave_sum(q > 0.0 ? q * (logq - logp) : 0.0);
+            if (lane == 0) sh.loss[wave] = sum;
+            if constexpr (Grad) {
+                const double gc = static_cast<double>(g) * c;
+                if (leads && inside) {
+                    if (sh.list_repeats[0] || sh.list_repeats[1])
+                        for (int i = tid + 1; i < p.k; ++i)
+                            if (sh.id[i] == id) q += sh.q[i];
+                    const int at = id + row.phase;
+                    slots.value[map[at / E] - 1][at % E] =
+                        static_cast<float>(gc * (mass * exp(logp) - q));
+                }
+                if (tid == 0) {
+                    sh.coef = none ? 0.0f
+                                   : static_cast<float>(gc * (mass * exp(c * (d.mt - d.m) - d.L) -
+                                                              rest * exp(-d.Lt)));
+                    sh.zero = !some || g == 0.0f || (empty && !bad && !nan);
+                }
+            }
+        }
+        __syncthreads();
+        if (tid == 0) {
+            double loss = sh.loss[0] + sh.loss[1];
+            if (rest > 0.0)
+                loss += rest * (log(rest) - (c * (d.mt - d.m) + d.Lt - d.L));
+            const float bad_value = __builtin_nanf("");
+            if (p.loss) p.loss[r] = !some ? 0.0f : bad || nan ? bad_value : static_cast<float>(loss);
+            if (p.stats) {
+                float* st = p.stats + 4 * r;
+                st[0] = !some ? 0.0f : nan ? bad_value : static_cast<float>(d.m);
+                st[1] = !some ? 0.0f : nan ? bad_value : static_cast<float>(d.L);
+                st[2] = !some || !p.tail ? 0.0f : nan ? bad_value : static_cast<float>(d.mt);
+                st[3] = !some || !p.tail ? 0.0f : nan ? bad_value : static_cast<float>(d.Lt);
+            }
+        }
+        if constexpr (Grad) {
+            const OutRow<T> out(p.out, r, p.ostride, row);
+            const bool zero = sh.zero;
+            const bool all_nan = !zero && (bad || nan);
+            const float flat = all_nan ? __builtin_nanf("") : 0.0f;
+            const float coef = sh.coef;
+#pragma unroll
+            for (int i = 0; i < Vecs; ++i) {
+                const int v = tid + i * Threads;
+                if (v >= row.nvec) continue;
+                float y[E];
+                if (zero || all_nan) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = flat;
+                } else {
+                    unpack<T>(raw[i], y);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - mt));
+                    const int slot = map[v];
+                    if (slot != 0) {
+                        const uint32_t mask = slots.mask[slot - 1];
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if ((mask >> e) & 1u) y[e] = slots.value[slot - 1][e];
+                    }
+                }
+                const bool partial = (v == 0 && row.first_partial()) ||
+                                     (v == row.nvec - 1 && row.last_partial());
+                if (partial) out.put_masked(row, v, y);
+                else out.put(v, y);
+            }
+        }
     }
 }
 
@@ -1411,11 +1793,12 @@ int check_dlogits(const fsdpshard_logits* x, const void* out, int64_t ostride, i
 
 constexpr int64_t kMaxGroups = 1 << 20;   // work-groups of a launch; each loops over its units
 
-int launch_units(const void* kernel, int64_t units, void* params, int64_t lds, void* stream) {
+int launch_units(const void* kernel, int64_t units, void* params, int64_t lds, void* stream,
+                 int threads = kBlock) {
     void* args[] = {params};
     const hipError_t e = hipLaunchKernel(
-        kernel, dim3(static_cast<unsigned>(units < kMaxGroups ? units : kMaxGroups)), dim3(kBlock),
-        args, static_cast<size_t>(lds), static_cast<hipStream_t>(stream));
+        kernel, dim3(static_cast<unsigned>(units < kMaxGroups ? units : kMaxGroups)),
+        dim3(static_cast<unsigned>(threads)), args, static_cast<size_t>(lds), static_cast<hipStream_t>(stream));
     return e == hipSuccess ? FSDPSHARD_OK : FSDPSHARD_ERR_HIP;
 }
 
@@ -1446,6 +1829,19 @@ Cut cut_rows(int64_t rows, int64_t vocab, int elem) {
     if (want > splits && most > splits) splits = want < most ? want : most;
     const int64_t part = (vecs + splits - 1) / splits;
     return {static_cast<int32_t>((vecs + part - 1) / part), static_cast<int32_t>(part)};
+}
+
+// Few rows that a work-group can hold whole: one of 1024 threads for each, in one launch.
+constexpr int kWide = 1024;
+constexpr int64_t kWideRows = 512;
+
+bool one_wide_group(int64_t rows, int64_t vocab, int elem) {
+    const int64_t per = 16 / elem;
+    return rows <= kWideRows && (vocab + 2 * per - 2) / per <= kMaxPartVecs;
+}
+Cut whole_rows(int64_t vocab, int elem) {
+    const int64_t per = 16 / elem;
+    return {1, static_cast<int32_t>((vocab + 2 * per - 2) / per)};
 }
 
 // The most parts of any type's rows (their workspace does not depend on the type).
@@ -1482,7 +1878,55 @@ DistillParams distill_params(const fsdpshard_logits* x, const fsdpshard_teacher*
     return p;
 }
 
+// The kernel that holds whole rows in registers, where they fit: the smallest work-group that
+// does, or the largest where rows are few.  Null: the row is too long.
+template <bool Grad>
+const void* whole_kernel(const DistillParams& p, int32_t dtype, int* threads) {
+    const int elem = element_bytes(dtype);
+    const int64_t per = 16 / elem;
+    const bool in_phase = aligned16(p.x) && (p.rows <= 1 || p.stride % per == 0);
+    const int64_t vecs = (p.vocab + (in_phase ? per - 1 : 2 * per - 2)) / per;
+    const bool few = p.rows <= kWideRows;
+    if (few && vecs <= 4 * 1024) {
+        *threads = 1024;
+        return by_dtype(dtype, [](auto t) {
+            return KERNEL(distill_whole_kernel<decltype(t), 1024, 4, Grad>);
+        });
+    }
+    if (vecs <= 16 * 256) {
+        *threads = 256;
+        return by_dtype(dtype, [](auto t) {
+            return KERNEL(distill_whole_kernel<decltype(t), 256, 16, Grad>);
+        });
+    }
+    if (!few && vecs <= 16 * 512) {
+        *threads = 512;
+        return by_dtype(dtype, [](auto t) {
+            return KERNEL(distill_whole_kernel<decltype(t), 512, 16, Grad>);
+        });
+    }
+    if (vecs <= 16 * 1024) {
+        *threads = 1024;
+        return by_dtype(dtype, [](auto t) {
+            return KERNEL(distill_whole_kernel<decltype(t), 1024, 16, Grad>);
+        });
+    }
+    return nullptr;
+}
+
+int launch_whole(const void* kernel, DistillParams& p, int threads, void* stream) {
+    for (p.row0 = 0; p.row0 < p.rows; p.row0 += kMaxGroups) {
+        const int64_t rows = p.rows - p.row0;
+        const int rc = launch_units(kernel, rows, &p, 0, stream, threads);
+        if (rc != FSDPSHARD_OK) return rc;
+    }
+    return FSDPSHARD_OK;
+}
+
 int launch_distill(DistillParams& p, int32_t dtype, void* workspace, void* stream) {
+    int threads = 0;
+    if (const void* whole = whole_kernel<false>(p, dtype, &threads))
+        return launch_whole(whole, p, threads, stream);
     p.part_sets = static_cast<float2*>(workspace);
     const void* kernel = by_dtype(
         dtype, [](auto t) { return KERNEL(distill_kernel<decltype(t)>); });
@@ -1540,7 +1984,9 @@ extern "C" int token_logprobs(const fsdpshard_logits* logits, const int64_t* ids
     const Span in[] = {{logits->data, xbytes}, {ids, 8 * rows}};
     if (!disjoint(out, 6, in, 2)) return FSDPSHARD_ERR_INVALID_ARG;
     if (rows == 0) return FSDPSHARD_OK;
-    const Cut cut = cut_rows(rows, logits->vocab, element_bytes(logits->dtype));
+    Cut cut = cut_rows(rows, logits->vocab, element_bytes(logits->dtype));
+    const bool wide = one_wide_group(rows, logits->vocab, element_bytes(logits->dtype));
+    if (wide) cut = whole_rows(logits->vocab, element_bytes(logits->dtype));
     LogprobParams p{};
     p.x = logits->data;
     p.rows = rows;
@@ -1560,9 +2006,13 @@ extern "C" int token_logprobs(const fsdpshard_logits* logits, const int64_t* ids
     p.part_keys = reinterpret_cast<unsigned long long*>(p.part_sets + rows * cut.splits);
     const void* kernel = by_dtype(logits->dtype, [&](auto t) {
         using T = decltype(t);
-        return top_k > 0 ? KERNEL(logprobs_kernel<T, true>) : KERNEL(logprobs_kernel<T, false>);
+        if (wide)
+            return top_k > 0 ? KERNEL(logprobs_kernel<T, true, kWide>)
+                             : KERNEL(logprobs_kernel<T, false, kWide>);
+        return top_k > 0 ? KERNEL(logprobs_kernel<T, true, kBlock>)
+                         : KERNEL(logprobs_kernel<T, false, kBlock>);
     });
-    rc = launch_units(kernel, rows * cut.splits, &p, 0, stream);
+    rc = launch_units(kernel, rows * cut.splits, &p, 0, stream, wide ? kWide : kBlock);
     if (rc != FSDPSHARD_OK || cut.splits == 1) return rc;
     kernel = by_dtype(logits->dtype, [&](auto t) {
         using T = decltype(t);
@@ -1691,6 +2141,13 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
     DistillParams p = distill_params(logits, teacher);
     p.loss = loss;
     p.stats = stats;
+    int threads = 0;
+    if (const void* whole = whole_kernel<true>(p, logits->dtype, &threads)) {
+        p.g = dloss;
+        p.out = dlogits;
+        p.ostride = dlogits_stride;
+        return launch_whole(whole, p, threads, stream);
+    }
     rc = launch_distill(p, logits->dtype, workspace, stream);
     if (rc != FSDPSHARD_OK) return rc;
     return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
