@@ -910,13 +910,13 @@ __device__ __forceinline__ void stream_through(const Row<T>& row, const OutRow<T
 }
 
 // Writes one value to a part.
-template <typename T>
+template <int Threads, typename T>
 __device__ __forceinline__ void fill_part(const Row<T>& row, const OutRow<T>& out,
                                           const Part& part, float value) {
     float x[kElems<T>];
 #pragma unroll
     for (int e = 0; e < kElems<T>; ++e) x[e] = value;
-    for (int v = part.va + static_cast<int>(threadIdx.x); v < part.vb; v += kBlock) out.put(v, x);
+    for (int v = part.va + static_cast<int>(threadIdx.x); v < part.vb; v += Threads) out.put(v, x);
     if ((part.first && threadIdx.x == 0) || (part.last && threadIdx.x == 1))
         out.put_masked(row, threadIdx.x == 0 ? part.lo : part.hi - 1, x);
 }
@@ -948,15 +948,15 @@ __global__ __launch_bounds__(kBlock) void logprobs_grad_kernel(LogprobGradParams
         const float m = p.stats[2 * r], L = p.stats[2 * r + 1];
         const float H = h != 0.0f ? p.entropy[r] : 0.0f;
         if (g == 0.0f && h == 0.0f) {
-            fill_part(row, out, part, 0.0f);
+            fill_part<kBlock>(row, out, part, 0.0f);
             continue;
         }
         if (y >= p.vocab || m != m) {
-            fill_part(row, out, part, __builtin_nanf(""));
+            fill_part<kBlock>(row, out, part, __builtin_nanf(""));
             continue;
         }
         if (m == -kInf) {
-            fill_part(row, out, part, 0.0f);
+            fill_part<kBlock>(row, out, part, 0.0f);
             continue;
         }
         // The token's entry: g (1 - p) through expm1, precise also where p is near 1.  Each thread
@@ -1102,7 +1102,7 @@ __device__ void load_teacher(const DistillParams& p, int64_t r, const Row<T>& ro
 // Fills the part's map: map[v - lo] is 0, or 1 + the slot of vector v.
 template <typename T>
 __device__ void map_list(const DistillParams& p, const Row<T>& row, const Part& part,
-                         const Teacher& t, uint8_t* map, Slots<T>& slots) {
+                         const int32_t* ids, uint8_t* map, Slots<T>& slots) {
     constexpr int E = kElems<T>;
     const int j = threadIdx.x, bytes = part.hi - part.lo;
     for (int i = j * 16; i < bytes; i += kBlock * 16)
@@ -1110,12 +1110,12 @@ __device__ void map_list(const DistillParams& p, const Row<T>& row, const Part& 
     if (j < kTop) slots.mask[j] = 0;
     __syncthreads();
     if (j < p.k) {
-        const int id = t.id[j];
+        const int id = ids[j];
         const int at = id + row.phase, v = at / E;
         if (id >= 0 && id < p.vocab && v >= part.lo && v < part.hi) {
             int slot = j;
             for (int i = p.k - 1; i >= 0; --i)
-                if (i < j && t.id[i] >= 0 && (t.id[i] + row.phase) / E == v) slot = i;
+                if (i < j && ids[i] >= 0 && (ids[i] + row.phase) / E == v) slot = i;
             if (slot == j) map[v - part.lo] = static_cast<uint8_t>(1 + j);
             atomicOr(&slots.mask[slot], 1u << (at % E));
         }
@@ -1258,34 +1258,25 @@ __device__ __forceinline__ void write_no_list(const DistillParams& p, int64_t r)
     }
 }
 
+// The tokens outside the list, part by part (rows longer than a work-group takes whole).
 template <typename T>
-__global__ __launch_bounds__(kBlock) void distill_kernel(DistillParams p) {
+__global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
     extern __shared__ __align__(16) uint8_t map[];
     __shared__ BlockScratch sh;
-    __shared__ Teacher t;
+    __shared__ int32_t ids[kTop];
     __shared__ Slots<T> slots;
-    const float c2 = p.c * kLog2e;
     const int64_t units = p.rows * p.splits;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const int64_t r = row_of(unit, p.splits);
         const Row<T> row(p.x, r, p.stride, p.vocab);
         const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
-        double logq;
-        float x;
-        bool leads;
-        load_teacher(p, r, row, t, sh, logq, x, leads);
-        if (!t.some) {
-            if (p.splits == 1) write_no_list(p, r);
-            continue;
-        }
-        map_list(p, row, part, t, map, slots);
-        const Set set = outside_set(row, part, c2, map, slots, sh);
-        if (p.splits == 1) {
-            const DistillRow d = join_list(set, x, leads, p.c, sh);
-            write_loss(p, r, t, d, logq, x, sh);
-        } else if (threadIdx.x == 0) {
-            p.part_sets[unit] = make_float2(set.m, set.r);
-        }
+        const int j = threadIdx.x;
+        const int id = j < p.k ? p.ids[r * p.tstride + j] : -1;
+        if (j < kTop) ids[j] = id;
+        if (!__syncthreads_or(id >= 0)) continue;
+        map_list(p, row, part, ids, map, slots);
+        const Set set = outside_set(row, part, p.c * kLog2e, map, slots, sh);
+        if (j == 0) p.part_sets[unit] = make_float2(set.m, set.r);
         __syncthreads();
     }
 }
@@ -1359,7 +1350,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
         const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
         const float g = p.g[r];
         if (g == 0.0f) {
-            fill_part(row, out, part, 0.0f);
+            fill_part<kBlock>(row, out, part, 0.0f);
             continue;
         }
         double logq;
@@ -1373,10 +1364,10 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
         d.Lt = p.tail ? p.stats[4 * r + 3] : 0.0;
         if (!t.some || t.bad || d.m != d.m || d.m == -HUGE_VAL) {
             const bool nan = t.some && (t.bad || d.m != d.m);
-            fill_part(row, out, part, nan ? __builtin_nanf("") : 0.0f);
+            fill_part<kBlock>(row, out, part, nan ? __builtin_nanf("") : 0.0f);
             continue;
         }
-        map_list(p, row, part, t, map, slots);
+        map_list(p, row, part, t.id, map, slots);
         float ref, coef;
         grad_values(p, row, part, t, d, g, x, leads, map, slots, ref, coef);
         stream_through(row, out, part, [&](float* y, int v) {
@@ -1394,9 +1385,13 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     }
 }
 
-// Whole rows in registers.  Each thread holds Vecs vectors of the row: loads are issued before the
-// list is worked out and arrive meanwhile, the maximum and the sum are taken from registers, and
-// with Grad the gradient is written from them, so that the row is read once.
+// Whole rows, one work-group each, in one of two forms.
+//   Vecs > 0   Each thread holds Vecs vectors of the row in registers: loads are issued before the
+//              list is worked out and arrive meanwhile, the maximum and the sum are taken from
+//              registers, and with Grad the gradient is written from them, so that the row is read
+//              once.
+//   Vecs == 0  The row is streamed (loss only): fewer registers, so more work-groups to a CU, which
+//              hide each other's work on the lists.
 
 template <typename T>
 constexpr uint32_t kMinusInfBits = 0;
@@ -1425,7 +1420,7 @@ __device__ __forceinline__ void mask_out(u32x4& raw, uint32_t mask) {
 // Keeps the compiler from holding the floats of an earlier unpacking of the row (two registers for
 // each one of 16-bit elements) instead of unpacking it again.
 template <int Vecs>
-__device__ __forceinline__ void forget_floats(u32x4 (&raw)[Vecs]) {
+__device__ __forceinline__ void forget_floats(u32x4 (&raw)[Vecs]) {   // (one unused when streaming)
 #pragma unroll
     for (int i = 0; i < Vecs; ++i) asm volatile("" : "+v"(raw[i]));
 }
@@ -1438,15 +1433,15 @@ struct WholeScratch {
     float wave_top[kMaxWaves], wave_rest[kMaxWaves];
     int wave_ones[kMaxWaves];
     float coef;
-    int zero;
+    int zero, owner;
     int32_t id[kTop];
     double q[kTop];
 };
 
 template <typename T, int Threads, int Vecs, bool Grad>
-__global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams p) {
+__global__ __launch_bounds__(Threads, Vecs > 0 ? LBG : LBS) void distill_whole_kernel(DistillParams p) {
     constexpr int E = kElems<T>, W = Threads / kWave;
-    __shared__ __align__(16) uint8_t map[Threads * Vecs];
+    extern __shared__ __align__(16) uint8_t map[];   // whole_map_bytes()
     __shared__ Slots<T> slots;
     __shared__ WholeScratch sh;
     __shared__ BlockScratch bs;
@@ -1466,7 +1461,7 @@ __global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams
             value = p.values[r * p.tstride + tid];
         }
         const float g = Grad ? p.g[r] : 0.0f;
-        u32x4 raw[Vecs];
+        u32x4 raw[Vecs > 0 ? Vecs : 1];
 #pragma unroll
         for (int i = 0; i < Vecs; ++i) {
             const int v = tid + i * Threads;
@@ -1474,10 +1469,8 @@ __global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams
             else raw[i] = u32x4{kMinusInfBits<T>, kMinusInfBits<T>, kMinusInfBits<T>,
                                 kMinusInfBits<T>};
         }
-#pragma unroll
-        for (int i = 0; i < (Vecs + 15) / 16; ++i)
-            if ((i * Threads + tid) * 16 < Threads * Vecs)
-                reinterpret_cast<u32x4*>(map)[i * Threads + tid] = u32x4{0, 0, 0, 0};
+        for (int i = tid * 16; i < (Vecs > 0 ? Threads * Vecs : row.nvec); i += Threads * 16)
+            *reinterpret_cast<u32x4*>(map + i) = u32x4{0, 0, 0, 0};
         const bool valid = id >= 0, inside = valid && id < p.vocab;
         float x = -kInf;
         if (tid < kTop) {
@@ -1540,8 +1533,38 @@ __global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams
             if (lane == 0) sh.list_max[wave] = odd ? __builtin_nanf("") : top;
         }
         if (!p.tail && mass > 0.0) mass = 1.0;
-        // Only what is outside the list stays in the registers.
+        // The tokens outside the list: their maximum, and in the streaming form their sum with it.
+        const Part part(row, 0, row.nvec);
+        const auto drop = [&](float* y, int v) {
+            const int slot = map[v];
+            if (slot != 0) {
+                const uint32_t mask = slots.mask[slot - 1];
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if ((mask >> e) & 1u) y[e] = -kInf;
+            }
+        };
         float own_top = kLowest;
+        Acc acc;
+        if constexpr (Vecs == 0) {
+            constexpr int U = kLoads<T>;
+            stream<Threads>(
+                row, part,
+                [&](float* y, int b) {
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int v = part.va + (b * U + i) * Threads + tid;
+                        if (v < part.vb) drop(y + i * E, v);
+                    }
+                    add_batch<kBatch, false>(acc, y, max_of<kBatch>(y), c2);
+                },
+                [&](float* y, int v) {
+                    drop(y, v);
+                    add_batch<E, false>(acc, y, max_of<E>(y), c2);
+                });
+            own_top = acc.m;
+        }
+        // In registers, only what is outside the list stays.
 #pragma unroll
         for (int i = 0; i < Vecs; ++i) {
             const int v = tid + i * Threads;
@@ -1566,30 +1589,62 @@ __global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams
         for (int i = 1; i < W; ++i) mt = fmaxf(mt, sh.wave_top[i]);
         const float list_max = fmaxf(sh.list_max[0], sh.list_max[1]);
         const bool list_nan = sh.list_max[0] != sh.list_max[0] || sh.list_max[1] != sh.list_max[1];
+        // In registers, 2^u is taken with one fused multiply-add: u = c2 x - b with b the rounded
+        // c2 mt.  The maximum's own term is then 2^delta, delta = c2 mt - b, instead of 1, and every
+        // sum is 2^delta times the true one; delta is at most 2^-5 while |c2 mt| < 2^20.  Beyond
+        // that (rows masked by the lowest value alone, say), the difference is taken first, in
+        // plain loops that read the row again: they are rare, and cost the others no registers.
+        const bool fused = fabsf(c2 * mt) < 0x1p20f;
+        const float base = fused ? c2 * mt : mt;
+        const float delta = fused && Vecs > 0 ? __builtin_fmaf(c2, mt, -base) : 0.0f;
+        const float one = exp2_fast(delta);
+        const auto exp_fused = [&](float y) { return exp2_fast(__builtin_fmaf(c2, y, -base)); };
+        const auto exp_apart = [&](float y) { return exp2_fast(c2 * (y - mt)); };
         float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < Vecs; i += kBatch / E) {
-            float part = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kBatch / E; ++j) {
-                if (i + j < Vecs) {
-                    float y[E];
-                    unpack<T>(raw[i + j], y);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) part += exp2_fast(c2 * (y[e] - mt));
-                }
-            }
-            s += part;
+        if constexpr (Vecs == 0) {
+            rebase<false>(acc, mt, c2);
+            s = acc.s;
         }
+        if (Vecs > 0 && fused) {
+#pragma unroll
+            for (int i = 0; i < Vecs; i += kBatch / E) {
+                float part_sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kBatch / E; ++j) {
+                    if (i + j < Vecs) {
+                        float y[E];
+                        unpack<T>(raw[i + j], y);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) part_sum += exp_fused(y[e]);
+                    }
+                }
+                s += part_sum;
+            }
+        }
+        // The same from memory: the terms, without the maximum's where it is left out.
+        const auto sum_again = [&](bool without_top) {
+            s = 0.0f;
+            for (int v = tid; v < row.nvec; v += Threads) {
+                float y[E], part_sum = 0.0f;
+                row.get_masked(v, y);
+                drop(y, v);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    part_sum += without_top && y[e] == mt ? 0.0f : exp_apart(y[e]);
+                s += part_sum;
+            }
+        };
+        if (Vecs > 0 && !fused) sum_again(false);
         forget_floats(raw);
         const bool is_top = own_top == mt && s != 0.0f;
         {
-            const float w = wave_sum(is_top ? s - 1.0f : s);
+            const float w = wave_sum(is_top ? s - one : s);
             const int ones = __popcll(__ballot(is_top));
             if (lane == 0) {
                 sh.wave_rest[wave] = w;
                 sh.wave_ones[wave] = ones;
             }
+            if (Vecs == 0 && is_top) sh.owner = tid;     // of one: used only then
         }
         // The maximum of the whole row, unless nothing outside the list is unmasked (then the
         // list's alone, found below).
@@ -1613,19 +1668,21 @@ __global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams
             rt += sh.wave_rest[i];
             ones += sh.wave_ones[i];
         }
-        rt += static_cast<float>(ones) - 1.0f;
+        rt = rt * exp2_fast(-delta) + (static_cast<float>(ones) - 1.0f);
         if (ones == 1 && rt < kPeaked) {
-            if (is_top) {
-                s = 0.0f;
-#pragma unroll
-                for (int i = 0; i < Vecs; ++i) {
-                    float y[E];
-                    unpack<T>(raw[i], y);
-                    s += rest_sum<E>(y, mt, c2);
+            if constexpr (Vecs > 0) {
+                if (is_top) {
+                    sum_again(true);
+                    s *= one;
                 }
+            } else {
+                if (is_top) s = 0.0f;
+                vectors_of<Threads>(row, part, sh.owner, [&](float* y, int v) {
+                    drop(y, v);
+                    s += rest_sum<E>(y, mt, c2);
+                });
             }
-            forget_floats(raw);
-            rt = block_sum(s, bs, 0, W);
+            rt = block_sum(s, bs, 0, W) * exp2_fast(-delta);
         }
         const bool none = rt == -1.0f;              // nothing unmasked outside the list
         const bool nan = rt != rt || list_nan;
@@ -1664,7 +1721,8 @@ __global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams
                 if (tid == 0) {
                     sh.coef = none ? 0.0f
                                    : static_cast<float>(gc * (mass * exp(c * (d.mt - d.m) - d.L) -
-                                                              rest * exp(-d.Lt)));
+                                                              rest * exp(-d.Lt))) *
+                                         exp2_fast(-delta);
                     sh.zero = !some || g == 0.0f || (empty && !bad && !nan);
                 }
             }
@@ -1690,30 +1748,40 @@ __global__ __launch_bounds__(Threads, 4) void distill_whole_kernel(DistillParams
             const bool all_nan = !zero && (bad || nan);
             const float flat = all_nan ? __builtin_nanf("") : 0.0f;
             const float coef = sh.coef;
+            const auto write = [&](int v, float* y) {
+                const int slot = map[v];
+                if (slot != 0) {
+                    const uint32_t mask = slots.mask[slot - 1];
 #pragma unroll
-            for (int i = 0; i < Vecs; ++i) {
-                const int v = tid + i * Threads;
-                if (v >= row.nvec) continue;
-                float y[E];
-                if (zero || all_nan) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) y[e] = flat;
-                } else {
-                    unpack<T>(raw[i], y);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - mt));
-                    const int slot = map[v];
-                    if (slot != 0) {
-                        const uint32_t mask = slots.mask[slot - 1];
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if ((mask >> e) & 1u) y[e] = slots.value[slot - 1][e];
-                    }
+                    for (int e = 0; e < E; ++e)
+                        if ((mask >> e) & 1u) y[e] = slots.value[slot - 1][e];
                 }
                 const bool partial = (v == 0 && row.first_partial()) ||
                                      (v == row.nvec - 1 && row.last_partial());
                 if (partial) out.put_masked(row, v, y);
                 else out.put(v, y);
+            };
+            if (zero || all_nan) {
+                fill_part<Threads>(row, out, part, flat);
+            } else if (fused) {
+#pragma unroll
+                for (int i = 0; i < Vecs; ++i) {
+                    const int v = tid + i * Threads;
+                    if (v >= row.nvec) continue;
+                    float y[E];
+                    unpack<T>(raw[i], y);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = coef * exp_fused(y[e]);
+                    write(v, y);
+                }
+            } else {
+                for (int v = tid; v < row.nvec; v += Threads) {   // in place: read, then written
+                    float y[E];
+                    row.get_masked(v, y);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = coef * exp_apart(y[e]);
+                    write(v, y);
+                }
             }
         }
     }
@@ -1878,58 +1946,56 @@ DistillParams distill_params(const fsdpshard_logits* x, const fsdpshard_teacher*
     return p;
 }
 
-// The kernel that holds whole rows in registers, where they fit: the smallest work-group that
-// does, or the largest where rows are few.  Null: the row is too long.
-template <bool Grad>
-const void* whole_kernel(const DistillParams& p, int32_t dtype, int* threads) {
-    const int elem = element_bytes(dtype);
-    const int64_t per = 16 / elem;
-    const bool in_phase = aligned16(p.x) && (p.rows <= 1 || p.stride % per == 0);
-    const int64_t vecs = (p.vocab + (in_phase ? per - 1 : 2 * per - 2)) / per;
-    const bool few = p.rows <= kWideRows;
-    if (few && vecs <= 4 * 1024) {
-        *threads = 1024;
-        return by_dtype(dtype, [](auto t) {
-            return KERNEL(distill_whole_kernel<decltype(t), 1024, 4, Grad>);
-        });
-    }
-    if (vecs <= 16 * 256) {
-        *threads = 256;
-        return by_dtype(dtype, [](auto t) {
-            return KERNEL(distill_whole_kernel<decltype(t), 256, 16, Grad>);
-        });
-    }
-    if (!few && vecs <= 16 * 512) {
-        *threads = 512;
-        return by_dtype(dtype, [](auto t) {
-            return KERNEL(distill_whole_kernel<decltype(t), 512, 16, Grad>);
-        });
-    }
-    if (vecs <= 16 * 1024) {
-        *threads = 1024;
-        return by_dtype(dtype, [](auto t) {
-            return KERNEL(distill_whole_kernel<decltype(t), 1024, 16, Grad>);
-        });
-    }
-    return nullptr;
+// The kernel for whole rows, or null where a row is too long for it.
+struct WholeKernel {
+    const void* kernel;
+    int threads, map_bytes;
+};
+
+template <int Threads, int Vecs, bool Grad>
+WholeKernel whole_form(int32_t dtype, int64_t vecs) {
+    return {by_dtype(dtype,
+                     [](auto t) {
+                         return KERNEL(distill_whole_kernel<decltype(t), Threads, Vecs, Grad>);
+                     }),
+            Threads, Vecs > 0 ? Threads * Vecs : static_cast<int>((vecs + 15) / 16 * 16)};
 }
 
-int launch_whole(const void* kernel, DistillParams& p, int threads, void* stream) {
+template <bool Grad>
+WholeKernel whole_kernel(const DistillParams& p, int32_t dtype) {
+    const int64_t per = 16 / element_bytes(dtype);
+    const bool in_phase = aligned16(p.x) && (p.rows <= 1 || p.stride % per == 0);
+    const int64_t vecs = (p.vocab + (in_phase ? per - 1 : 2 * per - 2)) / per;
+    // Few rows: the largest work-group, for latency.
+    if (p.rows <= kWideRows) {
+        if (vecs <= 4 * 1024) return whole_form<1024, 4, Grad>(dtype, vecs);
+        if (vecs <= 16 * 1024) return whole_form<1024, 16, Grad>(dtype, vecs);
+    }
+    if constexpr (Grad) {
+        if (vecs <= 16 * 256) return whole_form<256, 16, true>(dtype, vecs);
+        if (vecs <= 16 * 512) return whole_form<512, 16, true>(dtype, vecs);
+        if (vecs <= 16 * 1024) return whole_form<1024, 16, true>(dtype, vecs);
+    } else {
+        if (vecs <= kMaxPartVecs) return whole_form<256, 0, false>(dtype, vecs);
+    }
+    return {nullptr, 0, 0};
+}
+
+int launch_whole(const WholeKernel& whole, DistillParams& p, void* stream) {
     for (p.row0 = 0; p.row0 < p.rows; p.row0 += kMaxGroups) {
         const int64_t rows = p.rows - p.row0;
-        const int rc = launch_units(kernel, rows, &p, 0, stream, threads);
+        const int rc = launch_units(whole.kernel, rows, &p, whole.map_bytes, stream, whole.threads);
         if (rc != FSDPSHARD_OK) return rc;
     }
     return FSDPSHARD_OK;
 }
 
 int launch_distill(DistillParams& p, int32_t dtype, void* workspace, void* stream) {
-    int threads = 0;
-    if (const void* whole = whole_kernel<false>(p, dtype, &threads))
-        return launch_whole(whole, p, threads, stream);
+    const WholeKernel whole = whole_kernel<false>(p, dtype);
+    if (whole.kernel) return launch_whole(whole, p, stream);
     p.part_sets = static_cast<float2*>(workspace);
     const void* kernel = by_dtype(
-        dtype, [](auto t) { return KERNEL(distill_kernel<decltype(t)>); });
+        dtype, [](auto t) { return KERNEL(distill_part_kernel<decltype(t)>); });
     const int rc = launch_units(kernel, p.rows * p.splits, &p,
                                 map_bytes({p.splits, p.part_vecs}), stream);
     if (rc != FSDPSHARD_OK || p.splits == 1) return rc;
@@ -2141,12 +2207,12 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
     DistillParams p = distill_params(logits, teacher);
     p.loss = loss;
     p.stats = stats;
-    int threads = 0;
-    if (const void* whole = whole_kernel<true>(p, logits->dtype, &threads)) {
+    const WholeKernel whole = whole_kernel<true>(p, logits->dtype);
+    if (whole.kernel) {
         p.g = dloss;
         p.out = dlogits;
         p.ostride = dlogits_stride;
-        return launch_whole(whole, p, threads, stream);
+        return launch_whole(whole, p, stream);
     }
     rc = launch_distill(p, logits->dtype, workspace, stream);
     if (rc != FSDPSHARD_OK) return rc;
