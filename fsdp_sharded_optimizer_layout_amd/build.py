@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libfsdpshard.so")
 ARCH = "gfx950"
 
 HIP_SOURCES = [os.path.join(CSRC, "shard_step.hip"), os.path.join(CSRC, "reshard.hip"),
-               os.path.join(CSRC, "logits.hip"), os.path.join(CSRC, "calib.hip")]
+               os.path.join(CSRC, "token_logprobs.hip"), os.path.join(CSRC, "distill.hip"),
+               os.path.join(CSRC, "calib.hip")]
 HOST_SOURCES = [os.path.join(CSRC, "layout.cpp")]
 
 

@@ -1,0 +1,903 @@
+// Distillation from a teacher's top logits, of libfsdpshard.so on gfx950: the loss of every row, its
+// gradient, and both in one pass over the logits.
+//
+// The stream over a row takes only the tokens outside the teacher's list (their maximum and sum);
+// the at most 128 listed ones are added in float64 from their own loads.  So the mass outside the
+// list is a sum of its own and no difference, and a row whose likeliest token is listed, the usual
+// case, keeps the precision of a small L with no second look.  A byte for each vector of the row
+// (the map) says whether it holds listed tokens, and which slot describes them.
+
+#include "logits_common.h"
+
+namespace {
+
+struct DistillParams {
+    const void* x;
+    int64_t rows, vocab, stride;
+    float c;
+    const int32_t* ids;
+    const float* values;
+    int64_t tstride;
+    int32_t k, tail;
+    float *loss, *stats;
+    const float* g;
+    void* out;
+    int64_t ostride;
+    int32_t splits, part_vecs;
+    float2* part_sets;             // [rows][splits]: m, r of the tokens outside the list
+    int64_t unit0;                 // first unit of a launch
+};
+
+constexpr int kTop = FSDPSHARD_MAX_TOP;
+constexpr int kListWaves = kTop / kWave;
+
+// ------------------------------------------------------------------------------------------------
+// The list.  Thread j < kTop has place j.  q, log q and their sums are float64: 1 - sum q and p - q
+// are small differences.
+
+struct Place {
+    int id = -1;                   // below 0: empty
+    float value = 0.0f, x = -kInf; // the teacher's, the student's logit
+    bool valid = false, inside = false;
+    bool mapped = false;           // its token is in the part at hand
+    bool leads = false;            // the place that stands for its token
+    double logq = -HUGE_VAL, q = 0.0;
+};
+
+struct List {
+    float value_max[kListWaves], x_max[kListWaves];
+    int some[kListWaves], bad[kListWaves], ones[kListWaves];
+    double q_sum[kListWaves], term_sum[kListWaves], loss[kListWaves];
+    int repeats;                   // a token stands in several places
+    int32_t id[kTop];
+    double q[kTop];
+};
+
+// What the listed tokens of a vector do.
+template <typename T>
+struct Slots {
+    uint32_t mask[kTop];           // elements of the vector that are listed
+    float value[kTop][kElems<T>];  // their gradients
+};
+
+// Loads the list of row r.  Before the next step: a barrier.
+template <typename T>
+__device__ __forceinline__ Place open_list(const DistillParams& p, int64_t r, const Row<T>& row,
+                                           List& list) {
+    const int j = threadIdx.x;
+    Place a;
+    if (j < p.k) {
+        a.id = p.ids[r * p.tstride + j];
+        a.value = p.values[r * p.tstride + j];
+    }
+    a.valid = a.id >= 0;
+    a.inside = a.valid && a.id < p.vocab;
+    if (j == 0) list.repeats = 0;
+    if (j < kTop) {
+        if (a.inside) a.x = row.at(a.id);
+        list.id[j] = a.valid ? a.id : -1;
+        const float top = wave_max(a.valid ? a.value : -kInf);
+        const bool some = __ballot(a.valid) != 0;
+        const bool bad =
+            __ballot(a.valid && (!a.inside || a.value != a.value || a.value == kInf)) != 0;
+        if (j % kWave == 0) {
+            list.value_max[j / kWave] = top;
+            list.some[j / kWave] = some;
+            list.bad[j / kWave] = bad;
+        }
+    }
+    return a;
+}
+
+__device__ __forceinline__ bool list_some(const List& list) { return list.some[0] || list.some[1]; }
+__device__ __forceinline__ bool list_bad(const List& list) { return list.bad[0] || list.bad[1]; }
+
+// Enters a token into the map of vectors [lo, hi): map[v - lo] becomes 1 + the slot of its vector,
+// which is the number of the place that came first.  Whichever that is, the results are the same.
+// `map` and the slots' masks are clear; before the next step: a barrier.
+template <typename T>
+__device__ __forceinline__ void map_place(Place& a, const Row<T>& row, int lo, int hi,
+                                          uint8_t* map, Slots<T>& slots, List& list) {
+    constexpr int E = kElems<T>;
+    const int at = a.id + row.phase, v = at / E - lo;
+    if (!a.inside || v < 0 || v >= hi - lo) return;
+    a.mapped = true;
+    uint32_t* word = reinterpret_cast<uint32_t*>(map) + v / 4;
+    const int shift = v % 4 * 8;
+    uint32_t seen = *word;
+    int slot;
+    for (;;) {
+        const uint32_t byte = (seen >> shift) & 0xFFu;
+        if (byte != 0) {
+            slot = static_cast<int>(byte) - 1;
+            break;
+        }
+        const uint32_t before = atomicCAS(word, seen, seen | ((threadIdx.x + 1u) << shift));
+        if (before == seen) {
+            slot = threadIdx.x;
+            break;
+        }
+        seen = before;
+    }
+    const uint32_t bit = 1u << (at % E);
+    a.leads = (atomicOr(&slots.mask[slot], bit) & bit) == 0;
+    if (!a.leads) list.repeats = 1;
+}
+
+// The first of several places of a token leads (without repeats every place does, if mapped).
+__device__ __forceinline__ bool first_place(const DistillParams& p, const Place& a,
+                                            const List& list) {
+    const int j = threadIdx.x;
+    bool first = a.valid;
+    for (int i = 0; i < p.k; ++i) first = first && !(i < j && list.id[i] == a.id);
+    return first;
+}
+
+// The places' weights before they are normalised.  After open_list and a barrier; before the next
+// step: a barrier.
+__device__ __forceinline__ void weigh_list(const DistillParams& p, Place& a, List& list) {
+    const int j = threadIdx.x;
+    if (j >= kTop) return;
+    const float top = fmaxf(list.value_max[0], list.value_max[1]);
+    if (a.valid) {
+        a.logq = a.value;
+        if (!p.tail)
+            a.logq = top == -kInf ? -HUGE_VAL
+                                  : static_cast<double>(p.c) * (a.logq - static_cast<double>(top));
+        if (a.logq > -HUGE_VAL) a.q = exp(a.logq);
+    }
+    const double sum = wave_sum(a.q);
+    if (j % kWave == 0) list.q_sum[j / kWave] = sum;
+}
+
+// mass = sum q and, with a tail, rest = 1 - mass (all threads); q and log q of the places.
+__device__ __forceinline__ void settle_list(const DistillParams& p, Place& a, List& list,
+                                            double& mass, double& rest) {
+    mass = list.q_sum[0] + list.q_sum[1];
+    rest = 0.0;
+    if (p.tail) {
+        rest = fmax(0.0, 1.0 - mass);
+    } else if (mass > 0.0) {
+        if (threadIdx.x < kTop) {
+            a.q /= mass;
+            a.logq -= log(mass);
+        }
+        mass = 1.0;
+    }
+    if (threadIdx.x < kTop) list.q[threadIdx.x] = a.q;
+}
+
+// The maximum of the listed logits, by wave (NaN: a NaN or +inf among them).
+__device__ __forceinline__ void list_peak(const Place& a, List& list) {
+    const int j = threadIdx.x;
+    if (j >= kTop) return;
+    const float top = wave_max(a.leads ? a.x : -kInf);
+    const bool odd = __ballot(a.leads && !(a.x < kInf)) != 0;
+    if (j % kWave == 0) list.x_max[j / kWave] = odd ? __builtin_nanf("") : top;
+}
+
+// The listed tokens' terms against the row's maximum m, by wave: the terms of m are counted apart.
+__device__ __forceinline__ void list_terms(const DistillParams& p, const Place& a, float m,
+                                           List& list) {
+    const int j = threadIdx.x;
+    if (j >= kTop) return;
+    const float x = a.leads ? a.x : -kInf;
+    double e = 0.0;
+    if (x > -kInf && x != m) e = exp(static_cast<double>(p.c) * (static_cast<double>(x) - m));
+    const double sum = wave_sum(e);
+    const int ones = __popcll(__ballot(x > -kInf && x == m));
+    if (j % kWave == 0) {
+        list.term_sum[j / kWave] = sum;
+        list.ones[j / kWave] = ones;
+    }
+}
+
+// A row's statistics.  -inf stands for "nothing unmasked".
+struct RowResult {
+    double m, L;            // of the whole row
+    double mt, Lt;          // outside the list
+};
+
+// From the set outside the list (maximum mt, r = rt; rt = -1: nothing) and the list's terms.
+__device__ __forceinline__ RowResult solve_row(const DistillParams& p, float mt, float rt,
+                                               float list_max, const List& list) {
+    const double c = p.c;
+    const bool none = rt == -1.0f;
+    RowResult d;
+    d.m = none ? list_max : fmaxf(list_max, mt);
+    d.mt = none ? -HUGE_VAL : mt;
+    d.Lt = none ? -HUGE_VAL : log1p(static_cast<double>(rt));
+    double sum = list.term_sum[0] + list.term_sum[1];
+    int count = list.ones[0] + list.ones[1];
+    if (!none) {
+        if (mt >= list_max) {
+            count += 1;
+            sum += rt;
+        } else {
+            sum += (1.0 + rt) * exp(c * (static_cast<double>(mt) - list_max));
+        }
+    }
+    d.L = none && list_max == -kInf ? -HUGE_VAL : log1p(sum + (count - 1.0));
+    return d;
+}
+
+__device__ __forceinline__ double list_logp(const DistillParams& p, const Place& a,
+                                            const RowResult& d) {
+    return a.x == -kInf ? -HUGE_VAL : static_cast<double>(p.c) * (a.x - d.m) - d.L;
+}
+
+// The listed places' loss, by wave.
+__device__ __forceinline__ void list_loss(const Place& a, double logp, List& list) {
+    const double sum = wave_sum(a.q > 0.0 ? a.q * (a.logq - logp) : 0.0);
+    if (threadIdx.x % kWave == 0) list.loss[threadIdx.x / kWave] = sum;
+}
+
+// The gradient of a place's token, g c (mass p - q).
+template <typename T>
+__device__ __forceinline__ void set_value(const DistillParams& p, const Place& a, double logp,
+                                          double gc, double mass, const Row<T>& row, int lo,
+                                          const uint8_t* map, Slots<T>& slots, const List& list) {
+    if (!a.leads || !a.inside) return;
+    double q = a.q;
+    if (list.repeats)
+        for (int i = threadIdx.x + 1; i < p.k; ++i)
+            if (list.id[i] == a.id) q += list.q[i];
+    const int at = a.id + row.phase;
+    slots.value[map[at / kElems<T> - lo] - 1][at % kElems<T>] =
+        static_cast<float>(gc * (mass * exp(logp) - q));
+}
+
+// Any other token's is coef exp(c (x - mt)).
+__device__ __forceinline__ float outside_factor(const DistillParams& p, const RowResult& d,
+                                                double gc, double mass, double rest) {
+    if (d.mt == -HUGE_VAL) return 0.0f;
+    const double p_top = exp(static_cast<double>(p.c) * (d.mt - d.m) - d.L);
+    return static_cast<float>(gc * (mass * p_top - (rest > 0.0 ? rest * exp(-d.Lt) : 0.0)));
+}
+
+// Loss and statistics of a row, by thread 0, after the waves' losses and a barrier.
+__device__ __forceinline__ void write_row(const DistillParams& p, int64_t r, const RowResult& d,
+                                          double rest, bool nan, const List& list) {
+    const float bad_value = __builtin_nanf("");
+    const bool some = list_some(list);
+    double loss = list.loss[0] + list.loss[1];
+    if (rest > 0.0)
+        loss += rest * (log(rest) - (static_cast<double>(p.c) * (d.mt - d.m) + d.Lt - d.L));
+    p.loss[r] = !some ? 0.0f : list_bad(list) || nan ? bad_value : static_cast<float>(loss);
+    if (p.stats) {
+        const float tail_m = p.tail ? static_cast<float>(d.mt) : 0.0f;
+        const float tail_L = p.tail ? static_cast<float>(d.Lt) : 0.0f;
+        float* st = p.stats + 4 * r;
+        st[0] = !some ? 0.0f : nan ? bad_value : static_cast<float>(d.m);
+        st[1] = !some ? 0.0f : nan ? bad_value : static_cast<float>(d.L);
+        st[2] = !some || !p.tail ? 0.0f : nan ? bad_value : tail_m;
+        st[3] = !some || !p.tail ? 0.0f : nan ? bad_value : tail_L;
+    }
+}
+
+// Elements of vector v that are listed become -inf.
+template <typename T>
+__device__ __forceinline__ void drop_listed(float* y, int byte, const Slots<T>& slots) {
+    if (byte == 0) return;
+    const uint32_t mask = slots.mask[byte - 1];
+#pragma unroll
+    for (int e = 0; e < kElems<T>; ++e)
+        if ((mask >> e) & 1u) y[e] = -kInf;
+}
+
+// They get their values.
+template <typename T>
+__device__ __forceinline__ void put_listed(float* y, int byte, const Slots<T>& slots) {
+    if (byte == 0) return;
+    const uint32_t mask = slots.mask[byte - 1];
+#pragma unroll
+    for (int e = 0; e < kElems<T>; ++e)
+        if ((mask >> e) & 1u) y[e] = slots.value[byte - 1][e];
+}
+
+__device__ __forceinline__ void clear_map(uint8_t* map, int bytes, int threads) {
+    for (int i = threadIdx.x * 16; i < bytes; i += threads * 16)
+        *reinterpret_cast<u32x4*>(map + i) = u32x4{0, 0, 0, 0};
+}
+
+// ------------------------------------------------------------------------------------------------
+// Whole rows, one work-group each, in one of two forms.
+//   Vecs > 0   Each thread holds Vecs vectors of the row in registers: loads are issued before the
+//              list is worked out and arrive meanwhile, the maximum and the sum are taken from
+//              registers, and with Grad the gradient is written from them, so that the row is read
+//              once.
+//   Vecs == 0  The row is streamed (loss only): fewer registers, so more work-groups to a CU, which
+//              hide each other's work on the lists.
+// A launch has a work-group for each row and no loop over rows: in a loop the compiler would keep
+// the constants of the float64 functions in registers, twice as many as the rest needs.
+
+template <typename T>
+constexpr uint32_t kMinusInfBits = 0;
+template <>
+constexpr uint32_t kMinusInfBits<Bf16> = 0xFF80FF80u;
+template <>
+constexpr uint32_t kMinusInfBits<Fp16> = 0xFC00FC00u;
+template <>
+constexpr uint32_t kMinusInfBits<float> = 0xFF800000u;
+
+// Elements of `raw` whose bit is set become -inf.
+template <typename T>
+__device__ __forceinline__ void mask_out(u32x4& raw, uint32_t mask) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t drop;
+        if constexpr (sizeof(T) == 4)
+            drop = (mask >> i) & 1u ? ~0u : 0u;
+        else
+            drop = ((mask >> (2 * i)) & 1u ? 0xFFFFu : 0u) |
+                   ((mask >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+        raw[i] = (raw[i] & ~drop) | (kMinusInfBits<T> & drop);
+    }
+}
+
+// Keeps the compiler from holding the floats of an earlier unpacking of the row (two registers for
+// each one of 16-bit elements) instead of unpacking it again.
+template <int N>
+__device__ __forceinline__ void forget_floats(u32x4 (&raw)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(raw[i]));
+}
+
+struct WholeScratch {
+    float wave_top[kMaxWaves], wave_rest[kMaxWaves];
+    int wave_ones[kMaxWaves];
+    float coef;
+    int zero, owner;
+};
+
+template <typename T, int Threads, int Vecs, bool Grad>
+__global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kernel(DistillParams p) {
+    constexpr int E = kElems<T>, W = Threads / kWave;
+    extern __shared__ __align__(16) uint8_t map[];
+    __shared__ Slots<T> slots;
+    __shared__ List list;
+    __shared__ WholeScratch sh;
+    __shared__ BlockScratch bs;
+    const float c2 = p.c * kLog2e;
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    const int64_t r = p.unit0 + blockIdx.x;
+    const Row<T> row(p.x, r, p.stride, p.vocab);
+    const Part part(row, 0, row.nvec);
+
+    // The loads.
+    const float g = Grad ? p.g[r] : 0.0f;
+    u32x4 raw[Vecs > 0 ? Vecs : 1];
+#pragma unroll
+    for (int i = 0; i < Vecs; ++i) {
+        const int v = tid + i * Threads;
+        if (v < row.nvec) raw[i] = row.load(v);
+        else raw[i] = u32x4{kMinusInfBits<T>, kMinusInfBits<T>, kMinusInfBits<T>,
+                            kMinusInfBits<T>};
+    }
+    clear_map(map, Vecs > 0 ? Threads * Vecs : row.nvec, Threads);
+    if (tid < kTop) slots.mask[tid] = 0;
+    Place a = open_list(p, r, row, list);
+    __syncthreads();
+    if (!list_some(list)) {
+        if (tid == 0) write_row(p, r, RowResult{}, 0.0, false, list);
+        if constexpr (Grad)
+            fill_part<Threads>(row, OutRow<T>(p.out, r, p.ostride, row), part, 0.0f);
+        return;
+    }
+    if (tid < kTop) {
+        map_place(a, row, 0, row.nvec, map, slots, list);
+        weigh_list(p, a, list);
+    }
+    __syncthreads();
+    if (list.repeats) a.leads = a.mapped && first_place(p, a, list);
+    double mass, rest;
+    settle_list(p, a, list, mass, rest);
+    list_peak(a, list);
+
+    // The tokens outside the list: their maximum, and in the streaming form their sum with it.
+    float own_top = kLowest;
+    Acc acc;
+    if constexpr (Vecs == 0) {
+        constexpr int U = kLoads<T>;
+        stream<Threads>(
+            row, part,
+            [&](float* y, int b) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int v = part.va + (b * U + i) * Threads + tid;
+                    if (v < part.vb) drop_listed(y + i * E, map[v], slots);
+                }
+                add_batch<kBatch, false>(acc, y, max_of<kBatch>(y), c2);
+            },
+            [&](float* y, int v) {
+                drop_listed(y, map[v], slots);
+                add_batch<E, false>(acc, y, max_of<E>(y), c2);
+            });
+        own_top = acc.m;
+    }
+    // In registers, only what is outside the list stays.
+#pragma unroll
+    for (int i = 0; i < Vecs; ++i) {
+        const int v = tid + i * Threads;
+        uint32_t mask = 0;
+        const int byte = map[v];
+        if (byte != 0) mask = slots.mask[byte - 1];
+        if (v == 0) mask |= (1u << row.phase) - 1u;
+        const int end = (row.phase + row.vocab) - v * E;      // elements before the row's end
+        if (v == row.nvec - 1 && end < E) mask |= ~0u << end;
+        if (mask != 0) mask_out<T>(raw[i], mask);
+        float y[E];
+        unpack<T>(raw[i], y);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) own_top = max3(own_top, y[e], y[e + 1]);
+    }
+    forget_floats(raw);
+    const float wave_top = wave_max(own_top);
+    if (lane == 0) sh.wave_top[wave] = wave_top;
+    __syncthreads();
+    float mt = sh.wave_top[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) mt = fmaxf(mt, sh.wave_top[i]);
+    const float list_max = fmaxf(list.x_max[0], list.x_max[1]);
+    const bool list_nan = list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
+
+    // In registers, 2^u is taken with one fused multiply-add: u = c2 x - b with b the rounded
+    // c2 mt.  The maximum's own term is then 2^delta, delta = c2 mt - b, instead of 1, and every
+    // sum is 2^delta times the true one; delta is at most 2^-5 while |c2 mt| < 2^20.  Beyond
+    // that (rows masked by the lowest value alone, say), the difference is taken first, in
+    // plain loops that read the row again: they are rare, and cost the others no registers.
+    const bool fused = fabsf(c2 * mt) < 0x1p20f;
+    const float base = fused ? c2 * mt : mt;
+    const float delta = fused && Vecs > 0 ? __builtin_fmaf(c2, mt, -base) : 0.0f;
+    const float one = exp2_fast(delta);
+    const auto exp_fused = [&](float y) { return exp2_fast(__builtin_fmaf(c2, y, -base)); };
+    const auto exp_apart = [&](float y) { return exp2_fast(c2 * (y - mt)); };
+    float s = 0.0f;
+    // Sums of the terms, with the maximum's or without.
+    const auto sum_registers = [&](auto term) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Vecs; i += kBatch / E) {
+            float part_sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kBatch / E; ++j) {
+                if (i + j < Vecs) {
+                    float y[E];
+                    unpack<T>(raw[i + j], y);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) part_sum += term(y[e]);
+                }
+            }
+            s += part_sum;
+        }
+    };
+    const auto sum_memory = [&](bool without_top) {
+        s = 0.0f;
+        for (int v = tid; v < row.nvec; v += Threads) {
+            float y[E], part_sum = 0.0f;
+            row.get_masked(v, y);
+            drop_listed(y, map[v], slots);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                part_sum += without_top && y[e] == mt ? 0.0f : exp_apart(y[e]);
+            s += part_sum;
+        }
+    };
+    if constexpr (Vecs == 0) {
+        rebase<false>(acc, mt, c2);
+        s = acc.s;
+    } else {
+        if (fused) sum_registers(exp_fused);
+        else sum_memory(false);
+        forget_floats(raw);
+    }
+    const bool is_top = own_top == mt && s != 0.0f;      // a NaN sum counts
+    {
+        const float w = wave_sum(is_top ? s - one : s);
+        const int ones = __popcll(__ballot(is_top));
+        if (lane == 0) {
+            sh.wave_rest[wave] = w;
+            sh.wave_ones[wave] = ones;
+        }
+        if (is_top) sh.owner = tid;                      // of one: used only then
+    }
+    list_terms(p, a, fmaxf(list_max, mt), list);
+    __syncthreads();
+    float rt = sh.wave_rest[0];
+    int ones = sh.wave_ones[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+        rt += sh.wave_rest[i];
+        ones += sh.wave_ones[i];
+    }
+    rt = rt * exp2_fast(-delta) + (static_cast<float>(ones) - 1.0f);
+    if (ones == 1 && rt < kPeaked) {
+        // The sum of the thread that saw the maximum again, without the maximum.
+        if constexpr (Vecs == 0) {
+            if (is_top) s = 0.0f;
+            vectors_of<Threads>(row, part, sh.owner, [&](float* y, int v) {
+                drop_listed(y, map[v], slots);
+                s += rest_sum<E>(y, mt, c2);
+            });
+        } else {
+            if (is_top) {
+                if (fused) sum_registers([&](float y) { return y == mt ? 0.0f : exp_fused(y); });
+                else sum_memory(true);
+            }
+            forget_floats(raw);
+        }
+        rt = block_sum(s, bs, 0, W) * exp2_fast(-delta);
+    }
+    const bool nan = rt != rt || list_nan;
+    if (rt == -1.0f) rest = 0.0;                // nothing unmasked outside the list
+    mass += rest;
+    RowResult d{};
+    if (tid < kTop) {
+        d = solve_row(p, mt, rt, list_max, list);
+        const double logp = list_logp(p, a, d);
+        list_loss(a, logp, list);
+        if constexpr (Grad) {
+            const double gc = static_cast<double>(g) * p.c;
+            set_value(p, a, logp, gc, mass, row, 0, map, slots, list);
+            if (tid == 0) {
+                sh.coef = outside_factor(p, d, gc, mass, rest) * exp2_fast(-delta);
+                sh.zero = g == 0.0f || (d.L == -HUGE_VAL && !list_bad(list) && !nan);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) write_row(p, r, d, rest, nan, list);
+    if constexpr (Grad) {
+        const OutRow<T> out(p.out, r, p.ostride, row);
+        const float coef = sh.coef;
+        const auto write = [&](int v, float* y) {
+            put_listed(y, map[v], slots);
+            const bool partial = (v == 0 && row.first_partial()) ||
+                                 (v == row.nvec - 1 && row.last_partial());
+            if (partial) out.put_masked(row, v, y);
+            else out.put(v, y);
+        };
+        if (sh.zero) {
+            fill_part<Threads>(row, out, part, 0.0f);
+        } else if (list_bad(list) || nan) {
+            fill_part<Threads>(row, out, part, __builtin_nanf(""));
+        } else if (fused) {
+#pragma unroll
+            for (int i = 0; i < Vecs; ++i) {
+                const int v = tid + i * Threads;
+                if (v >= row.nvec) continue;
+                float y[E];
+                unpack<T>(raw[i], y);
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = coef * exp_fused(y[e]);
+                write(v, y);
+            }
+        } else {
+            for (int v = tid; v < row.nvec; v += Threads) {   // in place: read, then written
+                float y[E];
+                row.get_masked(v, y);
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = coef * exp_apart(y[e]);
+                write(v, y);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Rows in parts: rows too long for one work-group, and the gradient by itself.
+
+// The set of a part's tokens outside the list.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
+    constexpr int E = kElems<T>, U = kLoads<T>;
+    extern __shared__ __align__(16) uint8_t map[];
+    __shared__ BlockScratch bs;
+    __shared__ Slots<T> slots;
+    __shared__ List list;
+    const float c2 = p.c * kLog2e;
+    const int tid = threadIdx.x;
+    const int64_t unit = p.unit0 + blockIdx.x, r = row_of(unit, p.splits);
+    const Row<T> row(p.x, r, p.stride, p.vocab);
+    const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
+    Place a;
+    if (tid < p.k) a.id = p.ids[r * p.tstride + tid];
+    a.inside = a.id >= 0 && a.id < p.vocab;
+    clear_map(map, part.hi - part.lo, kBlock);
+    if (tid < kTop) slots.mask[tid] = 0;
+    if (!__syncthreads_or(a.id >= 0)) return;        // no list: the row's results are zeros
+    if (tid < kTop) map_place(a, row, part.lo, part.hi, map, slots, list);
+    __syncthreads();
+    Acc acc;
+    stream<kBlock>(
+        row, part,
+        [&](float* y, int b) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int v = part.va + (b * U + i) * kBlock + tid;
+                if (v < part.vb) drop_listed(y + i * E, map[v - part.lo], slots);
+            }
+            add_batch<kBatch, false>(acc, y, max_of<kBatch>(y), c2);
+        },
+        [&](float* y, int v) {
+            drop_listed(y, map[v - part.lo], slots);
+            add_batch<E, false>(acc, y, max_of<E>(y), c2);
+        });
+    const Set set = join_threads<false, kBlock / kWave>(acc, c2, bs, [&](int j, float m) {
+        float s = 0.0f;
+        vectors_of<kBlock>(row, part, j, [&](float* y, int v) {
+            drop_listed(y, map[v - part.lo], slots);
+            s += rest_sum<E>(y, m, c2);
+        });
+        return s;
+    });
+    if (tid == 0) p.part_sets[unit] = make_float2(set.m, set.r);
+}
+
+// Joins the parts of a row with its list.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
+    __shared__ List list;
+    const int64_t r = p.unit0 + blockIdx.x;
+    const Row<T> row(p.x, r, p.stride, p.vocab);
+    Place a = open_list(p, r, row, list);
+    const float2* sets = p.part_sets + r * p.splits;
+    const Set set = join_sets(p.splits, p.c * kLog2e,
+                              [&](int i) { return Set{sets[i].x, sets[i].y, 0.0f}; });
+    __syncthreads();
+    a.leads = a.inside && first_place(p, a, list);
+    weigh_list(p, a, list);
+    list_peak(a, list);
+    __syncthreads();
+    double mass, rest;
+    settle_list(p, a, list, mass, rest);
+    const float list_max = fmaxf(list.x_max[0], list.x_max[1]);
+    const bool list_nan = list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
+    list_terms(p, a, fmaxf(list_max, set.m), list);
+    __syncthreads();
+    RowResult d{};
+    if (threadIdx.x < kTop) {
+        d = solve_row(p, set.m, set.r, list_max, list);
+        list_loss(a, list_logp(p, a, d), list);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        write_row(p, r, d, set.r == -1.0f ? 0.0 : rest, set.r != set.r || list_nan, list);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
+    constexpr int E = kElems<T>;
+    extern __shared__ __align__(16) uint8_t map[];
+    __shared__ Slots<T> slots;
+    __shared__ List list;
+    __shared__ float shared_coef;
+    const float c2 = p.c * kLog2e;
+    const int tid = threadIdx.x;
+    const int64_t unit = p.unit0 + blockIdx.x, r = row_of(unit, p.splits);
+    const Row<T> row(p.x, r, p.stride, p.vocab);
+    const OutRow<T> out(p.out, r, p.ostride, row);
+    const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
+    const float g = p.g[r];
+    RowResult d;
+    d.m = p.stats[4 * r];
+    d.L = p.stats[4 * r + 1];
+    d.mt = p.tail ? p.stats[4 * r + 2] : d.m;         // without a tail the row's own will do
+    d.Lt = p.tail ? p.stats[4 * r + 3] : 0.0;
+    if (g == 0.0f) {
+        fill_part<kBlock>(row, out, part, 0.0f);
+        return;
+    }
+    Place a = open_list(p, r, row, list);
+    clear_map(map, part.hi - part.lo, kBlock);
+    if (tid < kTop) slots.mask[tid] = 0;
+    __syncthreads();
+    if (!list_some(list) || list_bad(list) || d.m != d.m || d.m == -HUGE_VAL) {
+        const bool nan = list_some(list) && (list_bad(list) || d.m != d.m);
+        fill_part<kBlock>(row, out, part, nan ? __builtin_nanf("") : 0.0f);
+        return;
+    }
+    if (tid < kTop) {
+        map_place(a, row, part.lo, part.hi, map, slots, list);
+        weigh_list(p, a, list);
+    }
+    __syncthreads();
+    if (list.repeats) a.leads = a.mapped && first_place(p, a, list);
+    double mass, rest;
+    settle_list(p, a, list, mass, rest);
+    if (d.mt == -HUGE_VAL) rest = 0.0;
+    mass += rest;
+    __syncthreads();                                  // the places' q
+    if (tid < kTop) {
+        const double gc = static_cast<double>(g) * p.c;
+        set_value(p, a, list_logp(p, a, d), gc, mass, row, part.lo, map, slots, list);
+        if (tid == 0) shared_coef = outside_factor(p, d, gc, mass, rest);
+    }
+    __syncthreads();
+    const float coef = shared_coef, ref = d.mt == -HUGE_VAL ? 0.0f : static_cast<float>(d.mt);
+    stream_through(row, out, part, [&](float* y, int v) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - ref));
+        put_listed(y, v < part.hi ? map[v - part.lo] : 0, slots);
+    });
+}
+
+// ------------------------------------------------------------------------------------------------
+// Host side.
+
+DistillParams distill_params(const fsdpshard_logits* x, const fsdpshard_teacher* t) {
+    DistillParams p{};
+    p.x = x->data;
+    p.rows = x->rows;
+    p.vocab = x->vocab;
+    p.stride = x->row_stride;
+    p.c = x->scale;
+    p.ids = t->ids;
+    p.values = t->values;
+    p.tstride = t->row_stride;
+    p.k = t->k;
+    p.tail = t->tail;
+    const Cut cut = cut_rows(x->rows, x->vocab, element_bytes(x->dtype));
+    p.splits = cut.splits;
+    p.part_vecs = cut.part_vecs;
+    return p;
+}
+
+// The kernel for whole rows, or null where a row is too long for it.
+struct WholeKernel {
+    const void* kernel;
+    int threads, map_bytes;
+};
+
+template <int Threads, int Vecs, bool Grad>
+WholeKernel whole_form(int32_t dtype, int64_t vecs) {
+    return {by_dtype(dtype,
+                     [](auto t) {
+                         return KERNEL(distill_whole_kernel<decltype(t), Threads, Vecs, Grad>);
+                     }),
+            Threads, Vecs > 0 ? Threads * Vecs : static_cast<int>((vecs + 15) / 16 * 16)};
+}
+
+template <bool Grad>
+WholeKernel whole_kernel(const DistillParams& p, int32_t dtype) {
+    const int64_t per = 16 / element_bytes(dtype);
+    const bool in_phase = aligned16(p.x) && (p.rows <= 1 || p.stride % per == 0);
+    const int64_t vecs = (p.vocab + (in_phase ? per - 1 : 2 * per - 2)) / per;
+    // Few rows: the largest work-group, for latency.
+    if (p.rows <= kWideRows) {
+        if (vecs <= 4 * 1024) return whole_form<1024, 4, Grad>(dtype, vecs);
+        if (vecs <= 16 * 1024) return whole_form<1024, 16, Grad>(dtype, vecs);
+    }
+    if constexpr (Grad) {
+        if (vecs <= 16 * 256) return whole_form<256, 16, true>(dtype, vecs);
+        if (vecs <= 16 * 512) return whole_form<512, 16, true>(dtype, vecs);
+        if (vecs <= 16 * 1024) return whole_form<1024, 16, true>(dtype, vecs);
+    } else {
+        if (vecs <= kMaxPartVecs) return whole_form<256, 0, false>(dtype, vecs);
+    }
+    return {nullptr, 0, 0};
+}
+
+int launch_distill(DistillParams& p, int32_t dtype, void* workspace, void* stream) {
+    const WholeKernel whole = whole_kernel<false>(p, dtype);
+    if (whole.kernel)
+        return launch_units(whole.kernel, p.rows, p, whole.map_bytes, stream, whole.threads);
+    p.part_sets = static_cast<float2*>(workspace);
+    const void* kernel = by_dtype(
+        dtype, [](auto t) { return KERNEL(distill_part_kernel<decltype(t)>); });
+    const int rc = launch_units(kernel, p.rows * p.splits, p,
+                                map_bytes({p.splits, p.part_vecs}), stream);
+    if (rc != FSDPSHARD_OK) return rc;
+    kernel = by_dtype(dtype, [](auto t) { return KERNEL(distill_join_kernel<decltype(t)>); });
+    return launch_units(kernel, p.rows, p, 0, stream);
+}
+
+int launch_distill_grad(DistillParams& p, int32_t dtype, const float* dloss, void* dlogits,
+                        int64_t dlogits_stride, void* stream) {
+    p.g = dloss;
+    p.out = dlogits;
+    p.ostride = dlogits_stride;
+    const void* kernel = by_dtype(
+        dtype, [](auto t) { return KERNEL(distill_grad_kernel<decltype(t)>); });
+    return launch_units(kernel, p.rows * p.splits, p, map_bytes({p.splits, p.part_vecs}),
+                        stream);
+}
+
+}  // namespace
+
+
+extern "C" int64_t distill_topk_workspace_bytes(int64_t rows, int64_t vocab) {
+    if (rows < 0 || vocab < 1 || vocab > FSDPSHARD_MAX_VOCAB || rows > kMaxRows) return -1;
+    const int64_t splits = most_splits(rows, vocab);
+    return splits > 1 ? (rows * splits * 8 + 15) / 16 * 16 : 0;
+}
+
+extern "C" int distill_topk(const fsdpshard_logits* logits, const fsdpshard_teacher* teacher,
+                            float* loss, float* stats, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+    int64_t xbytes = 0, tbytes = 0;
+    int rc = check_logits(logits, &xbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    rc = check_teacher(logits, teacher, &tbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    const int64_t rows = logits->rows;
+    if (rows > 0 && loss == nullptr) return FSDPSHARD_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, distill_topk_workspace_bytes(rows, logits->vocab),
+                      &rc))
+        return rc;
+    if (!aligned_to(loss, 4) || !aligned_to(stats, 4)) return FSDPSHARD_ERR_ALIGNMENT;
+    const Span out[] = {{loss, 4 * rows}, {stats, 16 * rows}, {workspace, workspace_bytes}};
+    const Span in[] = {{logits->data, xbytes}, {teacher->ids, tbytes}, {teacher->values, tbytes}};
+    if (!disjoint(out, 3, in, 3)) return FSDPSHARD_ERR_INVALID_ARG;
+    if (rows == 0) return FSDPSHARD_OK;
+    DistillParams p = distill_params(logits, teacher);
+    p.loss = loss;
+    p.stats = stats;
+    return launch_distill(p, logits->dtype, workspace, stream);
+}
+
+extern "C" int distill_topk_grad(const fsdpshard_logits* logits, const fsdpshard_teacher* teacher,
+                                 const float* stats, const float* dloss, void* dlogits,
+                                 int64_t dlogits_stride, void* stream) {
+    int64_t xbytes = 0, tbytes = 0, obytes = 0;
+    bool in_place = false;
+    int rc = check_logits(logits, &xbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    rc = check_teacher(logits, teacher, &tbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    rc = check_dlogits(logits, dlogits, dlogits_stride, &obytes, &in_place);
+    if (rc != FSDPSHARD_OK) return rc;
+    const int64_t rows = logits->rows;
+    if (rows > 0 && (stats == nullptr || dloss == nullptr)) return FSDPSHARD_ERR_INVALID_ARG;
+    if (!aligned_to(stats, 4) || !aligned_to(dloss, 4)) return FSDPSHARD_ERR_ALIGNMENT;
+    const Span out[] = {{dlogits, obytes}};
+    const Span in[] = {{in_place ? nullptr : logits->data, xbytes}, {teacher->ids, tbytes},
+                       {teacher->values, tbytes}, {stats, 16 * rows}, {dloss, 4 * rows}};
+    if (!disjoint(out, 1, in, 5)) return FSDPSHARD_ERR_INVALID_ARG;
+    if (rows == 0) return FSDPSHARD_OK;
+    DistillParams p = distill_params(logits, teacher);
+    p.stats = const_cast<float*>(stats);       // read only by this kernel
+    return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
+}
+
+extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
+                                      const fsdpshard_teacher* teacher, const float* dloss,
+                                      float* loss, float* stats, void* dlogits,
+                                      int64_t dlogits_stride, void* workspace,
+                                      int64_t workspace_bytes, void* stream) {
+    int64_t xbytes = 0, tbytes = 0, obytes = 0;
+    bool in_place = false;
+    int rc = check_logits(logits, &xbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    rc = check_teacher(logits, teacher, &tbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    rc = check_dlogits(logits, dlogits, dlogits_stride, &obytes, &in_place);
+    if (rc != FSDPSHARD_OK) return rc;
+    const int64_t rows = logits->rows;
+    if (rows > 0 && (loss == nullptr || stats == nullptr || dloss == nullptr))
+        return FSDPSHARD_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, distill_topk_workspace_bytes(rows, logits->vocab),
+                      &rc))
+        return rc;
+    if (!aligned_to(loss, 4) || !aligned_to(stats, 4) || !aligned_to(dloss, 4))
+        return FSDPSHARD_ERR_ALIGNMENT;
+    const Span out[] = {{loss, 4 * rows}, {stats, 16 * rows}, {dlogits, obytes},
+                        {workspace, workspace_bytes}};
+    const Span in[] = {{in_place ? nullptr : logits->data, xbytes}, {teacher->ids, tbytes},
+                       {teacher->values, tbytes}, {dloss, 4 * rows}};
+    if (!disjoint(out, 4, in, 4)) return FSDPSHARD_ERR_INVALID_ARG;
+    if (rows == 0) return FSDPSHARD_OK;
+    DistillParams p = distill_params(logits, teacher);
+    p.loss = loss;
+    p.stats = stats;
+    const WholeKernel whole = whole_kernel<true>(p, logits->dtype);
+    if (whole.kernel) {
+        p.g = dloss;
+        p.out = dlogits;
+        p.ostride = dlogits_stride;
+        return launch_units(whole.kernel, rows, p, whole.map_bytes, stream, whole.threads);
+    }
+    rc = launch_distill(p, logits->dtype, workspace, stream);
+    if (rc != FSDPSHARD_OK) return rc;
+    return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
+}
