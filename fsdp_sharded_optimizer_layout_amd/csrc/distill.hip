@@ -350,7 +350,7 @@ struct WholeScratch {
     int zero, owner;
 };
 
-template <typename T, int Threads, int Vecs, bool Grad>
+template <typename T, int Threads, int Vecs, bool Grad, bool Once>
 __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kernel(DistillParams p) {
     constexpr int E = kElems<T>, W = Threads / kWave;
     extern __shared__ __align__(16) uint8_t map[];
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     __shared__ BlockScratch bs;
     const float c2 = p.c * kLog2e;
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-    const int64_t r = p.unit0 + blockIdx.x;
+    const int64_t r = p.unit0 + unit_of_group();
     const Row<T> row(p.x, r, p.stride, p.vocab);
     const Part part(row, 0, row.nvec);
 
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     Acc acc;
     if constexpr (Vecs == 0) {
         constexpr int U = kLoads<T>;
-        stream<Threads>(
+        stream<Threads, Once>(
             row, part,
             [&](float* y, int b) {
 #pragma unroll
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
 // Rows in parts: rows too long for one work-group, and the gradient by itself.
 
 // The set of a part's tokens outside the list.
-template <typename T>
+template <typename T, bool Once>
 __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
     constexpr int E = kElems<T>, U = kLoads<T>;
     extern __shared__ __align__(16) uint8_t map[];
@@ -597,7 +597,7 @@ __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
     __shared__ List list;
     const float c2 = p.c * kLog2e;
     const int tid = threadIdx.x;
-    const int64_t unit = p.unit0 + blockIdx.x, r = row_of(unit, p.splits);
+    const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.splits);
     const Row<T> row(p.x, r, p.stride, p.vocab);
     const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
     Place a;
@@ -609,7 +609,7 @@ __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
     if (tid < kTop) map_place(a, row, part.lo, part.hi, map, slots, list);
     __syncthreads();
     Acc acc;
-    stream<kBlock>(
+    stream<kBlock, Once>(
         row, part,
         [&](float* y, int b) {
 #pragma unroll
@@ -638,7 +638,7 @@ __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
 template <typename T>
 __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
     __shared__ List list;
-    const int64_t r = p.unit0 + blockIdx.x;
+    const int64_t r = p.unit0 + unit_of_group();
     const Row<T> row(p.x, r, p.stride, p.vocab);
     Place a = open_list(p, r, row, list);
     const float2* sets = p.part_sets + r * p.splits;
@@ -665,6 +665,9 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
         write_row(p, r, d, set.r == -1.0f ? 0.0 : rest, set.r != set.r || list_nan, list);
 }
 
+// Vectors a thread takes; a part costs its share of the list's work.
+constexpr int kGradLoads = 4;
+
 template <typename T>
 __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     constexpr int E = kElems<T>;
@@ -674,7 +677,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     __shared__ float shared_coef;
     const float c2 = p.c * kLog2e;
     const int tid = threadIdx.x;
-    const int64_t unit = p.unit0 + blockIdx.x, r = row_of(unit, p.splits);
+    const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.splits);
     const Row<T> row(p.x, r, p.stride, p.vocab);
     const OutRow<T> out(p.out, r, p.ostride, row);
     const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
@@ -688,6 +691,8 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
         fill_part<kBlock>(row, out, part, 0.0f);
         return;
     }
+    u32x4 raw[kGradLoads];                            // arrives while the list is worked out
+    load_part(row, part, raw);
     Place a = open_list(p, r, row, list);
     clear_map(map, part.hi - part.lo, kBlock);
     if (tid < kTop) slots.mask[tid] = 0;
@@ -715,10 +720,10 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     }
     __syncthreads();
     const float coef = shared_coef, ref = d.mt == -HUGE_VAL ? 0.0f : static_cast<float>(d.mt);
-    stream_through(row, out, part, [&](float* y, int v) {
+    write_part(row, out, part, raw, [&](float* y, int v) {
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - ref));
-        put_listed(y, v < part.hi ? map[v - part.lo] : 0, slots);
+        put_listed(y, map[v - part.lo], slots);
     });
 }
 
@@ -749,17 +754,17 @@ struct WholeKernel {
     int threads, map_bytes;
 };
 
-template <int Threads, int Vecs, bool Grad>
+template <int Threads, int Vecs, bool Grad, bool Once = false>
 WholeKernel whole_form(int32_t dtype, int64_t vecs) {
     return {by_dtype(dtype,
                      [](auto t) {
-                         return KERNEL(distill_whole_kernel<decltype(t), Threads, Vecs, Grad>);
+                         return KERNEL(distill_whole_kernel<decltype(t), Threads, Vecs, Grad, Once>);
                      }),
             Threads, Vecs > 0 ? Threads * Vecs : static_cast<int>((vecs + 15) / 16 * 16)};
 }
 
 template <bool Grad>
-WholeKernel whole_kernel(const DistillParams& p, int32_t dtype) {
+WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     const int64_t per = 16 / element_bytes(dtype);
     const bool in_phase = aligned16(p.x) && (p.rows <= 1 || p.stride % per == 0);
     const int64_t vecs = (p.vocab + (in_phase ? per - 1 : 2 * per - 2)) / per;
@@ -773,18 +778,23 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype) {
         if (vecs <= 16 * 512) return whole_form<512, 16, true>(dtype, vecs);
         if (vecs <= 16 * 1024) return whole_form<1024, 16, true>(dtype, vecs);
     } else {
-        if (vecs <= kMaxPartVecs) return whole_form<256, 0, false>(dtype, vecs);
+        if (vecs <= kMaxPartVecs)
+            return once ? whole_form<256, 0, false, true>(dtype, vecs)
+                        : whole_form<256, 0, false>(dtype, vecs);
     }
     return {nullptr, 0, 0};
 }
 
-int launch_distill(DistillParams& p, int32_t dtype, void* workspace, void* stream) {
-    const WholeKernel whole = whole_kernel<false>(p, dtype);
+int launch_distill(DistillParams& p, int32_t dtype, bool once, void* workspace, void* stream) {
+    const WholeKernel whole = whole_kernel<false>(p, dtype, once);
     if (whole.kernel)
         return launch_units(whole.kernel, p.rows, p, whole.map_bytes, stream, whole.threads);
     p.part_sets = static_cast<float2*>(workspace);
     const void* kernel = by_dtype(
-        dtype, [](auto t) { return KERNEL(distill_part_kernel<decltype(t)>); });
+        dtype, [&](auto t) {
+            return once ? KERNEL(distill_part_kernel<decltype(t), true>)
+                        : KERNEL(distill_part_kernel<decltype(t), false>);
+        });
     const int rc = launch_units(kernel, p.rows * p.splits, p,
                                 map_bytes({p.splits, p.part_vecs}), stream);
     if (rc != FSDPSHARD_OK) return rc;
@@ -797,6 +807,9 @@ int launch_distill_grad(DistillParams& p, int32_t dtype, const float* dloss, voi
     p.g = dloss;
     p.out = dlogits;
     p.ostride = dlogits_stride;
+    const Cut cut = cut_gradient(p.vocab, element_bytes(dtype), kGradLoads * kBlock);
+    p.splits = cut.splits;
+    p.part_vecs = cut.part_vecs;
     const void* kernel = by_dtype(
         dtype, [](auto t) { return KERNEL(distill_grad_kernel<decltype(t)>); });
     return launch_units(kernel, p.rows * p.splits, p, map_bytes({p.splits, p.part_vecs}),
@@ -833,7 +846,7 @@ extern "C" int distill_topk(const fsdpshard_logits* logits, const fsdpshard_teac
     DistillParams p = distill_params(logits, teacher);
     p.loss = loss;
     p.stats = stats;
-    return launch_distill(p, logits->dtype, workspace, stream);
+    return launch_distill(p, logits->dtype, xbytes >= kOnceBytes, workspace, stream);
 }
 
 extern "C" int distill_topk_grad(const fsdpshard_logits* logits, const fsdpshard_teacher* teacher,
@@ -890,14 +903,14 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
     DistillParams p = distill_params(logits, teacher);
     p.loss = loss;
     p.stats = stats;
-    const WholeKernel whole = whole_kernel<true>(p, logits->dtype);
+    const WholeKernel whole = whole_kernel<true>(p, logits->dtype, false);
     if (whole.kernel) {
         p.g = dloss;
         p.out = dlogits;
         p.ostride = dlogits_stride;
         return launch_units(whole.kernel, rows, p, whole.map_bytes, stream, whole.threads);
     }
-    rc = launch_distill(p, logits->dtype, workspace, stream);
+    rc = launch_distill(p, logits->dtype, false, workspace, stream);   // the gradient reads on
     if (rc != FSDPSHARD_OK) return rc;
     return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
 }
