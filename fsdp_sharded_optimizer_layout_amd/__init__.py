@@ -616,7 +616,10 @@ def _logits_dtypes():
     return _LOGITS_DTYPES
 
 
-def _matrix(t, what, dtypes):
+# The checks below are on the path of calls that take a few microseconds: one pass over each
+# tensor's properties, and words only once something is wrong.
+
+def _matrix(t, what, dtypes, device=None):
     """(pointer, rows, columns, elements between rows) of a 2-D device tensor whose rows are
     contiguous."""
     if not t.is_cuda:
@@ -625,21 +628,28 @@ def _matrix(t, what, dtypes):
         raise ValueError(f"{what} must have two dimensions, rows and columns")
     if t.dtype not in dtypes:
         raise ValueError(f"{what} has dtype {t.dtype}")
+    if device is not None and t.get_device() != device:
+        raise ValueError("all tensors of a call must be on one device")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if rows <= 1:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what} must have contiguous rows")
+        return t.data_ptr(), rows, cols, cols
+    stride, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what} must have contiguous rows")
-    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
+    return t.data_ptr(), rows, cols, stride
 
 
 def _logits(t, scale):
     ptr, rows, vocab, stride = _matrix(t, "logits", _logits_dtypes())
-    return _Logits(ptr, rows, vocab, stride, _logits_dtypes()[t.dtype], float(scale))
+    return _Logits(ptr, rows, vocab, stride, _LOGITS_DTYPES[t.dtype], float(scale))
 
 
-def _teacher(ids, values, rows, tail):
+def _teacher(ids, values, rows, tail, device):
     import torch
-    ip, ir, ik, istride = _matrix(ids, "teacher_ids", {torch.int32})
-    vp, vr, vk, vstride = _matrix(values, "teacher_values", {torch.float32})
+    ip, ir, ik, istride = _matrix(ids, "teacher_ids", (torch.int32,), device)
+    vp, vr, vk, vstride = _matrix(values, "teacher_values", (torch.float32,), device)
     if (ir, ik) != (rows, vk) or vr != rows:
         raise ValueError("teacher_ids and teacher_values need one row for each row of the logits "
                          "and the same number of places")
@@ -648,44 +658,53 @@ def _teacher(ids, values, rows, tail):
     return _Teacher(ip, vp, istride, ik, 1 if tail else 0)
 
 
-def _dlogits(t, logits):
-    ptr, rows, vocab, stride = _matrix(t, "dlogits", {logits.dtype})
-    if tuple(t.shape) != tuple(logits.shape):
+def _dlogits(t, logits, device):
+    ptr, rows, vocab, stride = _matrix(t, "dlogits", (logits.dtype,), device)
+    if t.shape != logits.shape:
         raise ValueError("dlogits must have the shape of the logits")
     return ptr, stride
 
 
-def _of(t, what, dtype, numel):
+def _of(t, what, dtype, numel, device):
     """Pointer of a contiguous device tensor of exactly ``numel`` elements (None stays None)."""
-    if t is not None and not isinstance(t, int) and t.numel() != numel:
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.numel() == numel and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.numel() != numel:
         raise ValueError(f"{what} holds {t.numel()} elements, {numel} expected")
-    return _ptr(t, what, {dtype})
+    _ptr(t, what, (dtype,))
+    raise ValueError("all tensors of a call must be on one device")
 
 
-def _row_workspace(workspace, need, logits, stream):
-    """(pointer, bytes) of a call's workspace; allocated through PyTorch when omitted."""
+def _row_workspace(workspace, need, device, stream):
+    """(pointer, bytes, tensor) of a call's workspace; allocated through PyTorch when omitted."""
     if need < 0:
         raise ValueError("vocabulary or list size out of range")
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = _call_workspace(need, logits.device, stream)
-    return (_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace)
+        workspace = _call_workspace(need, f"cuda:{device}", stream)
+    elif workspace.get_device() != device:
+        raise ValueError("workspace must be on the device of the logits")
+    return _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
 
 
-def _on_device_of(call, logits, others, stream, run):
-    """run(stream handle) with the logits' device current; all tensors must be on it."""
+def _enqueue(call, function, device, stream, args):
+    """Calls the library with ``device`` current, on ``stream`` (or the device's current one)."""
     import torch
-    dev = logits.device
-    for t in others:
-        if t is not None and not isinstance(t, int) and t.device != dev:
-            raise ValueError("all tensors of a call must be on one device")
-    handle = _stream(stream, logits)
-    if torch.cuda.current_device() == dev.index:
-        _check(call, run(handle))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        code = function(*args, stream)
     else:
-        with torch.cuda.device(dev):
-            _check(call, run(handle))
+        with torch.cuda.device(device):
+            code = function(*args, stream)
+    if code != 0:
+        raise FsdpShardError(call, code)
 
 
 def token_logprobs_workspace_bytes(rows, vocab, top_k=0):
@@ -704,26 +723,26 @@ def token_logprobs(logits, ids=None, logprob=None, entropy=None, stats=None, top
     omitted, and then safe to use with any ``stream``)."""
     import torch
     x = _logits(logits, scale)
-    f32, rows, k = torch.float32, x.rows, 0
+    f32, rows, dev, k, h = torch.float32, x.rows, logits.get_device(), 0, lib()
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("give both of top_ids and top_logprobs, or neither")
+    if (ids is None) != (logprob is None):
+        raise ValueError("give both of ids and logprob, or neither")
+    top_i = top_v = None
     if top_ids is not None:
         if top_ids.dim() != 2 or top_ids.shape[0] != rows:
             raise ValueError("top_ids must be [rows, K]")
         k = top_ids.shape[1]
-    if (ids is None) != (logprob is None):
-        raise ValueError("give both of ids and logprob, or neither")
-    wp, wbytes, workspace = _row_workspace(
-        workspace, lib().token_logprobs_workspace_bytes(rows, x.vocab, k), logits, stream)
-    _on_device_of("token_logprobs", logits,
-                  (ids, logprob, entropy, stats, top_ids, top_logprobs, workspace), stream,
-                  lambda s: lib().token_logprobs(
-                      ctypes.byref(x), _of(ids, "ids", torch.int64, rows),
-                      _of(logprob, "logprob", f32, rows), _of(entropy, "entropy", f32, rows),
-                      _of(stats, "stats", f32, 2 * rows), k,
-                      _of(top_ids, "top_ids", torch.int32, k * rows) if k else None,
-                      _of(top_logprobs, "top_logprobs", f32, k * rows) if k else None,
-                      wp, wbytes, s))
+        top_i = _of(top_ids, "top_ids", torch.int32, k * rows, dev)
+        top_v = _of(top_logprobs, "top_logprobs", f32, k * rows, dev)
+        if k == 0:
+            top_i = top_v = None
+    ws, wbytes, workspace = _row_workspace(
+        workspace, h.token_logprobs_workspace_bytes(rows, x.vocab, k), dev, stream)
+    _enqueue("token_logprobs", h.token_logprobs, dev, stream,
+             (x, _of(ids, "ids", torch.int64, rows, dev), _of(logprob, "logprob", f32, rows, dev),
+              _of(entropy, "entropy", f32, rows, dev), _of(stats, "stats", f32, 2 * rows, dev), k,
+              top_i, top_v, ws, wbytes))
 
 
 def token_logprobs_grad(logits, ids, stats, dlogits, dlogprob=None, entropy=None, dentropy=None,
@@ -733,17 +752,14 @@ def token_logprobs_grad(logits, ids, stats, dlogits, dlogprob=None, entropy=None
     least one of them).  ``stats`` and ``entropy`` are what token_logprobs wrote."""
     import torch
     x = _logits(logits, scale)
-    f32, rows = torch.float32, x.rows
-    out, ostride = _dlogits(dlogits, logits)
+    f32, rows, dev = torch.float32, x.rows, logits.get_device()
+    out, ostride = _dlogits(dlogits, logits, dev)
     if dlogprob is None and dentropy is None:
         raise ValueError("give dlogprob, dentropy or both")
-    _on_device_of("token_logprobs_grad", logits,
-                  (ids, stats, dlogits, dlogprob, entropy, dentropy), stream,
-                  lambda s: lib().token_logprobs_grad(
-                      ctypes.byref(x), _of(ids, "ids", torch.int64, rows),
-                      _of(stats, "stats", f32, 2 * rows), _of(entropy, "entropy", f32, rows),
-                      _of(dlogprob, "dlogprob", f32, rows), _of(dentropy, "dentropy", f32, rows),
-                      out, ostride, s))
+    _enqueue("token_logprobs_grad", lib().token_logprobs_grad, dev, stream,
+             (x, _of(ids, "ids", torch.int64, rows, dev), _of(stats, "stats", f32, 2 * rows, dev),
+              _of(entropy, "entropy", f32, rows, dev), _of(dlogprob, "dlogprob", f32, rows, dev),
+              _of(dentropy, "dentropy", f32, rows, dev), out, ostride))
 
 
 def distill_topk_workspace_bytes(rows, vocab):
@@ -761,14 +777,13 @@ def distill_topk(logits, teacher_ids, teacher_values, loss, stats=None, tail=Fal
     (allocated here through PyTorch when omitted)."""
     import torch
     x = _logits(logits, scale)
-    t = _teacher(teacher_ids, teacher_values, x.rows, tail)
-    wp, wbytes, workspace = _row_workspace(
-        workspace, lib().distill_topk_workspace_bytes(x.rows, x.vocab), logits, stream)
-    _on_device_of("distill_topk", logits, (teacher_ids, teacher_values, loss, stats, workspace),
-                  stream,
-                  lambda s: lib().distill_topk(
-                      ctypes.byref(x), ctypes.byref(t), _of(loss, "loss", torch.float32, x.rows),
-                      _of(stats, "stats", torch.float32, 4 * x.rows), wp, wbytes, s))
+    f32, rows, dev, h = torch.float32, x.rows, logits.get_device(), lib()
+    t = _teacher(teacher_ids, teacher_values, rows, tail, dev)
+    ws, wbytes, workspace = _row_workspace(
+        workspace, h.distill_topk_workspace_bytes(rows, x.vocab), dev, stream)
+    _enqueue("distill_topk", h.distill_topk, dev, stream,
+             (x, t, _of(loss, "loss", f32, rows, dev), _of(stats, "stats", f32, 4 * rows, dev),
+              ws, wbytes))
 
 
 def distill_topk_grad(logits, teacher_ids, teacher_values, stats, dloss, dlogits, tail=False,
@@ -777,14 +792,12 @@ def distill_topk_grad(logits, teacher_ids, teacher_values, stats, dloss, dlogits
     for the gradient ``dloss`` (float32) of distill_topk's loss; ``stats`` is what it wrote."""
     import torch
     x = _logits(logits, scale)
-    t = _teacher(teacher_ids, teacher_values, x.rows, tail)
-    out, ostride = _dlogits(dlogits, logits)
-    _on_device_of("distill_topk_grad", logits,
-                  (teacher_ids, teacher_values, stats, dloss, dlogits), stream,
-                  lambda s: lib().distill_topk_grad(
-                      ctypes.byref(x), ctypes.byref(t),
-                      _of(stats, "stats", torch.float32, 4 * x.rows),
-                      _of(dloss, "dloss", torch.float32, x.rows), out, ostride, s))
+    f32, rows, dev = torch.float32, x.rows, logits.get_device()
+    t = _teacher(teacher_ids, teacher_values, rows, tail, dev)
+    out, ostride = _dlogits(dlogits, logits, dev)
+    _enqueue("distill_topk_grad", lib().distill_topk_grad, dev, stream,
+             (x, t, _of(stats, "stats", f32, 4 * rows, dev), _of(dloss, "dloss", f32, rows, dev),
+              out, ostride))
 
 
 def distill_topk_loss_grad(logits, teacher_ids, teacher_values, dloss, loss, stats, dlogits,
@@ -792,17 +805,14 @@ def distill_topk_loss_grad(logits, teacher_ids, teacher_values, dloss, loss, sta
     """distill_topk and distill_topk_grad in one call, for loss weights that are known before."""
     import torch
     x = _logits(logits, scale)
-    t = _teacher(teacher_ids, teacher_values, x.rows, tail)
-    out, ostride = _dlogits(dlogits, logits)
-    f32 = torch.float32
-    wp, wbytes, workspace = _row_workspace(
-        workspace, lib().distill_topk_workspace_bytes(x.rows, x.vocab), logits, stream)
-    _on_device_of("distill_topk_loss_grad", logits,
-                  (teacher_ids, teacher_values, dloss, loss, stats, dlogits, workspace), stream,
-                  lambda s: lib().distill_topk_loss_grad(
-                      ctypes.byref(x), ctypes.byref(t), _of(dloss, "dloss", f32, x.rows),
-                      _of(loss, "loss", f32, x.rows), _of(stats, "stats", f32, 4 * x.rows), out,
-                      ostride, wp, wbytes, s))
+    f32, rows, dev, h = torch.float32, x.rows, logits.get_device(), lib()
+    t = _teacher(teacher_ids, teacher_values, rows, tail, dev)
+    out, ostride = _dlogits(dlogits, logits, dev)
+    ws, wbytes, workspace = _row_workspace(
+        workspace, h.distill_topk_workspace_bytes(rows, x.vocab), dev, stream)
+    _enqueue("distill_topk_loss_grad", h.distill_topk_loss_grad, dev, stream,
+             (x, t, _of(dloss, "dloss", f32, rows, dev), _of(loss, "loss", f32, rows, dev),
+              _of(stats, "stats", f32, 4 * rows, dev), out, ostride, ws, wbytes))
 
 
 # ------------------------------------------------------------------------------ measurement aids

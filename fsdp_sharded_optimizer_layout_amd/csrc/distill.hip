@@ -779,8 +779,8 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
         if (vecs <= 16 * 1024) return whole_form<1024, 16, true>(dtype, vecs);
     } else {
         if (vecs <= kMaxPartVecs)
-            return once ? whole_form<256, 0, false, true>(dtype, vecs)
-                        : whole_form<256, 0, false>(dtype, vecs);
+            return once ? whole_form<kBlock, 0, false, true>(dtype, vecs)
+                        : whole_form<kBlock, 0, false>(dtype, vecs);
     }
     return {nullptr, 0, 0};
 }
