@@ -32,10 +32,10 @@ constexpr int kMaxima = 256;           // maxima of thread groups that the thres
 
 template <int Threads>
 struct TopScratch {
-    // 16-bit keys of the batches' maxima
-    uint16_t batch_max[(kMaxPartVecs + 4 * Threads - 1) / (4 * Threads) * Threads];
+    // 16-bit keys of the runs' maxima
+    uint16_t run_max[(kMaxPartVecs + 4 * Threads - 1) / (4 * Threads) * Threads];
     uint16_t maxima[kMaxima];
-    uint16_t list[kListed];            // batches that reach the threshold: batch * Threads + thread
+    uint16_t list[kListed];            // runs that reach the threshold
     int listed;
     int place[kBlock];
     alignas(16) uint32_t short_key[kBlock];
@@ -244,10 +244,11 @@ __device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint
 // Token log probabilities.
 //
 // One work-group streams one part of a row (a whole row when there are enough rows) and joins its
-// threads' running statistics.  For the alternatives it keeps, for each batch of 32 elements of a
-// thread, only the 16-bit key of the maximum.  The k-th largest of the 256 threads' maxima is a
-// lower bound of the k-th largest element, so only batches that reach it are read again (about k
-// of them), and the few elements that reach it are ranked.  The stream itself has no branch.
+// threads' running statistics.  For the alternatives it keeps, for each run of 32 neighbouring
+// elements, only the 16-bit key of the maximum.  The k-th largest of 256 maxima (of the threads'
+// elements) is a lower bound of the k-th largest element, so only runs that reach it are read again
+// (about k of them, 64 or 128 bytes each), and the few elements that reach it are ranked.  The
+// stream itself has no branch.
 
 struct LogprobParams {
     const void* x;
@@ -284,6 +285,26 @@ __device__ __forceinline__ void write_top(const LogprobParams& p, int64_t r, int
                             : (st.m != st.m ? st.m : -kInf);
 }
 
+// Notes the maxima of a batch's runs.  A run is 32 neighbouring elements, U lanes of one load; the
+// batch of U lanes has U of them, and each lane notes one: lane l that of load l % U.
+template <int Threads, int U>
+__device__ __forceinline__ void note_runs(float (&vec_max)[U], uint16_t* run_max) {
+    const auto with = [](float x, auto ctrl) {
+        const float y = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(
+            static_cast<int>(__float_as_uint(x)), decltype(ctrl)::value, 0xF, 0xF, true)));
+        return max3(x, y, y);
+    };
+    float pick = 0.0f;
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        float m = with(vec_max[q], std::integral_constant<int, 0xB1>{});       // lane ^ 1
+        m = with(m, std::integral_constant<int, 0x4E>{});                      // lane ^ 2
+        if constexpr (U == 8) m = with(m, std::integral_constant<int, 0x141>{});  // 8 mirrored
+        pick = q == 0 || static_cast<int>(threadIdx.x) % U == q ? m : pick;
+    }
+    run_max[threadIdx.x] = static_cast<uint16_t>(order_key16(pick));
+}
+
 template <typename T, bool Top, int Threads, bool Once>
 __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
     constexpr int E = kElems<T>, U = kLoads<T>;
@@ -306,9 +327,16 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
     stream<Threads, Once>(
         row, part,
         [&](const float* x, int b) {
-            const float top = max_of<kBatch>(x);
-            if constexpr (Top)
-                top_sh.batch_max[b * Threads + tid] = static_cast<uint16_t>(order_key16(top));
+            float top;
+            if constexpr (Top) {
+                float vec_max[U];
+#pragma unroll
+                for (int q = 0; q < U; ++q) vec_max[q] = max_of<E>(x + q * E);
+                top = max_of<U>(vec_max);
+                note_runs<Threads, U>(vec_max, top_sh.run_max + b * Threads);
+            } else {
+                top = max_of<kBatch>(x);
+            }
             add_batch<kBatch, true>(a, x, top, c2);
         },
         [&](const float* x, int) { add_batch<E, true>(a, x, max_of<E>(x), c2); });
@@ -338,13 +366,12 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
         set_threshold(own, p.k, top_sh);
         const uint32_t threshold = top_sh.threshold;
         const float least = from_key(threshold << 16);   // key16(x) >= threshold: x >= least
-        if (own >= threshold) {
+        {
             int b = 0;
             for (int v0 = part.va; v0 < part.vb; v0 += U * Threads, ++b)
-                if (top_sh.batch_max[b * Threads + tid] >= threshold) {
+                if (top_sh.run_max[b * Threads + tid] >= threshold) {
                     const int n = atomicAdd(&top_sh.listed, 1);
-                    if (n < kListed)
-                        top_sh.list[n] = static_cast<uint16_t>(b * Threads + tid);
+                    if (n < kListed) top_sh.list[n] = static_cast<uint16_t>(b * Threads + tid);
                 }
         }
         __syncthreads();
@@ -357,7 +384,7 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
                         top_sh.cand[n] = candidate(x[e], v * E + e - row.phase);
                 }
         };
-        // A lane for each vector of the listed batches, kRounds loads at once: one wait, mostly.
+        // A lane for each vector of the listed runs, kRounds loads at once: one wait, mostly.
         const int listed = top_sh.listed;
         const int wanted = (listed < kListed ? listed : kListed) * U;
         float x[E];
@@ -370,7 +397,8 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
                 at[n] = part.vb;
                 if (i < wanted) {
                     const int entry = top_sh.list[i / U];
-                    at[n] = part.va + (entry / Threads * U + i % U) * Threads + entry % Threads;
+                    at[n] = part.va + (entry / Threads * U + entry % U) * Threads +
+                            entry % Threads / U * U + i % U;
                 }
                 if (at[n] < part.vb) raw[n] = row.load(at[n]);
             }
