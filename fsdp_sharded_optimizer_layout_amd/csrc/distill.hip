@@ -394,11 +394,10 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     settle_list(p, a, list, mass, rest);
     list_peak(a, list);
 
-    // The tokens outside the list: their maximum, and in the streaming form their sum with it.
-    float own_top = kLowest;
+    // The tokens outside the list.  In registers, only they stay: the others become -inf.
+    constexpr int U = kLoads<T>;
     Acc acc;
     if constexpr (Vecs == 0) {
-        constexpr int U = kLoads<T>;
         stream<Threads, Once>(
             row, part,
             [&](float* y, int b) {
@@ -413,26 +412,33 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
                 drop_listed(y, map[v], slots);
                 add_batch<E, false>(acc, y, max_of<E>(y), c2);
             });
-        own_top = acc.m;
-    }
-    // In registers, only what is outside the list stays.
+    } else {
+        constexpr int Step = Vecs < U ? Vecs : U;
 #pragma unroll
-    for (int i = 0; i < Vecs; ++i) {
-        const int v = tid + i * Threads;
-        uint32_t mask = 0;
-        const int byte = map[v];
-        if (byte != 0) mask = slots.mask[byte - 1];
-        if (v == 0) mask |= (1u << row.phase) - 1u;
-        const int end = (row.phase + row.vocab) - v * E;      // elements before the row's end
-        if (v == row.nvec - 1 && end < E) mask |= ~0u << end;
-        if (mask != 0) mask_out<T>(raw[i], mask);
-        float y[E];
-        unpack<T>(raw[i], y);
+        for (int i0 = 0; i0 < Vecs; i0 += Step) {
+            float y[Step * E];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) own_top = max3(own_top, y[e], y[e + 1]);
+            for (int i = 0; i < Step; ++i) {
+                const int v = tid + (i0 + i) * Threads;
+                uint32_t mask = 0;
+                const int byte = map[v];
+                if (byte != 0) mask = slots.mask[byte - 1];
+                if (v == 0) mask |= (1u << row.phase) - 1u;
+                const int end = (row.phase + row.vocab) - v * E;   // elements before the row's end
+                if (v == row.nvec - 1 && end < E) mask |= ~0u << end;
+                if (mask != 0) mask_out<T>(raw[i0 + i], mask);
+            }
+#pragma unroll
+            for (int i = 0; i < Step; ++i) {
+                asm volatile("" : "+v"(raw[i0 + i]));      // one batch's floats at a time
+                unpack<T>(raw[i0 + i], y + i * E);
+            }
+            add_batch<Step * E, false>(acc, y, max_of<Step * E>(y), c2);
+            asm volatile("" : "+v"(acc.m), "+v"(acc.s));
+        }
+        forget_floats(raw);
     }
-    forget_floats(raw);
-    const float wave_top = wave_max(own_top);
+    const float wave_top = wave_max(acc.m);
     if (lane == 0) sh.wave_top[wave] = wave_top;
     __syncthreads();
     float mt = sh.wave_top[0];
@@ -440,66 +446,16 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     for (int i = 1; i < W; ++i) mt = fmaxf(mt, sh.wave_top[i]);
     const float list_max = fmaxf(list.x_max[0], list.x_max[1]);
     const bool list_nan = list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
-
-    // In registers, 2^u is taken with one fused multiply-add: u = c2 x - b with b the rounded
-    // c2 mt.  The maximum's own term is then 2^delta, delta = c2 mt - b, instead of 1, and every
-    // sum is 2^delta times the true one; delta is at most 2^-5 while |c2 mt| < 2^20.  Beyond
-    // that (rows masked by the lowest value alone, say), the difference is taken first, in
-    // plain loops that read the row again: they are rare, and cost the others no registers.
-    const bool fused = fabsf(c2 * mt) < 0x1p20f;
-    const float base = fused ? c2 * mt : mt;
-    const float delta = fused && Vecs > 0 ? __builtin_fmaf(c2, mt, -base) : 0.0f;
-    const float one = exp2_fast(delta);
-    const auto exp_fused = [&](float y) { return exp2_fast(__builtin_fmaf(c2, y, -base)); };
-    const auto exp_apart = [&](float y) { return exp2_fast(c2 * (y - mt)); };
-    float s = 0.0f;
-    // Sums of the terms, with the maximum's or without.
-    const auto sum_registers = [&](auto term) {
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < Vecs; i += kBatch / E) {
-            float part_sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kBatch / E; ++j) {
-                if (i + j < Vecs) {
-                    float y[E];
-                    unpack<T>(raw[i + j], y);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) part_sum += term(y[e]);
-                }
-            }
-            s += part_sum;
-        }
-    };
-    const auto sum_memory = [&](bool without_top) {
-        s = 0.0f;
-        for (int v = tid; v < row.nvec; v += Threads) {
-            float y[E], part_sum = 0.0f;
-            row.get_masked(v, y);
-            drop_listed(y, map[v], slots);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                part_sum += without_top && y[e] == mt ? 0.0f : exp_apart(y[e]);
-            s += part_sum;
-        }
-    };
-    if constexpr (Vecs == 0) {
-        rebase<false>(acc, mt, c2);
-        s = acc.s;
-    } else {
-        if (fused) sum_registers(exp_fused);
-        else sum_memory(false);
-        forget_floats(raw);
-    }
-    const bool is_top = own_top == mt && s != 0.0f;      // a NaN sum counts
+    const bool is_top = acc.m == mt && acc.s != 0.0f;     // a NaN sum counts
+    rebase<false>(acc, mt, c2);
     {
-        const float w = wave_sum(is_top ? s - one : s);
+        const float w = wave_sum(is_top ? acc.s - 1.0f : acc.s);
         const int ones = __popcll(__ballot(is_top));
         if (lane == 0) {
             sh.wave_rest[wave] = w;
             sh.wave_ones[wave] = ones;
         }
-        if (is_top) sh.owner = tid;                      // of one: used only then
+        if (is_top) sh.owner = tid;                       // of one: used only then
     }
     list_terms(p, a, fmaxf(list_max, mt), list);
     __syncthreads();
@@ -510,23 +466,27 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
         rt += sh.wave_rest[i];
         ones += sh.wave_ones[i];
     }
-    rt = rt * exp2_fast(-delta) + (static_cast<float>(ones) - 1.0f);
+    rt += static_cast<float>(ones) - 1.0f;
     if (ones == 1 && rt < kPeaked) {
         // The sum of the thread that saw the maximum again, without the maximum.
+        float s = is_top ? 0.0f : acc.s;
         if constexpr (Vecs == 0) {
-            if (is_top) s = 0.0f;
             vectors_of<Threads>(row, part, sh.owner, [&](float* y, int v) {
                 drop_listed(y, map[v], slots);
                 s += rest_sum<E>(y, mt, c2);
             });
         } else {
             if (is_top) {
-                if (fused) sum_registers([&](float y) { return y == mt ? 0.0f : exp_fused(y); });
-                else sum_memory(true);
+#pragma unroll
+                for (int i = 0; i < Vecs; ++i) {
+                    float y[E];
+                    unpack<T>(raw[i], y);
+                    s += rest_sum<E>(y, mt, c2);
+                }
             }
             forget_floats(raw);
         }
-        rt = block_sum(s, bs, 0, W) * exp2_fast(-delta);
+        rt = block_sum(s, bs, 0, W);
     }
     const bool nan = rt != rt || list_nan;
     if (rt == -1.0f) rest = 0.0;                // nothing unmasked outside the list
@@ -540,7 +500,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
             const double gc = static_cast<double>(g) * p.c;
             set_value(p, a, logp, gc, mass, row, 0, map, slots, list);
             if (tid == 0) {
-                sh.coef = outside_factor(p, d, gc, mass, rest) * exp2_fast(-delta);
+                sh.coef = outside_factor(p, d, gc, mass, rest);
                 sh.zero = g == 0.0f || (d.L == -HUGE_VAL && !list_bad(list) && !nan);
             }
         }
@@ -561,24 +521,17 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
             fill_part<Threads>(row, out, part, 0.0f);
         } else if (list_bad(list) || nan) {
             fill_part<Threads>(row, out, part, __builtin_nanf(""));
-        } else if (fused) {
+        } else {
 #pragma unroll
             for (int i = 0; i < Vecs; ++i) {
                 const int v = tid + i * Threads;
-                if (v >= row.nvec) continue;
+                if (v >= row.nvec) break;
                 float y[E];
                 unpack<T>(raw[i], y);
 #pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = coef * exp_fused(y[e]);
+                for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - mt));
                 write(v, y);
-            }
-        } else {
-            for (int v = tid; v < row.nvec; v += Threads) {   // in place: read, then written
-                float y[E];
-                row.get_masked(v, y);
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = coef * exp_apart(y[e]);
-                write(v, y);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
@@ -771,12 +724,14 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     // Few rows: the largest work-group, for latency.
     if (p.rows <= kWideRows) {
         if (vecs <= 4 * 1024) return whole_form<1024, 4, Grad>(dtype, vecs);
-        if (vecs <= 16 * 1024) return whole_form<1024, 16, Grad>(dtype, vecs);
+        if (!Grad && vecs <= 16 * 1024) return whole_form<1024, 16, false>(dtype, vecs);
     }
+    // With the gradient, rows up to 65,536 16-bit elements: longer ones leave a CU with one work-group,
+    // whose loads, arithmetic and stores then wait for each other.  Measured with 64 places: 4096 x
+    // 65536 bf16 227 us in registers, 88 + 181 in two passes; 2048 x 131072 278 and 92 + 176.
     if constexpr (Grad) {
         if (vecs <= 16 * 256) return whole_form<256, 16, true>(dtype, vecs);
         if (vecs <= 16 * 512) return whole_form<512, 16, true>(dtype, vecs);
-        if (vecs <= 16 * 1024) return whole_form<1024, 16, true>(dtype, vecs);
     } else {
         if (vecs <= kMaxPartVecs)
             return once ? whole_form<kBlock, 0, false, true>(dtype, vecs)
@@ -910,7 +865,8 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
         p.ostride = dlogits_stride;
         return launch_units(whole.kernel, rows, p, whole.map_bytes, stream, whole.threads);
     }
-    rc = launch_distill(p, logits->dtype, false, workspace, stream);   // the gradient reads on
+    // Otherwise two passes.  The second finds the logits in the last-level cache if that holds them.
+    rc = launch_distill(p, logits->dtype, xbytes > kLastLevelBytes, workspace, stream);
     if (rc != FSDPSHARD_OK) return rc;
     return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
 }

@@ -693,6 +693,7 @@ Cut whole_rows(int64_t vocab, int elem) {
 // 4096 x 32000 (262 MB) 58 and 53.  On one input again and again, which the 256 MB last-level cache
 // then holds, the second is 46 and 47, and below 100 MB the two are alike.
 constexpr int64_t kOnceBytes = int64_t{1} << 27;
+constexpr int64_t kLastLevelBytes = int64_t{1} << 28;
 
 // The most parts of any type's rows (their workspace does not depend on the type).
 int64_t most_splits(int64_t rows, int64_t vocab) {
