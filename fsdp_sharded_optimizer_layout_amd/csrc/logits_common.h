@@ -511,7 +511,7 @@ __device__ __forceinline__ void load_part(const Row<T>& row, const Part& part,
 #pragma unroll
     for (int q = 0; q < Loads; ++q) {
         const int v = part.va + q * kBlock + static_cast<int>(threadIdx.x);
-        raw[q] = row.load(v < part.vb ? v : part.lo);
+        raw[q] = row.load(v < part.vb ? v : 0);     // (a part may be empty; vector 0 is there)
     }
 }
 

@@ -339,6 +339,36 @@ def test_many_rows():
     assert (got["top_ids"] == want).all()
 
 
+def test_more_rows_than_one_launch_takes():
+    """Rows beyond 2^20 go to further launches of the same kernels."""
+    rows, vocab, k = (1 << 20) + 301, 5, 2
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(rows, vocab, generator=gen, device="cuda") * 2
+    ids = torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
+    f = dict(dtype=torch.float32, device="cuda")
+    lp, st = torch.full((rows,), 55.0, **f), torch.full((rows, 2), 55.0, **f)
+    ti = torch.full((rows, k), 55, dtype=torch.int32, device="cuda")
+    tl = torch.full((rows, k), 55.0, **f)
+    F.token_logprobs(x, ids, logprob=lp, stats=st, top_ids=ti, top_logprobs=tl)
+    want = torch.log_softmax(x.double(), 1)
+    best = want.topk(k, 1)
+    assert torch.equal(ti.long(), best.indices)
+    # unit(5) is 1.6e-5; |d| and |log p| are below 25 here
+    assert (lp - want.gather(1, ids[:, None])[:, 0]).abs().max() < 1e-3
+    assert (tl - best.values).abs().max() < 1e-3
+    g = torch.ones(rows, **f)
+    d = torch.full_like(x, 55.0)
+    F.token_logprobs_grad(x, ids, st, d, dlogprob=g)
+    hot = torch.nn.functional.one_hot(ids, vocab)
+    assert (d - (hot - want.exp())).abs().max() < 1e-3
+    loss, ds = torch.full((rows,), 55.0, **f), torch.full((rows, 4), 55.0, **f)
+    F.distill_topk_loss_grad(x, ti, tl, g, loss, ds, d)
+    q = torch.softmax(tl.double(), 1)
+    exact = (q * (q.log() - want.gather(1, ti.long()))).sum(1)
+    assert (loss - exact).abs().max() < 1e-3
+    assert (d - (want.exp() - torch.zeros_like(want).scatter(1, ti.long(), q))).abs().max() < 1e-3
+
+
 def test_no_rows():
     x = torch.empty(0, 50, device="cuda")
     e = torch.empty(0, device="cuda")
