@@ -24,7 +24,8 @@ struct DistillParams {
     void* out;
     int64_t ostride;
     int32_t splits, part_vecs;
-    float2* part_sets;             // [rows][splits]: m, r of the tokens outside the list
+    float2* part_sets;             // [rows][set_splits]: m, r of the tokens outside the list
+    int32_t set_splits;            // parts of the forward pass
     int64_t unit0;                 // first unit of a launch
 };
 
@@ -44,6 +45,8 @@ struct Place {
     double logq = -HUGE_VAL, q = 0.0;
 };
 
+constexpr int kSeen = 256;
+
 struct List {
     float value_max[kListWaves], x_max[kListWaves];
     int some[kListWaves], bad[kListWaves], ones[kListWaves];
@@ -51,6 +54,7 @@ struct List {
     int repeats;                   // a token stands in several places
     int32_t id[kTop];
     double q[kTop];
+    int32_t seen[kSeen];           // tokens, by a hash; -1: free
 };
 
 // What the listed tokens of a vector do.
@@ -122,6 +126,26 @@ __device__ __forceinline__ void map_place(Place& a, const Row<T>& row, int lo, i
     const uint32_t bit = 1u << (at % E);
     a.leads = (atomicOr(&slots.mask[slot], bit) & bit) == 0;
     if (!a.leads) list.repeats = 1;
+}
+
+// The same for a whole row without a map: a place leads if it enters its token first into a table.
+// `list.seen` is free (clear_seen and a barrier); before list.repeats is read: a barrier.
+__device__ __forceinline__ void clear_seen(List& list) {
+    if (threadIdx.x < kSeen) list.seen[threadIdx.x] = -1;
+}
+__device__ __forceinline__ bool enters_first(const Place& a, List& list) {
+    if (!a.inside) return false;
+    static_assert(kSeen >= 2 * kTop);             // half free: every search ends
+    uint32_t h = (static_cast<uint32_t>(a.id) * 2654435761u) >> 24;
+    for (;;) {
+        const int32_t before = atomicCAS(&list.seen[h], -1, a.id);
+        if (before == -1) return true;
+        if (before == a.id) {
+            list.repeats = 1;
+            return false;
+        }
+        h = (h + 1) % kSeen;
+    }
 }
 
 // The first of several places of a token leads (without repeats every place does, if mapped).
@@ -593,15 +617,17 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
     __shared__ List list;
     const int64_t r = p.unit0 + unit_of_group();
     const Row<T> row(p.x, r, p.stride, p.vocab);
+    clear_seen(list);
     Place a = open_list(p, r, row, list);
-    const float2* sets = p.part_sets + r * p.splits;
-    const Set set = join_sets(p.splits, p.c * kLog2e,
+    const float2* sets = p.part_sets + r * p.set_splits;
+    const Set set = join_sets(p.set_splits, p.c * kLog2e,
                               [&](int i) { return Set{sets[i].x, sets[i].y, 0.0f}; });
     __syncthreads();
-    a.leads = a.inside && first_place(p, a, list);
+    a.leads = enters_first(a, list);
     weigh_list(p, a, list);
     list_peak(a, list);
     __syncthreads();
+    if (list.repeats) a.leads = a.inside && first_place(p, a, list);
     double mass, rest;
     settle_list(p, a, list, mass, rest);
     const float list_max = fmaxf(list.x_max[0], list.x_max[1]);
@@ -618,29 +644,41 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
         write_row(p, r, d, set.r == -1.0f ? 0.0 : rest, set.r != set.r || list_nan, list);
 }
 
-// Vectors a thread takes; a part costs its share of the list's work.
+// The gradient.  With Join, after the parts alone: every work-group joins its row's parts with the
+// list by itself, and the first of a row writes loss and statistics.  That saves a launch where rows
+// are few; it needs the listed logits as they were, so not with the gradient in place.
+// A part costs its share of the list's work, so a thread takes 4 vectors (2 when nothing hangs on
+// the row, as in the gradient of log probabilities).
 constexpr int kGradLoads = 4;
 
-template <typename T>
+struct GradScratch {
+    float coef, ref;
+    int state;                     // what the row gets: 0 its gradient, 1 zeros, 2 NaN
+};
+
+template <typename T, bool Join>
 __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     constexpr int E = kElems<T>;
     extern __shared__ __align__(16) uint8_t map[];
     __shared__ Slots<T> slots;
     __shared__ List list;
-    __shared__ float shared_coef;
+    __shared__ GradScratch sh;
     const float c2 = p.c * kLog2e;
     const int tid = threadIdx.x;
     const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.splits);
+    const int split = static_cast<int>(unit - r * p.splits);
     const Row<T> row(p.x, r, p.stride, p.vocab);
     const OutRow<T> out(p.out, r, p.ostride, row);
-    const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
+    const Part part(row, split, p.part_vecs);
     const float g = p.g[r];
-    RowResult d;
-    d.m = p.stats[4 * r];
-    d.L = p.stats[4 * r + 1];
-    d.mt = p.tail ? p.stats[4 * r + 2] : d.m;         // without a tail the row's own will do
-    d.Lt = p.tail ? p.stats[4 * r + 3] : 0.0;
-    if (g == 0.0f) {
+    RowResult known{};
+    if constexpr (!Join) {
+        const float* st = p.stats + 4 * r;
+        known = {st[0], st[1], p.tail ? st[2] : st[0],    // without a tail the row's own will do
+                 p.tail ? st[3] : 0.0};
+    }
+    const bool writes_row = Join && split == 0;
+    if (g == 0.0f && !writes_row) {
         fill_part<kBlock>(row, out, part, 0.0f);
         return;
     }
@@ -649,30 +687,70 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     Place a = open_list(p, r, row, list);
     clear_map(map, part.hi - part.lo, kBlock);
     if (tid < kTop) slots.mask[tid] = 0;
+    Set set{};
+    if constexpr (Join) {
+        clear_seen(list);
+        const float2* sets = p.part_sets + r * p.set_splits;
+        set = join_sets(p.set_splits, c2,
+                        [&](int i) { return Set{sets[i].x, sets[i].y, 0.0f}; });
+    }
     __syncthreads();
-    if (!list_some(list) || list_bad(list) || d.m != d.m || d.m == -HUGE_VAL) {
-        const bool nan = list_some(list) && (list_bad(list) || d.m != d.m);
-        fill_part<kBlock>(row, out, part, nan ? __builtin_nanf("") : 0.0f);
+    if (!list_some(list)) {
+        if (writes_row && tid == 0) write_row(p, r, RowResult{}, 0.0, false, list);
+        fill_part<kBlock>(row, out, part, 0.0f);
         return;
     }
     if (tid < kTop) {
         map_place(a, row, part.lo, part.hi, map, slots, list);
         weigh_list(p, a, list);
     }
-    __syncthreads();
-    if (list.repeats) a.leads = a.mapped && first_place(p, a, list);
-    double mass, rest;
-    settle_list(p, a, list, mass, rest);
-    if (d.mt == -HUGE_VAL) rest = 0.0;
-    mass += rest;
-    __syncthreads();                                  // the places' q
-    if (tid < kTop) {
-        const double gc = static_cast<double>(g) * p.c;
-        set_value(p, a, list_logp(p, a, d), gc, mass, row, part.lo, map, slots, list);
-        if (tid == 0) shared_coef = outside_factor(p, d, gc, mass, rest);
+    bool first = false;                               // of the row's places of this token
+    if constexpr (Join) {
+        first = a.leads = enters_first(a, list);
+        list_peak(a, list);
     }
     __syncthreads();
-    const float coef = shared_coef, ref = d.mt == -HUGE_VAL ? 0.0f : static_cast<float>(d.mt);
+    if (list.repeats) {
+        first = a.inside && first_place(p, a, list);
+        if (Join) a.leads = first;
+    }
+    double mass, rest;
+    settle_list(p, a, list, mass, rest);
+    RowResult d{};
+    bool nan = false;
+    if constexpr (Join) {
+        const float list_max = fmaxf(list.x_max[0], list.x_max[1]);
+        nan = set.r != set.r || list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
+        list_terms(p, a, fmaxf(list_max, set.m), list);
+        __syncthreads();                              // the terms, and the places' q
+        if (tid < kTop) d = solve_row(p, set.m, set.r, list_max, list);
+        if (set.r == -1.0f) rest = 0.0;
+    } else {
+        d = known;
+        nan = d.m != d.m;
+        if (d.mt == -HUGE_VAL) rest = 0.0;
+        __syncthreads();                              // the places' q
+    }
+    mass += rest;
+    if (tid < kTop) {
+        const double gc = static_cast<double>(g) * p.c, logp = list_logp(p, a, d);
+        if constexpr (Join) list_loss(a, logp, list);
+        if (Join || list.repeats) a.leads = a.mapped && first;
+        set_value(p, a, logp, gc, mass, row, part.lo, map, slots, list);
+        if (tid == 0) {
+            const bool bad = list_bad(list) || nan;
+            sh.coef = outside_factor(p, d, gc, mass, rest);
+            sh.ref = d.mt == -HUGE_VAL ? 0.0f : static_cast<float>(d.mt);
+            sh.state = g == 0.0f || (d.m == -HUGE_VAL && !bad) ? 1 : bad ? 2 : 0;
+        }
+    }
+    __syncthreads();
+    if (writes_row && tid == 0) write_row(p, r, d, rest, nan, list);
+    if (sh.state != 0) {
+        fill_part<kBlock>(row, out, part, sh.state == 2 ? __builtin_nanf("") : 0.0f);
+        return;
+    }
+    const float coef = sh.coef, ref = sh.ref;
     write_part(row, out, part, raw, [&](float* y, int v) {
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - ref));
@@ -740,35 +818,39 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     return {nullptr, 0, 0};
 }
 
+constexpr int64_t kJoinRows = 512;
+
+// The sets of the rows' parts.
+int launch_parts(DistillParams& p, int32_t dtype, bool once, void* workspace, void* stream) {
+    p.part_sets = static_cast<float2*>(workspace);
+    p.set_splits = p.splits;
+    const void* kernel = by_dtype(dtype, [&](auto t) {
+        return once ? KERNEL(distill_part_kernel<decltype(t), true>)
+                    : KERNEL(distill_part_kernel<decltype(t), false>);
+    });
+    return launch_units(kernel, p.rows * p.splits, p, map_bytes({p.splits, p.part_vecs}), stream);
+}
+
 int launch_distill(DistillParams& p, int32_t dtype, bool once, void* workspace, void* stream) {
     const WholeKernel whole = whole_kernel<false>(p, dtype, once);
     if (whole.kernel)
         return launch_units(whole.kernel, p.rows, p, whole.map_bytes, stream, whole.threads);
-    p.part_sets = static_cast<float2*>(workspace);
-    const void* kernel = by_dtype(
-        dtype, [&](auto t) {
-            return once ? KERNEL(distill_part_kernel<decltype(t), true>)
-                        : KERNEL(distill_part_kernel<decltype(t), false>);
-        });
-    const int rc = launch_units(kernel, p.rows * p.splits, p,
-                                map_bytes({p.splits, p.part_vecs}), stream);
+    const int rc = launch_parts(p, dtype, once, workspace, stream);
     if (rc != FSDPSHARD_OK) return rc;
-    kernel = by_dtype(dtype, [](auto t) { return KERNEL(distill_join_kernel<decltype(t)>); });
+    const void* kernel =
+        by_dtype(dtype, [](auto t) { return KERNEL(distill_join_kernel<decltype(t)>); });
     return launch_units(kernel, p.rows, p, 0, stream);
 }
 
-int launch_distill_grad(DistillParams& p, int32_t dtype, const float* dloss, void* dlogits,
-                        int64_t dlogits_stride, void* stream) {
-    p.g = dloss;
-    p.out = dlogits;
-    p.ostride = dlogits_stride;
+int launch_distill_grad(DistillParams& p, int32_t dtype, bool join, void* stream) {
     const Cut cut = cut_gradient(p.vocab, element_bytes(dtype), kGradLoads * kBlock);
     p.splits = cut.splits;
     p.part_vecs = cut.part_vecs;
-    const void* kernel = by_dtype(
-        dtype, [](auto t) { return KERNEL(distill_grad_kernel<decltype(t)>); });
-    return launch_units(kernel, p.rows * p.splits, p, map_bytes({p.splits, p.part_vecs}),
-                        stream);
+    const void* kernel = by_dtype(dtype, [&](auto t) {
+        return join ? KERNEL(distill_grad_kernel<decltype(t), true>)
+                    : KERNEL(distill_grad_kernel<decltype(t), false>);
+    });
+    return launch_units(kernel, p.rows * p.splits, p, map_bytes(cut), stream);
 }
 
 }  // namespace
@@ -825,7 +907,10 @@ extern "C" int distill_topk_grad(const fsdpshard_logits* logits, const fsdpshard
     if (rows == 0) return FSDPSHARD_OK;
     DistillParams p = distill_params(logits, teacher);
     p.stats = const_cast<float*>(stats);       // read only by this kernel
-    return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
+    p.g = dloss;
+    p.out = dlogits;
+    p.ostride = dlogits_stride;
+    return launch_distill_grad(p, logits->dtype, false, stream);
 }
 
 extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
@@ -858,15 +943,20 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
     DistillParams p = distill_params(logits, teacher);
     p.loss = loss;
     p.stats = stats;
+    p.g = dloss;
+    p.out = dlogits;
+    p.ostride = dlogits_stride;
     const WholeKernel whole = whole_kernel<true>(p, logits->dtype, false);
-    if (whole.kernel) {
-        p.g = dloss;
-        p.out = dlogits;
-        p.ostride = dlogits_stride;
+    if (whole.kernel)
         return launch_units(whole.kernel, rows, p, whole.map_bytes, stream, whole.threads);
-    }
     // Otherwise two passes.  The second finds the logits in the last-level cache if that holds them.
+    // Few rows, unless in place: the parts' sets, which the gradient joins by itself.
+    if (rows <= kJoinRows && !in_place) {
+        rc = launch_parts(p, logits->dtype, false, workspace, stream);
+        if (rc != FSDPSHARD_OK) return rc;
+        return launch_distill_grad(p, logits->dtype, true, stream);
+    }
     rc = launch_distill(p, logits->dtype, xbytes > kLastLevelBytes, workspace, stream);
     if (rc != FSDPSHARD_OK) return rc;
-    return launch_distill_grad(p, logits->dtype, dloss, dlogits, dlogits_stride, stream);
+    return launch_distill_grad(p, logits->dtype, false, stream);
 }

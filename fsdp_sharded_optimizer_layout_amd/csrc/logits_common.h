@@ -653,7 +653,7 @@ const void* by_dtype(int32_t dtype, Get get) {
 // that), and where rows are few they are cut further, for about kWantUnits work-groups, but not
 // below kMinPartVecs vectors.
 constexpr int64_t kWantUnits = 1024;
-constexpr int64_t kMinPartVecs = 512;
+constexpr int64_t kMinPartVecs = 1024;
 
 struct Cut {
     int32_t splits, part_vecs;

@@ -182,6 +182,32 @@ def test_gradients_in_place():
             assert torch.equal(dev, apart) and torch.equal(loss, loss2) and torch.equal(st, st2)
 
 
+@pytest.mark.parametrize("dtype,rows,vocab", [("fp32", 3, 50021), ("bf16", 5, 131077),
+                                              ("fp16", 2, 262144), ("bf16", 520, 70001)])
+def test_gradients_in_place_of_long_rows(dtype, rows, vocab):
+    """Rows that take two passes: in place, the second must not need what it has overwritten."""
+    rng = _seed(rows, vocab, 31)
+    t, x64 = C.to_dtype(C.plain_rows(rng, rows, vocab), dtype)
+    f = dict(dtype=torch.float32, device="cuda")
+    g = np.linspace(0.5, 1.5, rows).astype(np.float32)
+    for tail in (False, True):
+        tid, tv = C.teacher_lists(rng, x64, 60, tail)
+        dev, whole = C.on_device(t, 3, 1)
+        before = whole.clone()
+        loss, st = torch.empty(rows, **f), torch.empty(rows, 4, **f)
+        say(f"in place, long rows {dtype} {rows} x {vocab} tail={tail}")
+        F.distill_topk_loss_grad(dev, torch.from_numpy(tid).cuda(), torch.from_numpy(tv).cuda(),
+                                 torch.from_numpy(g).cuda(), loss, st, dev, tail=tail)
+        some = list(range(min(rows, 6)))
+        C.check_distill(x64[some], tid[some], tv[some], 1.0, tail, loss.cpu().numpy()[some],
+                        st.cpu().numpy()[some], "in place")
+        C.check_distill_grad(x64[some], tid[some], tv[some], g[some], 1.0, tail, dtype,
+                             dev[some].double().cpu().numpy(), "in place")
+        between = torch.ones_like(whole, dtype=torch.bool)
+        between[1:1 + rows * (vocab + 3)].view(rows, vocab + 3)[:, :vocab] = False
+        assert torch.equal(whole[between].view(torch.uint8), before[between].view(torch.uint8))
+
+
 def _distill_all(dev, t, x64, tid, tv, g, scale, tail, dtype, what, opad=0, oshift=0):
     """Forward, backward and the joint call, each against the oracle."""
     rows = t.shape[0]
