@@ -418,7 +418,11 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     settle_list(p, a, list, mass, rest);
     list_peak(a, list);
 
-    // The tokens outside the list.  In registers, only they stay: the others become -inf.
+    // The tokens outside the list.  In registers, only they stay: the others become -inf, and so do
+    // the first and the last vector's elements that are not the row's.
+    const uint32_t first_mask = (1u << row.phase) - 1u;
+    const int end = row.phase + row.vocab - (row.nvec - 1) * E;    // of the last vector
+    const uint32_t last_mask = end < E ? ~0u << end : 0u;
     constexpr int U = kLoads<T>;
     Acc acc;
     if constexpr (Vecs == 0) {
@@ -447,9 +451,8 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
                 uint32_t mask = 0;
                 const int byte = map[v];
                 if (byte != 0) mask = slots.mask[byte - 1];
-                if (v == 0) mask |= (1u << row.phase) - 1u;
-                const int end = (row.phase + row.vocab) - v * E;   // elements before the row's end
-                if (v == row.nvec - 1 && end < E) mask |= ~0u << end;
+                if (v == 0) mask |= first_mask;
+                if (v == row.nvec - 1) mask |= last_mask;
                 if (mask != 0) mask_out<T>(raw[i0 + i], mask);
             }
 #pragma unroll
@@ -534,28 +537,34 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     if constexpr (Grad) {
         const OutRow<T> out(p.out, r, p.ostride, row);
         const float coef = sh.coef;
-        const auto write = [&](int v, float* y) {
-            put_listed(y, map[v], slots);
-            const bool partial = (v == 0 && row.first_partial()) ||
-                                 (v == row.nvec - 1 && row.last_partial());
-            if (partial) out.put_masked(row, v, y);
-            else out.put(v, y);
-        };
         if (sh.zero) {
             fill_part<Threads>(row, out, part, 0.0f);
         } else if (list_bad(list) || nan) {
             fill_part<Threads>(row, out, part, __builtin_nanf(""));
         } else {
-#pragma unroll
-            for (int i = 0; i < Vecs; ++i) {
-                const int v = tid + i * Threads;
-                if (v >= row.nvec) break;
-                float y[E];
-                unpack<T>(raw[i], y);
+            const auto gradient = [&](float* y, int v) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - mt));
-                write(v, y);
+                put_listed(y, map[v], slots);
+            };
+            int t = tid;                       // not the first pass's indices, kept in registers
+            asm volatile("" : "+v"(t));
+#pragma unroll
+            for (int i = 0; i < Vecs; ++i) {
+                const int v = t + i * Threads;
+                if (v < part.va || v >= part.vb) continue;
+                float y[E];
+                unpack<T>(raw[i], y);
+                gradient(y, v);
+                out.put(v, y);
                 __builtin_amdgcn_sched_barrier(0);
+            }
+            if ((part.first && tid == 0) || (part.last && tid == 1)) {
+                const int v = tid == 0 ? part.lo : part.hi - 1;
+                float y[E];
+                row.get_masked(v, y);          // not written yet, also in place
+                gradient(y, v);
+                out.put_masked(row, v, y);
             }
         }
     }
