@@ -394,7 +394,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
 #pragma unroll
     for (int i = 0; i < Vecs; ++i) {
         const int v = tid + i * Threads;
-        if (v < row.nvec) raw[i] = row.load(v);
+        if (v < row.nvec) raw[i] = Once ? row.load_once(v) : row.load(v);
         else raw[i] = u32x4{kMinusInfBits<T>, kMinusInfBits<T>, kMinusInfBits<T>,
                             kMinusInfBits<T>};
     }
@@ -817,8 +817,12 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     // whose loads, arithmetic and stores then wait for each other.  Measured with 64 places: 4096 x
     // 65536 bf16 227 us in registers, 88 + 181 in two passes; 2048 x 131072 278 and 92 + 176.
     if constexpr (Grad) {
-        if (vecs <= 16 * 256) return whole_form<256, 16, true>(dtype, vecs);
-        if (vecs <= 16 * 512) return whole_form<512, 16, true>(dtype, vecs);
+        if (vecs <= 16 * 256)
+            return once ? whole_form<256, 16, true, true>(dtype, vecs)
+                        : whole_form<256, 16, true>(dtype, vecs);
+        if (vecs <= 16 * 512)
+            return once ? whole_form<512, 16, true, true>(dtype, vecs)
+                        : whole_form<512, 16, true>(dtype, vecs);
     } else {
         if (vecs <= kMaxPartVecs)
             return once ? whole_form<kBlock, 0, false, true>(dtype, vecs)
@@ -955,7 +959,7 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
     p.g = dloss;
     p.out = dlogits;
     p.ostride = dlogits_stride;
-    const WholeKernel whole = whole_kernel<true>(p, logits->dtype, false);
+    const WholeKernel whole = whole_kernel<true>(p, logits->dtype, xbytes >= kOnceBytes);
     if (whole.kernel)
         return launch_units(whole.kernel, rows, p, whole.map_bytes, stream, whole.threads);
     // Otherwise two passes.  The second finds the logits in the last-level cache if that holds them.
