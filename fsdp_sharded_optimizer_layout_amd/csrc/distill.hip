@@ -57,11 +57,11 @@ struct List {
     int32_t seen[kSeen];           // tokens, by a hash; -1: free
 };
 
-// What the listed tokens of a vector do.
-template <typename T>
+// What the listed tokens of a vector do, in the bits of the type: one instruction for each 32 of them
+// where a vector has any (with 64 places, most loads of a wave meet one).
 struct Slots {
-    uint32_t mask[kTop];           // elements of the vector that are listed
-    float value[kTop][kElems<T>];  // their gradients
+    u32x4 listed[kTop];            // ones in the elements that are listed
+    u32x4 value[kTop];             // in those, their gradients
 };
 
 // Loads the list of row r.  Before the next step: a barrier.
@@ -96,12 +96,18 @@ __device__ __forceinline__ Place open_list(const DistillParams& p, int64_t r, co
 __device__ __forceinline__ bool list_some(const List& list) { return list.some[0] || list.some[1]; }
 __device__ __forceinline__ bool list_bad(const List& list) { return list.bad[0] || list.bad[1]; }
 
+// The bits of element e of a vector in its word.
+template <typename T>
+__device__ __forceinline__ uint32_t element_bits(int e) {
+    return sizeof(T) == 4 ? ~0u : e % 2 ? 0xFFFF0000u : 0xFFFFu;
+}
+
 // Enters a token into the map of vectors [lo, hi): map[v - lo] becomes 1 + the slot of its vector,
 // which is the number of the place that came first.  Whichever that is, the results are the same.
 // `map` and the slots' masks are clear; before the next step: a barrier.
 template <typename T>
 __device__ __forceinline__ void map_place(Place& a, const Row<T>& row, int lo, int hi,
-                                          uint8_t* map, Slots<T>& slots, List& list) {
+                                          uint8_t* map, Slots& slots, List& list) {
     constexpr int E = kElems<T>;
     const int at = a.id + row.phase, v = at / E - lo;
     if (!a.inside || v < 0 || v >= hi - lo) return;
@@ -123,8 +129,9 @@ __device__ __forceinline__ void map_place(Place& a, const Row<T>& row, int lo, i
         }
         seen = before;
     }
-    const uint32_t bit = 1u << (at % E);
-    a.leads = (atomicOr(&slots.mask[slot], bit) & bit) == 0;
+    const uint32_t bits = element_bits<T>(at % E);
+    uint32_t* listed = reinterpret_cast<uint32_t*>(&slots.listed[slot]) + at % E * 4 / E;
+    a.leads = (atomicOr(listed, bits) & bits) == 0;
     if (!a.leads) list.repeats = 1;
 }
 
@@ -260,15 +267,15 @@ __device__ __forceinline__ void list_loss(const Place& a, double logp, List& lis
 template <typename T>
 __device__ __forceinline__ void set_value(const DistillParams& p, const Place& a, double logp,
                                           double gc, double mass, const Row<T>& row, int lo,
-                                          const uint8_t* map, Slots<T>& slots, const List& list) {
+                                          const uint8_t* map, Slots& slots, const List& list) {
     if (!a.leads || !a.inside) return;
     double q = a.q;
     if (list.repeats)
         for (int i = threadIdx.x + 1; i < p.k; ++i)
             if (list.id[i] == a.id) q += list.q[i];
     const int at = a.id + row.phase;
-    slots.value[map[at / kElems<T> - lo] - 1][at % kElems<T>] =
-        static_cast<float>(gc * (mass * exp(logp) - q));
+    reinterpret_cast<T*>(&slots.value[map[at / kElems<T> - lo] - 1])[at % kElems<T>] =
+        narrow<T>(static_cast<float>(gc * (mass * exp(logp) - q)));
 }
 
 // Any other token's is coef exp(c (x - mt)).
@@ -299,24 +306,29 @@ __device__ __forceinline__ void write_row(const DistillParams& p, int64_t r, con
     }
 }
 
-// Elements of vector v that are listed become -inf.
+// The listed elements of a vector become -inf.
 template <typename T>
-__device__ __forceinline__ void drop_listed(float* y, int byte, const Slots<T>& slots) {
+__device__ __forceinline__ void drop_listed(u32x4& raw, int byte, const Slots& slots) {
+    if (byte != 0) mask_out<T>(raw, slots.listed[byte - 1]);
+}
+
+// Of a partial vector, as floats.
+template <typename T>
+__device__ __forceinline__ void drop_listed(float* y, int byte, const Slots& slots) {
     if (byte == 0) return;
-    const uint32_t mask = slots.mask[byte - 1];
+    const uint32_t* listed = reinterpret_cast<const uint32_t*>(&slots.listed[byte - 1]);
 #pragma unroll
     for (int e = 0; e < kElems<T>; ++e)
-        if ((mask >> e) & 1u) y[e] = -kInf;
+        if (listed[e * 4 / kElems<T>] & element_bits<T>(e)) y[e] = -kInf;
 }
 
 // They get their values.
-template <typename T>
-__device__ __forceinline__ void put_listed(float* y, int byte, const Slots<T>& slots) {
-    if (byte == 0) return;
-    const uint32_t mask = slots.mask[byte - 1];
-#pragma unroll
-    for (int e = 0; e < kElems<T>; ++e)
-        if ((mask >> e) & 1u) y[e] = slots.value[byte - 1][e];
+__device__ __forceinline__ u32x4 put_listed(u32x4 out, int byte, const Slots& slots) {
+    if (byte != 0) {
+        const u32x4 listed = slots.listed[byte - 1];
+        out = (out & ~listed) | (slots.value[byte - 1] & listed);
+    }
+    return out;
 }
 
 __device__ __forceinline__ void clear_map(uint8_t* map, int bytes, int threads) {
@@ -334,30 +346,6 @@ __device__ __forceinline__ void clear_map(uint8_t* map, int bytes, int threads) 
 //              hide each other's work on the lists.
 // A launch has a work-group for each row and no loop over rows: in a loop the compiler would keep
 // the constants of the float64 functions in registers, twice as many as the rest needs.
-
-template <typename T>
-constexpr uint32_t kMinusInfBits = 0;
-template <>
-constexpr uint32_t kMinusInfBits<Bf16> = 0xFF80FF80u;
-template <>
-constexpr uint32_t kMinusInfBits<Fp16> = 0xFC00FC00u;
-template <>
-constexpr uint32_t kMinusInfBits<float> = 0xFF800000u;
-
-// Elements of `raw` whose bit is set become -inf.
-template <typename T>
-__device__ __forceinline__ void mask_out(u32x4& raw, uint32_t mask) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t drop;
-        if constexpr (sizeof(T) == 4)
-            drop = (mask >> i) & 1u ? ~0u : 0u;
-        else
-            drop = ((mask >> (2 * i)) & 1u ? 0xFFFFu : 0u) |
-                   ((mask >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
-        raw[i] = (raw[i] & ~drop) | (kMinusInfBits<T> & drop);
-    }
-}
 
 // Keeps the compiler from holding the floats of an earlier unpacking of the row (two registers for
 // each one of 16-bit elements) instead of unpacking it again.
@@ -378,7 +366,7 @@ template <typename T, int Threads, int Vecs, bool Grad, bool Once>
 __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kernel(DistillParams p) {
     constexpr int E = kElems<T>, W = Threads / kWave;
     extern __shared__ __align__(16) uint8_t map[];
-    __shared__ Slots<T> slots;
+    __shared__ Slots slots;
     __shared__ List list;
     __shared__ WholeScratch sh;
     __shared__ BlockScratch bs;
@@ -399,7 +387,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
                             kMinusInfBits<T>};
     }
     clear_map(map, Vecs > 0 ? Threads * Vecs : row.nvec, Threads);
-    if (tid < kTop) slots.mask[tid] = 0;
+    if (tid < kTop) slots.listed[tid] = u32x4{0, 0, 0, 0};
     Place a = open_list(p, r, row, list);
     __syncthreads();
     if (!list_some(list)) {
@@ -420,40 +408,36 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
 
     // The tokens outside the list.  In registers, only they stay: the others become -inf, and so do
     // the first and the last vector's elements that are not the row's.
-    const uint32_t first_mask = (1u << row.phase) - 1u;
     const int end = row.phase + row.vocab - (row.nvec - 1) * E;    // of the last vector
-    const uint32_t last_mask = end < E ? ~0u << end : 0u;
-    constexpr int U = kLoads<T>;
+    u32x4 first_mask = {0, 0, 0, 0}, last_mask = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e < row.phase) first_mask[e * 4 / E] |= element_bits<T>(e);
+        if (e >= end) last_mask[e * 4 / E] |= element_bits<T>(e);
+    }
     Acc acc;
     if constexpr (Vecs == 0) {
         stream<Threads, Once>(
             row, part,
-            [&](float* y, int b) {
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int v = part.va + (b * U + i) * Threads + tid;
-                    if (v < part.vb) drop_listed(y + i * E, map[v], slots);
-                }
+            [&](u32x4& w, int v) { drop_listed<T>(w, v < part.vb ? map[v] : 0, slots); },
+            [&](float* y, int) {
                 add_batch<kBatch, false>(acc, y, max_of<kBatch>(y), c2);
             },
             [&](float* y, int v) {
-                drop_listed(y, map[v], slots);
+                drop_listed<T>(y, map[v], slots);
                 add_batch<E, false>(acc, y, max_of<E>(y), c2);
             });
     } else {
-        constexpr int Step = Vecs < U ? Vecs : U;
+        constexpr int Step = Vecs < kLoads<T> ? Vecs : kLoads<T>;
 #pragma unroll
         for (int i0 = 0; i0 < Vecs; i0 += Step) {
             float y[Step * E];
 #pragma unroll
             for (int i = 0; i < Step; ++i) {
                 const int v = tid + (i0 + i) * Threads;
-                uint32_t mask = 0;
-                const int byte = map[v];
-                if (byte != 0) mask = slots.mask[byte - 1];
-                if (v == 0) mask |= first_mask;
-                if (v == row.nvec - 1) mask |= last_mask;
-                if (mask != 0) mask_out<T>(raw[i0 + i], mask);
+                if (v == 0) mask_out<T>(raw[i0 + i], first_mask);
+                if (v == row.nvec - 1) mask_out<T>(raw[i0 + i], last_mask);
+                drop_listed<T>(raw[i0 + i], map[v], slots);
             }
 #pragma unroll
             for (int i = 0; i < Step; ++i) {
@@ -496,11 +480,11 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     rt += static_cast<float>(ones) - 1.0f;
     if (ones == 1 && rt < kPeaked) {
         // The sum of the thread that saw the maximum again, without the maximum.
-        float s = is_top ? 0.0f : acc.s;
+        float2 s = make_float2(is_top ? 0.0f : acc.s, 0.0f);
         if constexpr (Vecs == 0) {
             vectors_of<Threads>(row, part, sh.owner, [&](float* y, int v) {
-                drop_listed(y, map[v], slots);
-                s += rest_sum<E>(y, mt, c2);
+                drop_listed<T>(y, map[v], slots);
+                add_rest<E, false>(s, y, mt, c2);
             });
         } else {
             if (is_top) {
@@ -508,12 +492,12 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
                 for (int i = 0; i < Vecs; ++i) {
                     float y[E];
                     unpack<T>(raw[i], y);
-                    s += rest_sum<E>(y, mt, c2);
+                    add_rest<E, false>(s, y, mt, c2);
                 }
             }
             forget_floats(raw);
         }
-        rt = block_sum(s, bs, 0, W);
+        rt = block_sum(s.x, bs, 0, W);
     }
     const bool nan = rt != rt || list_nan;
     if (rt == -1.0f) rest = 0.0;                // nothing unmasked outside the list
@@ -542,29 +526,41 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
         } else if (list_bad(list) || nan) {
             fill_part<Threads>(row, out, part, __builtin_nanf(""));
         } else {
+            // 2^u by one fused multiply-add, as in add_batch; far from 0, the row is read again.
+            const float base = c2 * mt, delta = __builtin_fmaf(c2, mt, -base);
+            const float fused_coef = coef * exp2_fast(-delta);
             const auto gradient = [&](float* y, int v) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - mt));
-                put_listed(y, map[v], slots);
+                return put_listed(pack<T>(y), map[v], slots);
             };
-            int t = tid;                       // not the first pass's indices, kept in registers
-            asm volatile("" : "+v"(t));
+            if (fabsf(base) < 0x1p20f) {
+                int t = tid;                   // not the first pass's indices, kept in registers
+                asm volatile("" : "+v"(t));
 #pragma unroll
-            for (int i = 0; i < Vecs; ++i) {
-                const int v = t + i * Threads;
-                if (v < part.va || v >= part.vb) continue;
-                float y[E];
-                unpack<T>(raw[i], y);
-                gradient(y, v);
-                out.put(v, y);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < Vecs; ++i) {
+                    const int v = t + i * Threads;
+                    if (v < part.va || v >= part.vb) continue;
+                    float y[E];
+                    unpack<T>(raw[i], y);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        y[e] = fused_coef * exp2_fast(__builtin_fmaf(c2, y[e], -base));
+                    out.put(v, put_listed(pack<T>(y), map[v], slots));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+                for (int v = part.va + tid; v < part.vb; v += Threads) {
+                    float y[E];
+                    unpack<T>(row.load(v), y);
+                    out.put(v, gradient(y, v));
+                }
             }
             if ((part.first && tid == 0) || (part.last && tid == 1)) {
                 const int v = tid == 0 ? part.lo : part.hi - 1;
                 float y[E];
                 row.get_masked(v, y);          // not written yet, also in place
-                gradient(y, v);
-                out.put_masked(row, v, y);
+                out.put_masked(row, v, gradient(y, v));
             }
         }
     }
@@ -576,10 +572,10 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
 // The set of a part's tokens outside the list.
 template <typename T, bool Once>
 __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
-    constexpr int E = kElems<T>, U = kLoads<T>;
+    constexpr int E = kElems<T>;
     extern __shared__ __align__(16) uint8_t map[];
     __shared__ BlockScratch bs;
-    __shared__ Slots<T> slots;
+    __shared__ Slots slots;
     __shared__ List list;
     const float c2 = p.c * kLog2e;
     const int tid = threadIdx.x;
@@ -590,32 +586,28 @@ __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
     if (tid < p.k) a.id = p.ids[r * p.tstride + tid];
     a.inside = a.id >= 0 && a.id < p.vocab;
     clear_map(map, part.hi - part.lo, kBlock);
-    if (tid < kTop) slots.mask[tid] = 0;
+    if (tid < kTop) slots.listed[tid] = u32x4{0, 0, 0, 0};
     if (!__syncthreads_or(a.id >= 0)) return;        // no list: the row's results are zeros
     if (tid < kTop) map_place(a, row, part.lo, part.hi, map, slots, list);
     __syncthreads();
     Acc acc;
     stream<kBlock, Once>(
         row, part,
-        [&](float* y, int b) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int v = part.va + (b * U + i) * kBlock + tid;
-                if (v < part.vb) drop_listed(y + i * E, map[v - part.lo], slots);
-            }
+        [&](u32x4& w, int v) { drop_listed<T>(w, v < part.vb ? map[v - part.lo] : 0, slots); },
+        [&](float* y, int) {
             add_batch<kBatch, false>(acc, y, max_of<kBatch>(y), c2);
         },
         [&](float* y, int v) {
-            drop_listed(y, map[v - part.lo], slots);
+            drop_listed<T>(y, map[v - part.lo], slots);
             add_batch<E, false>(acc, y, max_of<E>(y), c2);
         });
     const Set set = join_threads<false, kBlock / kWave>(acc, c2, bs, [&](int j, float m) {
-        float s = 0.0f;
+        float2 rest = make_float2(0.0f, 0.0f);
         vectors_of<kBlock>(row, part, j, [&](float* y, int v) {
-            drop_listed(y, map[v - part.lo], slots);
-            s += rest_sum<E>(y, m, c2);
+            drop_listed<T>(y, map[v - part.lo], slots);
+            add_rest<E, false>(rest, y, m, c2);
         });
-        return s;
+        return rest;
     });
     if (tid == 0) p.part_sets[unit] = make_float2(set.m, set.r);
 }
@@ -669,7 +661,7 @@ template <typename T, bool Join>
 __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     constexpr int E = kElems<T>;
     extern __shared__ __align__(16) uint8_t map[];
-    __shared__ Slots<T> slots;
+    __shared__ Slots slots;
     __shared__ List list;
     __shared__ GradScratch sh;
     const float c2 = p.c * kLog2e;
@@ -695,7 +687,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     load_part(row, part, raw);
     Place a = open_list(p, r, row, list);
     clear_map(map, part.hi - part.lo, kBlock);
-    if (tid < kTop) slots.mask[tid] = 0;
+    if (tid < kTop) slots.listed[tid] = u32x4{0, 0, 0, 0};
     Set set{};
     if constexpr (Join) {
         clear_seen(list);
@@ -763,7 +755,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     write_part(row, out, part, raw, [&](float* y, int v) {
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = coef * exp2_fast(c2 * (y[e] - ref));
-        put_listed(y, map[v - part.lo], slots);
+        return put_listed(pack<T>(y), map[v - part.lo], slots);
     });
 }
 

@@ -273,15 +273,18 @@ __device__ __forceinline__ void rebase(Acc& a, float m, float c2) {
     a.m = m;
 }
 
-// One batch, with its maximum.  Its terms are added up by themselves first: fewer additions at the size of the
-// whole sum.
+// One batch, with its maximum.  Its terms are added up by themselves first: fewer additions at the
+// size of the whole sum.  The forward passes are bound by these instructions, so 2^u takes one fused
+// multiply-add where it can: with b the rounded c2 m, the batch adds up 2^(c2 x - b), which is
+// 2^delta times its terms, delta = c2 m - b, at most 2^-5 while |c2 m| < 2^20.  Beyond that (and
+// while only masked elements were seen) the difference is taken first.  Measured on 8192 x 32000
+// bf16: 87 us with the difference throughout.
 template <int N, bool Entropy>
 __device__ __forceinline__ void add_batch(Acc& a, const float* x, float top, float c2) {
     rebase<Entropy>(a, fmaxf(a.m, top), c2);
+    const float b = c2 * a.m;
     float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float u0 = c2 * (x[i] - a.m), u1 = c2 * (x[i + 1] - a.m);
+    const auto add = [&](float u0, float u1) {
         const float e0 = exp2_fast(u0), e1 = exp2_fast(u1);
         s0 += e0;
         s1 += e1;
@@ -289,9 +292,21 @@ __device__ __forceinline__ void add_batch(Acc& a, const float* x, float top, flo
             t0 = __builtin_fmaf(e0, fmaxf(u0, kNegligible), t0);
             t1 = __builtin_fmaf(e1, fmaxf(u1, kNegligible), t1);
         }
+    };
+    if (__any(!(fabsf(b) < 0x1p20f))) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) add(c2 * (x[i] - a.m), c2 * (x[i + 1] - a.m));
+        a.s += s0 + s1;
+        if (Entropy) a.t += t0 + t1;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            add(__builtin_fmaf(c2, x[i], -b), __builtin_fmaf(c2, x[i + 1], -b));
+        const float delta = __builtin_fmaf(c2, a.m, -b), scale = exp2_fast(-delta);
+        a.s = __builtin_fmaf(s0 + s1, scale, a.s);
+        if (Entropy)
+            a.t = __builtin_fmaf(__builtin_fmaf(-delta, s0 + s1, t0 + t1), scale, a.t);
     }
-    a.s += s0 + s1;
-    if (Entropy) a.t += t0 + t1;
 }
 
 // What is known of a set of elements: maximum m, r = sum 2^u - 1 (the maximum's own term left
@@ -317,8 +332,8 @@ __device__ __forceinline__ float block_sum(float x, BlockScratch& sh, int slot, 
     return total;
 }
 
-// Joins the threads' accumulators.  rest_of(j) is called by all threads and returns this thread's
-// share of sum 2^u over the elements of thread j other than its maximum.
+// Joins the threads' accumulators.  rest_of(j, m) is called by all threads and returns this thread's
+// share of sum 2^u, and of sum 2^u u, over the elements of thread j other than its maximum m.
 template <bool Entropy, int Waves, typename RestOf>
 __device__ Set join_threads(Acc a, float c2, BlockScratch& sh, RestOf rest_of) {
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -350,8 +365,11 @@ __device__ Set join_threads(Acc a, float c2, BlockScratch& sh, RestOf rest_of) {
         n += static_cast<float>(sh.d[0][i]);
     }
     r += n - 1.0f;
-    if (n == 1.0f && r < kPeaked)
-        r = block_sum((top ? 0.0f : a.s) + rest_of(sh.owner, m), sh, 1, Waves);
+    if (n == 1.0f && r < kPeaked) {
+        const float2 rest = rest_of(sh.owner, m);
+        r = block_sum((top ? 0.0f : a.s) + rest.x, sh, 1, Waves);
+        if (Entropy) t = block_sum((top ? 0.0f : a.t) + rest.y, sh, 2, Waves);
+    }
     return Set{m, r, t};
 }
 
@@ -395,11 +413,27 @@ __device__ __forceinline__ float log_p(float x, float m, float L, float c) {
     return x == -kInf ? (m != m ? m : -kInf) : c * (x - m) - L;
 }
 
-// Streams a part: calls batch(x, b) with kBatch floats of this thread's b-th batch of whole
-// vectors (-inf past the end), and edge(x, v) with the kElems floats of a partial vector v.  Once: the
-// matrix is too large to be found in a cache again, and is loaded without keeping it there.
-template <int Threads, bool Once, typename T, typename Batch, typename Edge>
-__device__ __forceinline__ void stream(const Row<T>& row, const Part& part, Batch batch,
+// Elements of `raw` where `drop` has ones become -inf.
+template <typename T>
+constexpr uint32_t kMinusInfBits = 0;
+template <>
+constexpr uint32_t kMinusInfBits<Bf16> = 0xFF80FF80u;
+template <>
+constexpr uint32_t kMinusInfBits<Fp16> = 0xFC00FC00u;
+template <>
+constexpr uint32_t kMinusInfBits<float> = 0xFF800000u;
+
+template <typename T>
+__device__ __forceinline__ void mask_out(u32x4& raw, u32x4 drop) {
+    raw = (raw & ~drop) | (drop & kMinusInfBits<T>);
+}
+
+// Streams a part: calls fix(raw, v) for each whole vector (it may mask elements out), batch(x, b)
+// with kBatch floats of this thread's b-th batch of whole vectors (-inf past the end), and edge(x, v)
+// with the kElems floats of a partial vector v.  Once: the matrix is too large to be found in a cache
+// again, and is loaded without keeping it there.
+template <int Threads, bool Once, typename T, typename Fix, typename Batch, typename Edge>
+__device__ __forceinline__ void stream(const Row<T>& row, const Part& part, Fix fix, Batch batch,
                                        Edge edge) {
     constexpr int E = kElems<T>, U = kLoads<T>;
     const int tid = threadIdx.x;
@@ -412,16 +446,18 @@ __device__ __forceinline__ void stream(const Row<T>& row, const Part& part, Batc
             const int v = v0 + q * Threads + tid, at = whole || v < part.vb ? v : part.va;
             raw[q] = Once ? row.load_once(at) : row.load(at);
         }
-        float x[kBatch];
-#pragma unroll
-        for (int q = 0; q < U; ++q) unpack<T>(raw[q], x + q * E);
         if (!whole) {
+            asm volatile("");              // a branch: the selects would cost every batch
 #pragma unroll
             for (int q = 0; q < U; ++q)
-                if (v0 + q * Threads + tid >= part.vb) {
+                if (v0 + q * Threads + tid >= part.vb)
+                    mask_out<T>(raw[q], u32x4{~0u, ~0u, ~0u, ~0u});
+        }
+        float x[kBatch];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[q * E + e] = -kInf;
-                }
+        for (int q = 0; q < U; ++q) {
+            fix(raw[q], v0 + q * Threads + tid);
+            unpack<T>(raw[q], x + q * E);
         }
         batch(x, b);
     }
@@ -449,17 +485,35 @@ __device__ __forceinline__ void vectors_of(const Row<T>& row, const Part& part, 
     }
 }
 
-template <int N>
-__device__ __forceinline__ float rest_sum(const float* x, float m, float c2) {
-    float s = 0.0f;
+// Adds the terms of a vector that are not the maximum's.
+template <int N, bool Entropy>
+__device__ __forceinline__ void add_rest(float2& rest, const float* x, float m, float c2) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) s += x[e] == m ? 0.0f : exp2_fast(c2 * (x[e] - m));
-    return s;
+    for (int e = 0; e < N; ++e) {
+        const float u = c2 * (x[e] - m), p = x[e] == m ? 0.0f : exp2_fast(u);
+        rest.x += p;
+        if (Entropy) rest.y = __builtin_fmaf(p, fmaxf(u, kNegligible), rest.y);
+    }
 }
 
 // ------------------------------------------------------------------------------------------------
 // Gradients.  Element-wise streams: a work-group writes one part of a row, each vector from one
 // exponential an element.
+
+// A vector of the type from floats, each rounded once.
+template <typename T>
+__device__ __forceinline__ u32x4 pack(const float* x) {
+    u32x4 out;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4)
+            out[i] = __float_as_uint(x[i]);
+        else
+            out[i] = narrow<T>(x[2 * i]).bits |
+                     (static_cast<uint32_t>(narrow<T>(x[2 * i + 1]).bits) << 16);
+    }
+    return out;
+}
 
 // The vectors of a gradient's row, which may start at another phase of 16 bytes than the logits'.
 template <typename T>
@@ -471,17 +525,7 @@ struct OutRow {
         base = static_cast<char*>(data) + (r * stride - row.phase) * static_cast<int64_t>(sizeof(T));
         aligned = (reinterpret_cast<uintptr_t>(base) & 15u) == 0;
     }
-    __device__ __forceinline__ void put(int v, const float* x) const {
-        u32x4 out;
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out[i] = __float_as_uint(x[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                out[i] = narrow<T>(x[2 * i]).bits |
-                         (static_cast<uint32_t>(narrow<T>(x[2 * i + 1]).bits) << 16);
-        }
+    __device__ __forceinline__ void put(int v, u32x4 out) const {
         char* at = base + static_cast<int64_t>(v) * 16;
         if (aligned) {
             __builtin_nontemporal_store(out, reinterpret_cast<u32x4*>(at));
@@ -492,18 +536,22 @@ struct OutRow {
         }
     }
     // The elements of vector v that are the row's.
-    __device__ __forceinline__ void put_masked(const Row<T>& row, int v, const float* x) const {
-        T* at = reinterpret_cast<T*>(base + static_cast<int64_t>(v) * 16);
+    __device__ __forceinline__ void put_masked(const Row<T>& row, int v, u32x4 out) const {
+        using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+        Bits* at = reinterpret_cast<Bits*>(base + static_cast<int64_t>(v) * 16);
+        constexpr int PerWord = 4 / static_cast<int>(sizeof(T));
 #pragma unroll
         for (int e = 0; e < kElems<T>; ++e) {
             const int i = v * kElems<T> + e - row.phase;
-            if (i >= 0 && i < row.vocab) at[e] = narrow<T>(x[e]);
+            const uint32_t word = out[e / PerWord];
+            if (i >= 0 && i < row.vocab)
+                at[e] = static_cast<Bits>(word >> (e % PerWord * 16));
         }
     }
 };
 
 // A gradient's part is one batch of at most Loads vectors a thread: load_part reads it (edges aside),
-// write_part turns each vector's floats into the gradient's with f(x, v) and stores them.  Short
+// write_part stores what f(x, v) makes of each vector's floats.  Short
 // parts, because a work-group that loops waits for its loads again after each batch of stores.
 template <int Loads, typename T>
 __device__ __forceinline__ void load_part(const Row<T>& row, const Part& part,
@@ -525,15 +573,13 @@ __device__ __forceinline__ void write_part(const Row<T>& row, const OutRow<T>& o
         if (v >= part.vb) break;
         float x[kElems<T>];
         unpack<T>(raw[q], x);
-        f(x, v);
-        out.put(v, x);
+        out.put(v, f(x, v));
     }
     if ((part.first && tid == 0) || (part.last && tid == 1)) {
         const int v = tid == 0 ? part.lo : part.hi - 1;
         float x[kElems<T>];
         row.get_masked(v, x);
-        f(x, v);
-        out.put_masked(row, v, x);
+        out.put_masked(row, v, f(x, v));
     }
 }
 
@@ -544,9 +590,10 @@ __device__ __forceinline__ void fill_part(const Row<T>& row, const OutRow<T>& ou
     float x[kElems<T>];
 #pragma unroll
     for (int e = 0; e < kElems<T>; ++e) x[e] = value;
-    for (int v = part.va + static_cast<int>(threadIdx.x); v < part.vb; v += Threads) out.put(v, x);
+    const u32x4 out_vec = pack<T>(x);
+    for (int v = part.va + static_cast<int>(threadIdx.x); v < part.vb; v += Threads) out.put(v, out_vec);
     if ((part.first && threadIdx.x == 0) || (part.last && threadIdx.x == 1))
-        out.put_masked(row, threadIdx.x == 0 ? part.lo : part.hi - 1, x);
+        out.put_masked(row, threadIdx.x == 0 ? part.lo : part.hi - 1, out_vec);
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -325,7 +325,7 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
     }
     Acc a;
     stream<Threads, Once>(
-        row, part,
+        row, part, [](u32x4&, int) {},
         [&](const float* x, int b) {
             float top;
             if constexpr (Top) {
@@ -342,10 +342,11 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
         [&](const float* x, int) { add_batch<E, true>(a, x, max_of<E>(x), c2); });
     const Set set = join_threads<true, Threads / kWave>(
         a, c2, bs, [&](int j, float m) {
-            float s = 0.0f;
-            vectors_of<Threads>(row, part, j,
-                                [&](const float* x, int) { s += rest_sum<E>(x, m, c2); });
-            return s;
+            float2 rest = make_float2(0.0f, 0.0f);
+            vectors_of<Threads>(row, part, j, [&](const float* x, int) {
+                add_rest<E, true>(rest, x, m, c2);
+            });
+            return rest;
         });
     const RowStats st = finish(set);
     if (p.splits == 1) {
@@ -556,6 +557,7 @@ __global__ __launch_bounds__(kBlock) void logprobs_grad_kernel(LogprobGradParams
             for (int i = 0; i < E; ++i)
                 x[i] = -gc * exp2_fast(__builtin_fmaf(c2, x[i] - m, -L2));
             if (v == token_vec) set_token(x);
+            return pack<T>(x);
         });
     } else {
         // -p (g + h (log p + H)) with log p in units of log 2; the clamp keeps 0 times -inf
@@ -568,6 +570,7 @@ __global__ __launch_bounds__(kBlock) void logprobs_grad_kernel(LogprobGradParams
                 x[i] = -exp2_fast(u) * __builtin_fmaf(h2, fmaxf(u, kNegligible), base);
             }
             if (v == token_vec) set_token(x);
+            return pack<T>(x);
         });
     }
 }
