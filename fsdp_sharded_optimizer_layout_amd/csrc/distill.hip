@@ -33,7 +33,7 @@ constexpr int kTop = FSDPSHARD_MAX_TOP;
 constexpr int kListWaves = kTop / kWave;
 
 // ------------------------------------------------------------------------------------------------
-// The list.  Thread j < kTop has place j.  q, log q and their sums are float64: 1 - sum q and p - q
+// The list.  Thread j has place j.  q, log q and their sums are float64: 1 - sum q and p - q
 // are small differences.
 
 struct Place {
@@ -64,6 +64,11 @@ struct Slots {
     u32x4 value[kTop];             // in those, their gradients
 };
 
+// The threads that work on a list: the waves that have places.
+__device__ __forceinline__ int list_threads(const DistillParams& p) {
+    return p.k <= kWave ? kWave : kTop;
+}
+
 // Loads the list of row r.  Before the next step: a barrier.
 template <typename T>
 __device__ __forceinline__ Place open_list(const DistillParams& p, int64_t r, const Row<T>& row,
@@ -76,8 +81,15 @@ __device__ __forceinline__ Place open_list(const DistillParams& p, int64_t r, co
     }
     a.valid = a.id >= 0;
     a.inside = a.valid && a.id < p.vocab;
-    if (j == 0) list.repeats = 0;
-    if (j < kTop) {
+    if (j == 0) {
+        list.repeats = 0;
+        if (p.k <= kWave) {                       // what an absent second wave adds
+            list.value_max[1] = list.x_max[1] = -kInf;
+            list.some[1] = list.bad[1] = list.ones[1] = 0;
+            list.q_sum[1] = list.term_sum[1] = list.loss[1] = 0.0;
+        }
+    }
+    if (j < list_threads(p)) {
         if (a.inside) a.x = row.at(a.id);
         list.id[j] = a.valid ? a.id : -1;
         const float top = wave_max(a.valid ? a.value : -kInf);
@@ -168,7 +180,7 @@ __device__ __forceinline__ bool first_place(const DistillParams& p, const Place&
 // step: a barrier.
 __device__ __forceinline__ void weigh_list(const DistillParams& p, Place& a, List& list) {
     const int j = threadIdx.x;
-    if (j >= kTop) return;
+    if (j >= list_threads(p)) return;
     const float top = fmaxf(list.value_max[0], list.value_max[1]);
     if (a.valid) {
         a.logq = a.value;
@@ -189,19 +201,19 @@ __device__ __forceinline__ void settle_list(const DistillParams& p, Place& a, Li
     if (p.tail) {
         rest = fmax(0.0, 1.0 - mass);
     } else if (mass > 0.0) {
-        if (threadIdx.x < kTop) {
+        if (static_cast<int>(threadIdx.x) < list_threads(p)) {
             a.q /= mass;
             a.logq -= log(mass);
         }
         mass = 1.0;
     }
-    if (threadIdx.x < kTop) list.q[threadIdx.x] = a.q;
+    if (static_cast<int>(threadIdx.x) < list_threads(p)) list.q[threadIdx.x] = a.q;
 }
 
 // The maximum of the listed logits, by wave (NaN: a NaN or +inf among them).
-__device__ __forceinline__ void list_peak(const Place& a, List& list) {
+__device__ __forceinline__ void list_peak(const DistillParams& p, const Place& a, List& list) {
     const int j = threadIdx.x;
-    if (j >= kTop) return;
+    if (j >= list_threads(p)) return;
     const float top = wave_max(a.leads ? a.x : -kInf);
     const bool odd = __ballot(a.leads && !(a.x < kInf)) != 0;
     if (j % kWave == 0) list.x_max[j / kWave] = odd ? __builtin_nanf("") : top;
@@ -211,7 +223,7 @@ __device__ __forceinline__ void list_peak(const Place& a, List& list) {
 __device__ __forceinline__ void list_terms(const DistillParams& p, const Place& a, float m,
                                            List& list) {
     const int j = threadIdx.x;
-    if (j >= kTop) return;
+    if (j >= list_threads(p)) return;
     const float x = a.leads ? a.x : -kInf;
     double e = 0.0;
     if (x > -kInf && x != m) e = exp(static_cast<double>(p.c) * (static_cast<double>(x) - m));
@@ -396,7 +408,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
             fill_part<Threads>(row, OutRow<T>(p.out, r, p.ostride, row), part, 0.0f);
         return;
     }
-    if (tid < kTop) {
+    if (tid < list_threads(p)) {
         map_place(a, row, 0, row.nvec, map, slots, list);
         weigh_list(p, a, list);
     }
@@ -404,7 +416,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     if (list.repeats) a.leads = a.mapped && first_place(p, a, list);
     double mass, rest;
     settle_list(p, a, list, mass, rest);
-    list_peak(a, list);
+    list_peak(p, a, list);
 
     // The tokens outside the list.  In registers, only they stay: the others become -inf, and so do
     // the first and the last vector's elements that are not the row's.
@@ -503,7 +515,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     if (rt == -1.0f) rest = 0.0;                // nothing unmasked outside the list
     mass += rest;
     RowResult d{};
-    if (tid < kTop) {
+    if (tid < list_threads(p)) {
         d = solve_row(p, mt, rt, list_max, list);
         const double logp = list_logp(p, a, d);
         list_loss(a, logp, list);
@@ -588,7 +600,7 @@ __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
     clear_map(map, part.hi - part.lo, kBlock);
     if (tid < kTop) slots.listed[tid] = u32x4{0, 0, 0, 0};
     if (!__syncthreads_or(a.id >= 0)) return;        // no list: the row's results are zeros
-    if (tid < kTop) map_place(a, row, part.lo, part.hi, map, slots, list);
+    if (tid < list_threads(p)) map_place(a, row, part.lo, part.hi, map, slots, list);
     __syncthreads();
     Acc acc;
     stream<kBlock, Once>(
@@ -626,7 +638,7 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
     __syncthreads();
     a.leads = enters_first(a, list);
     weigh_list(p, a, list);
-    list_peak(a, list);
+    list_peak(p, a, list);
     __syncthreads();
     if (list.repeats) a.leads = a.inside && first_place(p, a, list);
     double mass, rest;
@@ -636,7 +648,7 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
     list_terms(p, a, fmaxf(list_max, set.m), list);
     __syncthreads();
     RowResult d{};
-    if (threadIdx.x < kTop) {
+    if (static_cast<int>(threadIdx.x) < list_threads(p)) {
         d = solve_row(p, set.m, set.r, list_max, list);
         list_loss(a, list_logp(p, a, d), list);
     }
@@ -701,14 +713,14 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
         fill_part<kBlock>(row, out, part, 0.0f);
         return;
     }
-    if (tid < kTop) {
+    if (tid < list_threads(p)) {
         map_place(a, row, part.lo, part.hi, map, slots, list);
         weigh_list(p, a, list);
     }
     bool first = false;                               // of the row's places of this token
     if constexpr (Join) {
         first = a.leads = enters_first(a, list);
-        list_peak(a, list);
+        list_peak(p, a, list);
     }
     __syncthreads();
     if (list.repeats) {
@@ -724,7 +736,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
         nan = set.r != set.r || list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
         list_terms(p, a, fmaxf(list_max, set.m), list);
         __syncthreads();                              // the terms, and the places' q
-        if (tid < kTop) d = solve_row(p, set.m, set.r, list_max, list);
+        if (tid < list_threads(p)) d = solve_row(p, set.m, set.r, list_max, list);
         if (set.r == -1.0f) rest = 0.0;
     } else {
         d = known;
@@ -733,7 +745,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
         __syncthreads();                              // the places' q
     }
     mass += rest;
-    if (tid < kTop) {
+    if (tid < list_threads(p)) {
         const double gc = static_cast<double>(g) * p.c, logp = list_logp(p, a, d);
         if constexpr (Join) list_loss(a, logp, list);
         if (Join || list.repeats) a.leads = a.mapped && first;
