@@ -121,8 +121,9 @@ template <typename T>
 __device__ __forceinline__ void map_place(Place& a, const Row<T>& row, int lo, int hi,
                                           uint8_t* map, Slots& slots, List& list) {
     constexpr int E = kElems<T>;
+    if (!a.inside) return;
     const int at = a.id + row.phase, v = at / E - lo;
-    if (!a.inside || v < 0 || v >= hi - lo) return;
+    if (v < 0 || v >= hi - lo) return;
     a.mapped = true;
     uint32_t* word = reinterpret_cast<uint32_t*>(map) + v / 4;
     const int shift = v % 4 * 8;
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     __shared__ List list;
     __shared__ WholeScratch sh;
     __shared__ BlockScratch bs;
-    const float c2 = p.c * kLog2e;
+    const float c2 = in_log2(p.c);
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     const int64_t r = p.unit0 + unit_of_group();
     const Row<T> row(p.x, r, p.stride, p.vocab);
@@ -589,7 +590,7 @@ __global__ __launch_bounds__(kBlock) void distill_part_kernel(DistillParams p) {
     __shared__ BlockScratch bs;
     __shared__ Slots slots;
     __shared__ List list;
-    const float c2 = p.c * kLog2e;
+    const float c2 = in_log2(p.c);
     const int tid = threadIdx.x;
     const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.splits);
     const Row<T> row(p.x, r, p.stride, p.vocab);
@@ -633,7 +634,7 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
     clear_seen(list);
     Place a = open_list(p, r, row, list);
     const float2* sets = p.part_sets + r * p.set_splits;
-    const Set set = join_sets(p.set_splits, p.c * kLog2e,
+    const Set set = join_sets(p.set_splits, in_log2(p.c),
                               [&](int i) { return Set{sets[i].x, sets[i].y, 0.0f}; });
     __syncthreads();
     a.leads = enters_first(a, list);
@@ -676,7 +677,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
     __shared__ Slots slots;
     __shared__ List list;
     __shared__ GradScratch sh;
-    const float c2 = p.c * kLog2e;
+    const float c2 = in_log2(p.c);
     const int tid = threadIdx.x;
     const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.splits);
     const int split = static_cast<int>(unit - r * p.splits);

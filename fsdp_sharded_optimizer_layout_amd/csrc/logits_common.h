@@ -242,6 +242,9 @@ constexpr float kNegligible = -200.0f;      // 2^-200 is 0 in float32
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// The scale for exponentials to base 2, finite for any finite scale.
+__device__ __forceinline__ float in_log2(float c) { return fminf(c * kLog2e, -kLowest); }
+
 struct Acc {
     float m = kLowest, s = 0.0f, t = 0.0f;
 };

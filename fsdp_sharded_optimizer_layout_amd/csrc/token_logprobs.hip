@@ -25,7 +25,7 @@ __device__ __forceinline__ unsigned long long candidate(float x, int i) {
            (0xFFFFFFFFu - static_cast<uint32_t>(i));
 }
 
-constexpr int kCandidates = 1024;
+constexpr int kCandidates = 768;      // (8 work-groups to a CU fit its LDS)
 constexpr int kListed = 1024;
 constexpr int kRounds = 3;
 constexpr int kMaxima = 256;           // maxima of thread groups that the threshold is taken from
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
     constexpr int E = kElems<T>, U = kLoads<T>;
     __shared__ BlockScratch bs;
     __shared__ typename std::conditional<Top, TopScratch<Threads>, int>::type top_sh;
-    const float c2 = p.c * kLog2e;
+    const float c2 = in_log2(p.c);
     const int tid = threadIdx.x;
     const int64_t unit = p.unit0 + unit_of_group();
     const int64_t r = row_of(unit, p.splits);
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(Threads) void logprobs_kernel(LogprobParams p) {
 template <typename T, bool Top>
 __global__ __launch_bounds__(kBlock) void logprobs_join_kernel(LogprobParams p) {
     __shared__ typename std::conditional<Top, TopScratch<kBlock>, int>::type sh;
-    const float c2 = p.c * kLog2e;
+    const float c2 = in_log2(p.c);
     const int tid = threadIdx.x;
     const int64_t r = p.unit0 + unit_of_group();
     const float4* sets = p.part_sets + r * p.splits;
@@ -510,7 +510,7 @@ struct LogprobGradParams {
 template <typename T>
 __global__ __launch_bounds__(kBlock) void logprobs_grad_kernel(LogprobGradParams p) {
     constexpr int E = kElems<T>;
-    const float c2 = p.c * kLog2e;
+    const float c2 = in_log2(p.c);
     const int64_t unit = p.unit0 + unit_of_group();
     const int64_t r = row_of(unit, p.splits);
     const Row<T> row(p.x, r, p.stride, p.vocab);

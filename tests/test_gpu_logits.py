@@ -270,6 +270,49 @@ def test_distill_special_rows(vocab, dtype, tail):
                      dtype, f"distill special {vocab} {dtype} k={k} {tail}")
 
 
+@pytest.mark.parametrize("vocab", [700, 40001, 150001])
+def test_logits_far_from_zero(vocab):
+    """|scale x| beyond 2^20 with neighbours that still share the mass: the difference to the
+    maximum has to be taken before anything is rounded."""
+    rng = _seed(vocab, 41)
+    scale, rows = 300.0, 3
+    x = 1e4 + 0.02 * rng.standard_normal((rows, vocab))
+    x[1] = -1e4 + 0.02 * rng.standard_normal(vocab)
+    x[2] = 3.0 * rng.standard_normal(vocab)                    # an ordinary row beside them
+    t, x64 = C.to_dtype(x, "fp32")
+    dev, _ = C.on_device(t, 1, 1)
+    ids = rng.integers(0, vocab, rows)
+    got = C.run_logprobs(dev, ids, scale, 20)
+    C.check_logprobs(x64, ids, scale, 20, C.host(got), f"far {vocab}")
+    g, h = np.ones(rows, np.float32), np.full(rows, 0.3, np.float32)
+    out, _ = C.filled_like(t)
+    F.token_logprobs_grad(dev, torch.as_tensor(ids).cuda(), got["stats"], out, scale=scale,
+                          dlogprob=torch.from_numpy(g).cuda(), entropy=got["entropy"],
+                          dentropy=torch.from_numpy(h).cuda())
+    C.check_logprobs_grad(x64, ids, g, h, scale, "fp32", out.double().cpu().numpy(), "far")
+    for tail in (False, True):
+        tid, tv = C.teacher_lists(rng, x64, 30, tail)
+        tv = np.where(np.isfinite(tv), tv / (1 if tail else scale), tv).astype(np.float32)
+        _distill_all(dev, t, x64, torch.from_numpy(tid), torch.from_numpy(tv), g, scale, tail,
+                     "fp32", f"far {vocab} {tail}")
+
+
+@pytest.mark.parametrize("scale", [3e38, 1e-30])
+def test_extreme_scales(scale):
+    """The largest scale leaves all mass on the maximum, the smallest spreads it evenly."""
+    rng = _seed(43)
+    x = rng.standard_normal((4, 5003)).astype(np.float32)
+    dev = torch.from_numpy(x).cuda()
+    best = torch.from_numpy(x.argmax(1)).cuda()
+    got = C.run_logprobs(dev, best.cpu().numpy(), scale, 3)
+    lp = 0.0 if scale > 1 else -np.log(5003)
+    assert torch.allclose(got["logprob"].double(), torch.full((4,), lp, dtype=torch.float64,
+                                                              device="cuda"), rtol=1e-4, atol=0)
+    assert torch.allclose(got["entropy"].double(), torch.full((4,), -lp, dtype=torch.float64,
+                                                              device="cuda"), rtol=1e-4, atol=0)
+    assert torch.equal(got["top_ids"][:, 0].long(), best)
+
+
 def test_distill_list_of_the_whole_vocabulary():
     """Nothing outside the list, every token in it (some twice)."""
     rng = _seed(11)

@@ -173,3 +173,15 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         F.token_logprobs_grad(x, None, torch.zeros(2, 2), x, dlogprob=torch.zeros(2))
     with pytest.raises(ValueError, match="device tensor"):
         F.distill_topk(x, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1), torch.zeros(2))
+
+
+def test_header_is_plain_c(tmp_path):
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "use.c"
+    src.write_text('#include "fsdpshard_logits.h"\n'
+                   'int use(const fsdpshard_logits* x, const fsdpshard_teacher* t, float* f) {\n'
+                   '    return distill_topk(x, t, f, f, 0, 0, 0) + (FSDPSHARD_MAX_VOCAB > 0);\n}\n')
+    subprocess.run(["gcc", "-std=c99", "-pedantic", "-Wall", "-Wextra", "-Werror", "-fsyntax-only",
+                    f"-I{os.path.join(root, 'include')}", str(src)], check=True)
