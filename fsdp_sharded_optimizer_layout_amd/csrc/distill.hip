@@ -69,10 +69,11 @@ __device__ __forceinline__ int list_threads(const DistillParams& p) {
     return p.k <= kWave ? kWave : kTop;
 }
 
-// Loads the list of row r.  Before the next step: a barrier.
+// Loads the list of row r, and the listed logits unless they come later.  Before the next step: a
+// barrier.
 template <typename T>
 __device__ __forceinline__ Place open_list(const DistillParams& p, int64_t r, const Row<T>& row,
-                                           List& list) {
+                                           List& list, bool with_logits = true) {
     const int j = threadIdx.x;
     Place a;
     if (j < p.k) {
@@ -90,7 +91,7 @@ __device__ __forceinline__ Place open_list(const DistillParams& p, int64_t r, co
         }
     }
     if (j < list_threads(p)) {
-        if (a.inside) a.x = row.at(a.id);
+        if (a.inside && with_logits) a.x = row.at(a.id);
         list.id[j] = a.valid ? a.id : -1;
         const float top = wave_max(a.valid ? a.value : -kInf);
         const bool some = __ballot(a.valid) != 0;
@@ -372,7 +373,8 @@ struct WholeScratch {
     float wave_top[kMaxWaves], wave_rest[kMaxWaves];
     int wave_ones[kMaxWaves];
     float coef;
-    int zero, owner;
+    int state;                     // what the row gets: 0 its gradient, 1 zeros, 2 NaN
+    int owner;
 };
 
 template <typename T, int Threads, int Vecs, bool Grad, bool Once>
@@ -401,7 +403,10 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     }
     clear_map(map, Vecs > 0 ? Threads * Vecs : row.nvec, Threads);
     if (tid < kTop) slots.listed[tid] = u32x4{0, 0, 0, 0};
-    Place a = open_list(p, r, row, list);
+    // The listed logits pass through the registers, too: up to one wave of places, they are picked up
+    // there, by way of the slots, instead of from memory, a cache line each.
+    const bool pick_up = Vecs > 0 && p.k <= kWave;
+    Place a = open_list(p, r, row, list, !pick_up);
     __syncthreads();
     if (!list_some(list)) {
         if (tid == 0) write_row(p, r, RowResult{}, 0.0, false, list);
@@ -417,7 +422,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     if (list.repeats) a.leads = a.mapped && first_place(p, a, list);
     double mass, rest;
     settle_list(p, a, list, mass, rest);
-    list_peak(p, a, list);
+    if (!pick_up) list_peak(p, a, list);
 
     // The tokens outside the list.  In registers, only they stay: the others become -inf, and so do
     // the first and the last vector's elements that are not the row's.
@@ -450,7 +455,10 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
                 const int v = tid + (i0 + i) * Threads;
                 if (v == 0) mask_out<T>(raw[i0 + i], first_mask);
                 if (v == row.nvec - 1) mask_out<T>(raw[i0 + i], last_mask);
-                drop_listed<T>(raw[i0 + i], map[v], slots);
+                if (const int byte = map[v]; byte != 0) {
+                    slots.value[byte - 1] = raw[i0 + i];
+                    mask_out<T>(raw[i0 + i], slots.listed[byte - 1]);
+                }
             }
 #pragma unroll
             for (int i = 0; i < Step; ++i) {
@@ -468,8 +476,19 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     float mt = sh.wave_top[0];
 #pragma unroll
     for (int i = 1; i < W; ++i) mt = fmaxf(mt, sh.wave_top[i]);
-    const float list_max = fmaxf(list.x_max[0], list.x_max[1]);
-    const bool list_nan = list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
+    float list_max;                             // (in the list's threads)
+    bool list_nan;
+    if (pick_up) {
+        if (tid < kWave && a.mapped) {
+            const int at = a.id + row.phase;
+            a.x = widen(reinterpret_cast<const T*>(&slots.value[map[at / E] - 1])[at % E]);
+        }
+        list_max = wave_max(a.leads ? a.x : -kInf);
+        list_nan = __ballot(a.leads && !(a.x < kInf)) != 0;
+    } else {
+        list_max = fmaxf(list.x_max[0], list.x_max[1]);
+        list_nan = list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
+    }
     const bool is_top = acc.m == mt && acc.s != 0.0f;     // a NaN sum counts
     rebase<false>(acc, mt, c2);
     {
@@ -525,7 +544,8 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
             set_value(p, a, logp, gc, mass, row, 0, map, slots, list);
             if (tid == 0) {
                 sh.coef = outside_factor(p, d, gc, mass, rest);
-                sh.zero = g == 0.0f || (d.L == -HUGE_VAL && !list_bad(list) && !nan);
+                const bool bad = list_bad(list) || nan;
+                sh.state = g == 0.0f || (d.L == -HUGE_VAL && !bad) ? 1 : bad ? 2 : 0;
             }
         }
     }
@@ -534,10 +554,8 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     if constexpr (Grad) {
         const OutRow<T> out(p.out, r, p.ostride, row);
         const float coef = sh.coef;
-        if (sh.zero) {
-            fill_part<Threads>(row, out, part, 0.0f);
-        } else if (list_bad(list) || nan) {
-            fill_part<Threads>(row, out, part, __builtin_nanf(""));
+        if (sh.state != 0) {
+            fill_part<Threads>(row, out, part, sh.state == 2 ? __builtin_nanf("") : 0.0f);
         } else {
             // 2^u by one fused multiply-add, as in add_batch; far from 0, the row is read again.
             const float base = c2 * mt, delta = __builtin_fmaf(c2, mt, -base);
