@@ -195,21 +195,23 @@ __device__ __forceinline__ void weigh_list(const DistillParams& p, Place& a, Lis
     if (j % kWave == 0) list.q_sum[j / kWave] = sum;
 }
 
-// mass = sum q and, with a tail, rest = 1 - mass (all threads); q and log q of the places.
-__device__ __forceinline__ void settle_list(const DistillParams& p, Place& a, List& list,
-                                            double& mass, double& rest) {
-    mass = list.q_sum[0] + list.q_sum[1];
-    rest = 0.0;
-    if (p.tail) {
-        rest = fmax(0.0, 1.0 - mass);
-    } else if (mass > 0.0) {
-        if (static_cast<int>(threadIdx.x) < list_threads(p)) {
-            a.q /= mass;
-            a.logq -= log(mass);
-        }
-        mass = 1.0;
+// mass = sum q and, with a tail, rest = 1 - mass.  After weigh_list and a barrier.
+__device__ __forceinline__ void list_mass(const DistillParams& p, const List& list, double& mass,
+                                          double& rest) {
+    const double sum = list.q_sum[0] + list.q_sum[1];
+    mass = p.tail || sum == 0.0 ? sum : 1.0;
+    rest = p.tail ? fmax(0.0, 1.0 - sum) : 0.0;
+}
+
+// q and log q of the places.  After weigh_list and a barrier.
+__device__ __forceinline__ void settle_list(const DistillParams& p, Place& a, List& list) {
+    if (static_cast<int>(threadIdx.x) >= list_threads(p)) return;
+    const double sum = list.q_sum[0] + list.q_sum[1];
+    if (!p.tail && sum > 0.0) {
+        a.q /= sum;
+        a.logq -= log(sum);
     }
-    if (static_cast<int>(threadIdx.x) < list_threads(p)) list.q[threadIdx.x] = a.q;
+    list.q[threadIdx.x] = a.q;
 }
 
 // The maximum of the listed logits, by wave (NaN: a NaN or +inf among them).
@@ -420,8 +422,7 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
     }
     __syncthreads();
     if (list.repeats) a.leads = a.mapped && first_place(p, a, list);
-    double mass, rest;
-    settle_list(p, a, list, mass, rest);
+    settle_list(p, a, list);
     if (!pick_up) list_peak(p, a, list);
 
     // The tokens outside the list.  In registers, only they stay: the others become -inf, and so do
@@ -532,6 +533,8 @@ __global__ __launch_bounds__(Threads, Vecs > 0 ? 4 : 1) void distill_whole_kerne
         rt = block_sum(s.x, bs, 0, W);
     }
     const bool nan = rt != rt || list_nan;
+    double mass, rest;
+    list_mass(p, list, mass, rest);
     if (rt == -1.0f) rest = 0.0;                // nothing unmasked outside the list
     mass += rest;
     RowResult d{};
@@ -661,7 +664,8 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillParams p) {
     __syncthreads();
     if (list.repeats) a.leads = a.inside && first_place(p, a, list);
     double mass, rest;
-    settle_list(p, a, list, mass, rest);
+    settle_list(p, a, list);
+    list_mass(p, list, mass, rest);
     const float list_max = fmaxf(list.x_max[0], list.x_max[1]);
     const bool list_nan = list.x_max[0] != list.x_max[0] || list.x_max[1] != list.x_max[1];
     list_terms(p, a, fmaxf(list_max, set.m), list);
@@ -747,7 +751,8 @@ __global__ __launch_bounds__(kBlock) void distill_grad_kernel(DistillParams p) {
         if (Join) a.leads = first;
     }
     double mass, rest;
-    settle_list(p, a, list, mass, rest);
+    settle_list(p, a, list);
+    list_mass(p, list, mass, rest);
     RowResult d{};
     bool nan = false;
     if constexpr (Join) {
