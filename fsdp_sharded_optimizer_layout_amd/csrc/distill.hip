@@ -843,7 +843,7 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     }
     // With the gradient, rows up to 65,536 16-bit elements: longer ones leave a CU with one work-group,
     // whose loads, arithmetic and stores then wait for each other.  Measured with 64 places: 4096 x
-    // 65536 bf16 227 us in registers, 88 + 181 in two passes; 2048 x 131072 278 and 92 + 176.
+    // 65536 bf16 203 us in registers, 262 in two passes; 2048 x 131072 277 and 264.
     if constexpr (Grad) {
         if (vecs <= 16 * 256)
             return once ? whole_form<256, 16, true, true>(dtype, vecs)
@@ -859,7 +859,13 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     return {nullptr, 0, 0};
 }
 
-constexpr int64_t kJoinRows = 512;
+// Loss and gradient in two passes, few rows: the gradient joins the parts by itself (one launch less)
+// for matrices of up to 32 MiB, and beyond where the loss would give each row to one work-group.
+// Measured with 16 places, joined in the gradient and by the loss, us: fp32 32 x 131072 17.5 and
+// 20.4, 64 rows 28.2 and 27.8, 256 rows 84 and 77, 512 rows 153 and 142; bf16 64 x 131072 19.7 and
+// 24.0, 256 rows 47.1 and 46.0, 512 rows 84 and 90 (rows of one work-group).
+constexpr int64_t kJoinRows = 512, kJoinBytes = int64_t{32} << 20;
+static_assert(kWantUnits / kJoinRows >= 2, "rows whose parts the gradient joins are cut");
 
 // The sets of the rows' parts.
 int launch_parts(DistillParams& p, int32_t dtype, bool once, void* workspace, void* stream) {
@@ -895,7 +901,6 @@ int launch_distill_grad(DistillParams& p, int32_t dtype, bool join, void* stream
 }
 
 }  // namespace
-
 
 extern "C" int64_t distill_topk_workspace_bytes(int64_t rows, int64_t vocab) {
     if (rows < 0 || vocab < 1 || vocab > FSDPSHARD_MAX_VOCAB || rows > kMaxRows) return -1;
@@ -992,7 +997,9 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
         return launch_units(whole.kernel, rows, p, whole.map_bytes, stream, whole.threads);
     // Otherwise two passes.  The second finds the logits in the last-level cache if that holds them.
     // Few rows, unless in place: the parts' sets, which the gradient joins by itself.
-    if (rows <= kJoinRows && !in_place) {
+    if (rows <= kJoinRows && !in_place &&
+        (rows * logits->vocab * element_bytes(logits->dtype) <= kJoinBytes ||
+         whole_kernel<false>(p, logits->dtype, false).kernel != nullptr)) {
         rc = launch_parts(p, logits->dtype, false, workspace, stream);
         if (rc != FSDPSHARD_OK) return rc;
         return launch_distill_grad(p, logits->dtype, true, stream);

@@ -554,8 +554,8 @@ struct OutRow {
 };
 
 // A gradient's part is one batch of at most Loads vectors a thread: load_part reads it (edges aside),
-// write_part stores what f(x, v) makes of each vector's floats.  Short
-// parts, because a work-group that loops waits for its loads again after each batch of stores.
+// write_part stores what f(x, v) makes of each vector's floats.  Short parts, because a work-group
+// that loops waits for its loads again after each batch of stores.
 template <int Loads, typename T>
 __device__ __forceinline__ void load_part(const Row<T>& row, const Part& part,
                                           u32x4 (&raw)[Loads]) {
@@ -594,9 +594,10 @@ __device__ __forceinline__ void fill_part(const Row<T>& row, const OutRow<T>& ou
 #pragma unroll
     for (int e = 0; e < kElems<T>; ++e) x[e] = value;
     const u32x4 out_vec = pack<T>(x);
-    for (int v = part.va + static_cast<int>(threadIdx.x); v < part.vb; v += Threads) out.put(v, out_vec);
-    if ((part.first && threadIdx.x == 0) || (part.last && threadIdx.x == 1))
-        out.put_masked(row, threadIdx.x == 0 ? part.lo : part.hi - 1, out_vec);
+    const int tid = threadIdx.x;
+    for (int v = part.va + tid; v < part.vb; v += Threads) out.put(v, out_vec);
+    if ((part.first && tid == 0) || (part.last && tid == 1))
+        out.put_masked(row, tid == 0 ? part.lo : part.hi - 1, out_vec);
 }
 
 // ------------------------------------------------------------------------------------------------

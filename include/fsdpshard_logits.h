@@ -10,8 +10,9 @@
  *
  * The conventions of fsdpshard.h hold: device pointers owned by the caller, no allocation, no
  * memset, no synchronisation (so every call can be captured in a HIP graph), argument errors found
- * before anything is enqueued, a status returned.  A call enqueues one to three kernels.  Results
- * do not depend on the launch: sums have a fixed order, and there are no atomic additions of
+ * before anything is enqueued, a status returned.  A call enqueues one to three kernels (each in
+ * several launches where a matrix has more than 2^20 rows or parts of rows).  Results do not
+ * depend on the launch: sums have a fixed order, and there are no atomic additions of
  * floating-point values.
  *
  * Logits.  A matrix of `rows` rows of `vocab` values, `row_stride` elements apart, in bf16, fp16

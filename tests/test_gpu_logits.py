@@ -250,6 +250,20 @@ def test_distill_shapes(shape, dtype, tail):
                      opad=(k + pad) % 3, oshift=k % 2)
 
 
+# Long rows at both sides of the size up to which the joint call's gradient joins a row's parts (32
+# MiB), and rows that the loss by itself gives to one work-group each.
+@pytest.mark.parametrize("dtype,rows", [("fp32", 119), ("fp32", 121), ("bf16", 241)])
+def test_distill_few_long_rows(dtype, rows):
+    vocab = 70001
+    rng = _seed(rows, vocab, len(dtype))
+    t, x64 = C.to_dtype(C.plain_rows(rng, rows, vocab), dtype)
+    dev, _ = C.on_device(t)
+    tid, tv = C.teacher_lists(rng, x64, 16, True)
+    g = rng.standard_normal(rows).astype(np.float32)
+    _distill_all(dev, t, x64, torch.from_numpy(tid), torch.from_numpy(tv), g, 1.0, True, dtype,
+                 f"distill {rows} x {vocab} {dtype}")
+
+
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("vocab", [40, 9001])
