@@ -281,7 +281,7 @@ __device__ __forceinline__ void rebase(Acc& a, float m, float c2) {
 // multiply-add where it can: with b the rounded c2 m, the batch adds up 2^(c2 x - b), which is
 // 2^delta times its terms, delta = c2 m - b, at most 2^-5 while |c2 m| < 2^20.  Beyond that (and
 // while only masked elements were seen) the difference is taken first.  Measured on 8192 x 32000
-// bf16: 87 us with the difference throughout.
+// bf16: 85 us, 87 with the difference throughout.
 template <int N, bool Entropy>
 __device__ __forceinline__ void add_batch(Acc& a, const float* x, float top, float c2) {
     rebase<Entropy>(a, fmaxf(a.m, top), c2);
