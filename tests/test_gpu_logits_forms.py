@@ -1,0 +1,161 @@
+"""The kernels that large matrices of logits take, by value against the float64 oracle: more than 512
+rows of real, odd vocabularies in every type, below and beyond 128 MiB (where rows are loaded without
+keeping them in a cache), in one work-group a row and in parts, and the largest vocabulary.
+
+A sample of rows goes to the oracle, with the error bounds of logits_cases: one row of each kind of
+special_rows, spread over the matrix, and 8 ordinary ones between them.  All rows are checked for
+having been written, and what lies between them for not having been."""
+
+import numpy as np
+import pytest
+import torch
+
+import fsdp_sharded_optimizer_layout_amd as F
+import logits_cases as C
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+# (dtype, rows, vocab, pad between rows, shift of the base).  Vectors a row decide the joint call's
+# kernel: up to 4096 one work-group of 256 threads, up to 8192 one of 512, beyond that two passes.
+MATRICES = [
+    ("bf16", 600, 5003, 0, 1), ("fp16", 600, 31999, 1, 0), ("fp32", 600, 16001, 3, 1),
+    ("bf16", 530, 50021, 0, 3), ("fp32", 530, 32003, 0, 1),
+    ("fp16", 520, 100003, 5, 0),                                  # two passes, whole rows
+    # 128 MiB and more
+    ("bf16", 2100, 32003, 0, 1), ("fp16", 2100, 32000, 0, 0), ("fp32", 2200, 16001, 0, 1),
+    ("fp16", 1400, 50021, 0, 0), ("fp32", 1100, 32003, 5, 0),
+    ("bf16", 530, 131071, 0, 1),                                  # two passes, whole rows
+    ("bf16", 600, 140001, 0, 1), ("fp32", 600, 70001, 0, 0),      # parts
+    ("fp16", 1000, 140001, 0, 1),                                 # beyond 256 MiB
+]
+
+
+def _matrix(dtype, rows, vocab, pad, shift):
+    """(logits on the GPU, sampled rows, their values as float64)."""
+    rng = np.random.default_rng([rows, vocab, len(dtype)])
+    gen = torch.Generator(device="cuda").manual_seed(rows * 7 + vocab)
+    stride = vocab + pad
+    buf = torch.full((shift + rows * stride + 8,), float("nan"), dtype=C.DTYPES[dtype],
+                     device="cuda")
+    x = buf[shift:shift + rows * stride].view(rows, stride)[:, :vocab]
+    for r in range(0, rows, 256):
+        n = min(256, rows - r)
+        x[r:r + n] = torch.randn(n, vocab, generator=gen, device="cuda") * 3
+    odd, _ = C.to_dtype(C.special_rows(rng, vocab, dtype), dtype)
+    spread = np.linspace(0, rows - 1, 24).round().astype(np.int64)
+    special = spread[np.arange(16) * 3 // 2]
+    x[torch.from_numpy(special).cuda()] = odd.cuda()
+    return x, spread, x[torch.from_numpy(spread).cuda()].double().cpu().numpy(), special
+
+
+def _gradient_like(x, pad, shift):
+    rows, vocab = x.shape
+    whole = torch.full((shift + rows * (vocab + pad) + 8,), 77.0, dtype=x.dtype, device="cuda")
+    return whole[shift:shift + rows * (vocab + pad)].view(rows, -1)[:, :vocab], whole
+
+
+def _check_written(out, whole, pad, shift, what):
+    """Gradients here are below 77, so no element of the rows still holds it, and all others do."""
+    rows, vocab = out.shape
+    assert not (out == 77).any(), f"{what}: elements not written"
+    end = shift + rows * (vocab + pad)
+    assert (whole[:shift] == 77).all() and (whole[end:] == 77).all(), f"{what}: written outside"
+    if pad:
+        between = whole[shift:end].view(rows, vocab + pad)[:, vocab:]
+        assert (between == 77).all(), f"{what}: written between the rows"
+
+
+def _pick(t, rows):
+    return t[torch.from_numpy(rows).to(t.device)]
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype,rows,vocab,pad,shift", MATRICES)
+def test_logprobs_of_large_matrices(dtype, rows, vocab, pad, shift):
+    x, some, x64, special = _matrix(dtype, rows, vocab, pad, shift)
+    rng = np.random.default_rng([rows, vocab, 1])
+    ids = C.tokens(rng, rows, vocab)
+    ids[special[[0, 9]]] = -1, vocab
+    ids[special[3]], ids[special[12]] = vocab // 2, vocab // 3
+    got = None
+    for k in (0, 20, 128):
+        what = f"logprobs {dtype} {rows} x {vocab} k={k}"
+        say(what)
+        got = C.run_logprobs(x, ids, 1.0, k)
+        for name, t in got.items():
+            assert name == "top_ids" or not (t == 55).any(), f"{what}: {name} not written"
+        C.check_logprobs(x64, ids[some], 1.0, k, C.host({n: _pick(t, some)
+                                                         for n, t in got.items()}), what)
+    g, h = (rng.standard_normal(rows).astype(np.float32) for _ in range(2))
+    g[rng.random(rows) < 0.2] = 0
+    h[rng.random(rows) < 0.2] = 0
+    idt, gd, hd = torch.as_tensor(ids).cuda(), torch.from_numpy(g).cuda(), torch.from_numpy(h).cuda()
+    for hh in (None, hd):
+        what = f"logprobs grad {dtype} {rows} x {vocab} h={hh is not None}"
+        say(what)
+        out, whole = _gradient_like(x, pad, shift)
+        F.token_logprobs_grad(x, idt, got["stats"], out, dlogprob=gd, entropy=got["entropy"],
+                              dentropy=hh)
+        C.check_logprobs_grad(x64, ids[some], g[some], (0 * h if hh is None else h)[some], 1.0,
+                              dtype, _np(_pick(out, some)), what)
+        _check_written(out, whole, pad, shift, what)
+
+
+def _lists(x, k, tail, special):
+    """Half of each list the row's best tokens, half drawn (so that some stand in it twice); a tenth
+    of the places empty, every ninth list, and what test_distill_special_rows gives its rows."""
+    rows, vocab = x.shape
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    ids = torch.randint(0, vocab, (rows, k), generator=gen, device="cuda")
+    ids[:, :(k + 1) // 2] = x.topk((k + 1) // 2, 1).indices
+    w = torch.rand(rows, k, generator=gen, device="cuda") ** 3 + 1e-6
+    share = torch.rand(rows, 1, generator=gen, device="cuda") * 0.7 + 0.3 if tail else 1.0
+    values = (w / w.sum(1, keepdim=True) * share).log()
+    ids[torch.rand(rows, k, generator=gen, device="cuda") < 0.1] = -1
+    ids[4::9] = -1
+    sp = special.tolist()
+    ids[sp[12], 0] = vocab // 3
+    ids[sp[9], 1], ids[sp[10], 0] = vocab, 2 ** 31 - 1
+    ids[sp[11], 0], values[sp[11], 0] = 1, float("nan")
+    ids[sp[8], 0], values[sp[8], 0] = 1, float("inf")
+    values[sp[14]] = -float("inf")
+    return ids.int(), values
+
+
+@pytest.mark.parametrize("k,tail", [(64, False), (100, True)])
+@pytest.mark.parametrize("dtype,rows,vocab,pad,shift", MATRICES)
+def test_distill_of_large_matrices(dtype, rows, vocab, pad, shift, k, tail):
+    x, some, x64, special = _matrix(dtype, rows, vocab, pad, shift)
+    rng = np.random.default_rng([rows, vocab, k])
+    tid, tv = _lists(x, k, tail, special)
+    g = rng.uniform(0.5, 1.5, rows).astype(np.float32)
+    g[rng.random(rows) < 0.1] = 0
+    gd = torch.from_numpy(g).cuda()
+    si, sv = _pick(tid, some).cpu().numpy(), _pick(tv, some).cpu().numpy()
+    f = dict(dtype=torch.float32, device="cuda")
+    for joint in (False, True):
+        what = f"distill {dtype} {rows} x {vocab} k={k} tail={tail} {'joint' if joint else 'apart'}"
+        say(what)
+        loss, stats = torch.full((rows,), 55.0, **f), torch.full((rows, 4), 55.0, **f)
+        out, whole = _gradient_like(x, pad, shift)
+        if joint:
+            F.distill_topk_loss_grad(x, tid, tv, gd, loss, stats, out, tail=tail)
+        else:
+            F.distill_topk(x, tid, tv, loss, stats, tail=tail)
+            F.distill_topk_grad(x, tid, tv, stats, gd, out, tail=tail)
+        assert not (loss == 55).any() and not (stats == 55).any(), f"{what}: not written"
+        C.check_distill(x64, si, sv, 1.0, tail, _np(_pick(loss, some)), _np(_pick(stats, some)),
+                        what)
+        C.check_distill_grad(x64, si, sv, g[some], 1.0, tail, dtype, _np(_pick(out, some)), what)
+        _check_written(out, whole, pad, shift, what)
+    say(f"{what}, in place")
+    loss2, stats2 = torch.empty(rows, **f), torch.empty(rows, 4, **f)
+    F.distill_topk_loss_grad(x, tid, tv, gd, loss2, stats2, x, tail=tail)
+    bits = torch.int32 if dtype == "fp32" else torch.int16
+    for a, b in ((loss, loss2), (stats, stats2)):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32)), what
+    assert torch.equal(x.view(bits), out.view(bits)), what
