@@ -159,3 +159,43 @@ def test_distill_of_large_matrices(dtype, rows, vocab, pad, shift, k, tail):
     for a, b in ((loss, loss2), (stats, stats2)):
         assert torch.equal(a.view(torch.int32), b.view(torch.int32)), what
     assert torch.equal(x.view(bits), out.view(bits)), what
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_largest_vocabulary(dtype):
+    """Hundreds of parts a row, each with its own list of alternatives: an ordinary row, one masked in
+    large part, and one of many ties."""
+    rows, vocab, k = 3, (1 << 21) - 3, 128
+    rng = np.random.default_rng([vocab, len(dtype)])
+    v = C.plain_rows(rng, rows, vocab)
+    v[1, rng.random(vocab) < 0.7] = -np.inf
+    v[2] = np.round(v[2])
+    t, x64 = C.to_dtype(v, dtype)
+    x, _ = C.on_device(t, 2, 1)
+    ids = np.array([vocab - 1, int(np.argmax(x64[1])), 0])
+    say(f"logprobs {dtype} {rows} x {vocab}")
+    got = C.run_logprobs(x, ids, 1.0, k)
+    C.check_logprobs(x64, ids, 1.0, k, C.host(got), f"largest vocabulary {dtype}")
+    g, h = np.ones(rows, np.float32), np.full(rows, -0.5, np.float32)
+    gd = torch.from_numpy(g).cuda()
+    say("logprobs grad")
+    out, whole = C.filled_like(t, 1, 3)
+    F.token_logprobs_grad(x, torch.as_tensor(ids).cuda(), got["stats"], out, dlogprob=gd,
+                          entropy=got["entropy"], dentropy=torch.from_numpy(h).cuda())
+    C.check_logprobs_grad(x64, ids, g, h, 1.0, dtype, _np(out), f"largest vocabulary {dtype}")
+    C.assert_between_rows_untouched(out, whole, dtype)
+    tid, tv = C.teacher_lists(rng, x64, k, True)
+    tid[0, :2] = vocab - 1, 0
+    tid_d, tv_d = torch.from_numpy(tid).cuda(), torch.from_numpy(tv).cuda()
+    for joint in (False, True):
+        say(f"distill {'joint' if joint else 'apart'}")
+        loss, stats = torch.full((rows,), 55.0).cuda(), torch.full((rows, 4), 55.0).cuda()
+        out, whole = C.filled_like(t, 1, 3)
+        if joint:
+            F.distill_topk_loss_grad(x, tid_d, tv_d, gd, loss, stats, out, tail=True)
+        else:
+            F.distill_topk(x, tid_d, tv_d, loss, stats, tail=True)
+            F.distill_topk_grad(x, tid_d, tv_d, stats, gd, out, tail=True)
+        C.check_distill(x64, tid, tv, 1.0, True, _np(loss), _np(stats), dtype)
+        C.check_distill_grad(x64, tid, tv, g, 1.0, True, dtype, _np(out), dtype)
+        C.assert_between_rows_untouched(out, whole, dtype)

@@ -185,3 +185,26 @@ def test_header_is_plain_c(tmp_path):
                    '    return distill_topk(x, t, f, f, 0, 0, 0) + (FSDPSHARD_MAX_VOCAB > 0);\n}\n')
     subprocess.run(["gcc", "-std=c99", "-pedantic", "-Wall", "-Wextra", "-Werror", "-fsyntax-only",
                     f"-I{os.path.join(root, 'include')}", str(src)], check=True)
+
+
+MOST = 1 << 21                       # the largest vocabulary that the header promises
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_vocabulary_limit(call):
+    wide = dict(row_stride=1 << 22, rows=0)
+    assert call(x=_logits(vocab=MOST, **wide)) == OK
+    assert call(x=_logits(vocab=MOST + 1, **wide)) == UNSUP
+    assert call(x=_logits(vocab=MOST + 1, row_stride=1 << 22, rows=1)) == UNSUP
+
+
+def test_vocabulary_limit_of_the_workspaces():
+    for rows in (1, 4, 1000):
+        need = F.token_logprobs_workspace_bytes(rows, MOST, 128)
+        assert need > 0 and F.token_logprobs_workspace_bytes(rows, MOST + 1, 128) == -1
+        x = _logits(rows=rows, vocab=MOST, row_stride=MOST)
+        assert logprobs(x=x, k=128, wbytes=need - 1) == CAPACITY
+        need = F.distill_topk_workspace_bytes(rows, MOST)
+        assert need > 0 and F.distill_topk_workspace_bytes(rows, MOST + 1) == -1
+        assert distill(x=x, wbytes=need - 1) == CAPACITY
+        assert distill_loss_grad(x=x, stride=MOST, wbytes=need - 1) == CAPACITY
