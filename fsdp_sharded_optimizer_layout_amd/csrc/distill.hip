@@ -837,10 +837,14 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     const bool in_phase = aligned16(p.x) && (p.rows <= 1 || p.stride % per == 0);
     const int64_t vecs = (p.vocab + (in_phase ? per - 1 : 2 * per - 2)) / per;
     // Few rows: the largest work-group, for latency.
-    if (p.rows <= kWideRows) {
-        if (vecs <= 4 * 1024) return whole_form<1024, 4, Grad>(dtype, vecs);
-        if (!Grad && vecs <= 16 * 1024) return whole_form<1024, 16, false>(dtype, vecs);
-    }
+    if (p.rows <= kWideRows && vecs <= 4 * 1024) return whole_form<1024, 4, Grad>(dtype, vecs);
+    // The loss alone, longer rows: held in the registers of 1024 threads it is faster than streamed by
+    // 256 where rows are fewer and longer still.  Measured with 32 places, us held and streamed: bf16
+    // 64 x 80000 13.3 and 13.2, 64 x 90000 13.8 and 14.8, 128 x 90000 15.1 and 15.1, 160 x 90000 16.1
+    // and 15.3, 128 x 110000 15.8 and 17.3, 192 x 131072 18.8 and 18.9, 256 x 131072 22.2 and 19.2;
+    // fp32 64 x 40000 10.3 and 10.9, 128 x 50000 12.3 and 13.3, 192 x 50000 14.1 and 13.6.
+    if (!Grad && p.rows <= kWideRows / 2 && vecs > 10 * 1024 && vecs <= 16 * 1024)
+        return whole_form<1024, 16, false>(dtype, vecs);
     // With the gradient, rows up to 65,536 16-bit elements: longer ones leave a CU with one work-group,
     // whose loads, arithmetic and stores then wait for each other.  Measured with 64 places: 4096 x
     // 65536 bf16 203 us in registers, 262 in two passes; 2048 x 131072 277 and 264.

@@ -727,12 +727,14 @@ Cut cut_gradient(int64_t vocab, int elem, int64_t most) {
     return {static_cast<int32_t>((vecs + part - 1) / part), static_cast<int32_t>(part)};
 }
 
-// Threads of a work-group that takes a whole row.  Measured on rows of 32,000 bf16 with 20
-// alternatives: 16 rows 16.9 us with 256 threads (split, two launches), 12.5 with 1024; 512 rows 20
-// and 20; 1024 rows 19 and 39 (21.5 with 512).
-constexpr int64_t kWideRows = 512;
-
-int row_threads(int64_t rows) { return rows <= kWideRows ? 1024 : kBlock; }
+// Up to this many rows, each has a CU to itself, and a whole row takes a work-group of 1024 threads;
+// where some CUs have a second row, work-groups of 256 are faster.  Measured on bf16, us with 1024
+// threads and with 256: log probabilities with 20 alternatives, rows of 32,000, 192 rows 10.1 and
+// 10.8, 256 rows 10.7 and 11.1, 257 rows 17.0 and 12.0, 512 rows 19.4 and 13.2, 1024 rows 35 and 19;
+// rows of 131,072, 192 rows 17.6 and 23.2, 256 rows 18.8 and 23.5, 257 rows 31.6 and 28.7; loss and
+// gradient with 32 places, rows of 32,000, 256 rows 12.2 and 15.0, 257 rows 19.6 and 17.6, 512 rows
+// 22.7 and 20.1.
+constexpr int64_t kWideRows = 256;
 
 Cut whole_rows(int64_t vocab, int elem) {
     const int64_t per = 16 / elem;

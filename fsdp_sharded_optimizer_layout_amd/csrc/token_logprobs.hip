@@ -634,7 +634,7 @@ extern "C" int token_logprobs(const fsdpshard_logits* logits, const int64_t* ids
     const Cut whole = whole_rows(logits->vocab, element_bytes(logits->dtype));
     if (whole.part_vecs <= kMaxPartVecs && !worth_splitting(rows, logits->vocab, top_k)) {
         cut = whole;
-        threads = row_threads(rows);
+        threads = rows <= kWideRows ? 1024 : kBlock;
     }
     LogprobParams p{};
     p.x = logits->data;

@@ -1,6 +1,7 @@
-"""The kernels that large matrices of logits take, by value against the float64 oracle: more than 512
-rows of real, odd vocabularies in every type, below and beyond 128 MiB (where rows are loaded without
-keeping them in a cache), in one work-group a row and in parts, and the largest vocabulary.
+"""The kernels that matrices of logits of real sizes take, by value against the float64 oracle: rows of
+odd vocabularies in every type, as many as the CUs and more, below and beyond 128 MiB (where rows are
+loaded without keeping them in a cache), in one work-group a row and in parts, and the largest
+vocabulary.
 
 A sample of rows goes to the oracle, with the error bounds of logits_cases: one row of each kind of
 special_rows, spread over the matrix, and 8 ordinary ones between them.  All rows are checked for
@@ -19,6 +20,12 @@ pytestmark = pytest.mark.gpu
 # (dtype, rows, vocab, pad between rows, shift of the base).  Vectors a row decide the joint call's
 # kernel: up to 4096 one work-group of 256 threads, up to 8192 one of 512, beyond that two passes.
 MATRICES = [
+    # few rows: a row has a CU to itself up to 256 of them; the loss alone holds rows in registers up
+    # to 128 rows beyond 81,920 elements of 16 bits
+    ("bf16", 256, 32003, 0, 1), ("fp16", 257, 32003, 0, 1), ("bf16", 128, 90001, 1, 0),
+    ("fp16", 129, 90001, 0, 1), ("fp32", 128, 50021, 0, 1), ("fp32", 400, 16001, 0, 1),
+    ("bf16", 300, 100003, 0, 0),
+    # more
     ("bf16", 600, 5003, 0, 1), ("fp16", 600, 31999, 1, 0), ("fp32", 600, 16001, 3, 1),
     ("bf16", 530, 50021, 0, 3), ("fp32", 530, 32003, 0, 1),
     ("fp16", 520, 100003, 5, 0),                                  # two passes, whole rows
@@ -137,28 +144,25 @@ def test_distill_of_large_matrices(dtype, rows, vocab, pad, shift, k, tail):
     gd = torch.from_numpy(g).cuda()
     si, sv = _pick(tid, some).cpu().numpy(), _pick(tv, some).cpu().numpy()
     f = dict(dtype=torch.float32, device="cuda")
-    for joint in (False, True):
-        what = f"distill {dtype} {rows} x {vocab} k={k} tail={tail} {'joint' if joint else 'apart'}"
+    for form in ("apart", "joint", "joint, in place"):
+        what = f"distill {dtype} {rows} x {vocab} k={k} tail={tail} {form}"
         say(what)
         loss, stats = torch.full((rows,), 55.0, **f), torch.full((rows, 4), 55.0, **f)
-        out, whole = _gradient_like(x, pad, shift)
-        if joint:
-            F.distill_topk_loss_grad(x, tid, tv, gd, loss, stats, out, tail=tail)
+        if form == "joint, in place":
+            out, whole = x, None
         else:
+            out, whole = _gradient_like(x, pad, shift)
+        if form == "apart":
             F.distill_topk(x, tid, tv, loss, stats, tail=tail)
             F.distill_topk_grad(x, tid, tv, stats, gd, out, tail=tail)
+        else:
+            F.distill_topk_loss_grad(x, tid, tv, gd, loss, stats, out, tail=tail)
         assert not (loss == 55).any() and not (stats == 55).any(), f"{what}: not written"
         C.check_distill(x64, si, sv, 1.0, tail, _np(_pick(loss, some)), _np(_pick(stats, some)),
                         what)
         C.check_distill_grad(x64, si, sv, g[some], 1.0, tail, dtype, _np(_pick(out, some)), what)
-        _check_written(out, whole, pad, shift, what)
-    say(f"{what}, in place")
-    loss2, stats2 = torch.empty(rows, **f), torch.empty(rows, 4, **f)
-    F.distill_topk_loss_grad(x, tid, tv, gd, loss2, stats2, x, tail=tail)
-    bits = torch.int32 if dtype == "fp32" else torch.int16
-    for a, b in ((loss, loss2), (stats, stats2)):
-        assert torch.equal(a.view(torch.int32), b.view(torch.int32)), what
-    assert torch.equal(x.view(bits), out.view(bits)), what
+        if whole is not None:
+            _check_written(out, whole, pad, shift, what)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
