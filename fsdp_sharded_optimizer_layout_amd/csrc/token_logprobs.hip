@@ -166,9 +166,10 @@ __device__ int block_count(int n, TopScratch<Threads>& sh) {
     return total;
 }
 
-// More candidates than fit (many equal values, or the best ones in few threads): find the k-th
-// largest value's key by bisection with counting passes over the part, then take what is above it
-// and, of the equal ones, the lowest indices.  Slow and exact.
+// More candidates than fit (many equal values, the best ones in few threads, or a row so short that
+// fewer than k threads have any of it): find the k-th largest value's key by bisection with counting
+// passes over the part, then take what is above it and, of the equal ones, the lowest indices.  Slow
+// and exact.
 template <typename T, int Threads>
 __device__ void collect_exactly(const Row<T>& row, const Part& part, int k, uint32_t lo_key,
                                 float top, TopScratch<Threads>& sh) {
@@ -585,6 +586,20 @@ bool worth_splitting(int64_t rows, int64_t vocab, int32_t top_k) {
     return rows <= 32 && vocab > 65536 && top_k <= 32;
 }
 
+// Threads of a work-group that takes a whole row.  A list of k alternatives needs its threshold from
+// more than k of the 256 maxima, and 1024 threads have one for each four vectors: a row that fills
+// fewer than 5 k / 4 of them takes 256 threads, with one for each vector, before most of its elements
+// become candidates and the exact search starts.  Measured on bf16, us with 1024 threads and with 256:
+// 64 x 2000 with 64 alternatives 37.0 and 8.5, with 128 38.0 and 10.4; 64 x 4000 with 64 10.0 and 8.7,
+// with 128 42.8 and 11.6; 64 x 8000 with 128 10.8 and 12.5; fp32 64 x 2000 with 128 35.8 and 16.5,
+// 64 x 4000 11.9 and 18.0.  Rows of at most k vectors have too few maxima either way, and 1024 threads
+// are the better at ranking every element: 64 x 700 with 128 22.9 and 36.1 (64 x 1000, which has more
+// elements than candidates fit, 37.4 and 32.5).
+int row_threads(int64_t rows, int64_t vecs, int32_t top_k) {
+    const bool short_row = vecs > top_k && vecs < 5 * static_cast<int64_t>(top_k);
+    return rows <= kWideRows && !short_row ? 1024 : kBlock;
+}
+
 // The largest work-group is for matrices that fit a cache.
 template <typename T, bool Top>
 const void* logprobs_form(int threads, bool once) {
@@ -634,7 +649,7 @@ extern "C" int token_logprobs(const fsdpshard_logits* logits, const int64_t* ids
     const Cut whole = whole_rows(logits->vocab, element_bytes(logits->dtype));
     if (whole.part_vecs <= kMaxPartVecs && !worth_splitting(rows, logits->vocab, top_k)) {
         cut = whole;
-        threads = rows <= kWideRows ? 1024 : kBlock;
+        threads = row_threads(rows, whole.part_vecs, top_k);
     }
     LogprobParams p{};
     p.x = logits->data;

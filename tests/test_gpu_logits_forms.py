@@ -203,3 +203,21 @@ def test_largest_vocabulary(dtype):
         C.check_distill(x64, tid, tv, 1.0, True, _np(loss), _np(stats), dtype)
         C.check_distill_grad(x64, tid, tv, g, 1.0, True, dtype, _np(out), dtype)
         C.assert_between_rows_untouched(out, whole, dtype)
+
+
+# Vectors a row, at both sides of five for each alternative: the number of threads changes there, and
+# short rows have fewer maxima than alternatives.
+@pytest.mark.parametrize("dtype,vocab,k", [("bf16", 5106, 128), ("bf16", 5098, 128),
+                                           ("fp16", 2554, 64), ("bf16", 2546, 64),
+                                           ("fp32", 2557, 128), ("fp32", 2553, 128),
+                                           ("bf16", 801, 20), ("bf16", 769, 128),
+                                           ("fp32", 900, 128)])
+def test_lists_of_short_rows(dtype, vocab, k):
+    rng = np.random.default_rng([vocab, k])
+    t, x64 = C.to_dtype(C.special_rows(rng, vocab, dtype), dtype)
+    ids = np.where(np.arange(16) % 3 == 0, -1, np.arange(16) % vocab)
+    for pad, shift in ((0, 0), (3, 1)):
+        x, _ = C.on_device(t, pad, shift)
+        say(f"lists of short rows {dtype} {vocab} k={k} shift={shift}")
+        got = C.run_logprobs(x, ids, 1.0, k)
+        C.check_logprobs(x64, ids, 1.0, k, C.host(got), f"{dtype} {vocab} k={k} shift={shift}")
