@@ -863,12 +863,14 @@ WholeKernel whole_kernel(const DistillParams& p, int32_t dtype, bool once) {
     return {nullptr, 0, 0};
 }
 
-// Loss and gradient in two passes, few rows: the gradient joins the parts by itself (one launch less)
-// for matrices of up to 32 MiB, and beyond where the loss would give each row to one work-group.
-// Measured with 16 places, joined in the gradient and by the loss, us: fp32 32 x 131072 17.5 and
-// 20.4, 64 rows 28.2 and 27.8, 256 rows 84 and 77, 512 rows 153 and 142; bf16 64 x 131072 19.7 and
-// 24.0, 256 rows 47.1 and 46.0, 512 rows 84 and 90 (rows of one work-group).
-constexpr int64_t kJoinRows = 512, kJoinBytes = int64_t{32} << 20;
+// Loss and gradient in two passes, small matrices: the gradient joins the rows' parts by itself, one
+// launch less.  Measured with 16 places, us joined in the gradient and after a loss of its own: fp32
+// 32 x 131072 17.4 and 20.8, 64 rows (32 MiB) 28.1 and 28.5, 128 rows 45.7 and 43.1, 256 rows 82 and
+// 76; 128 x 40000 18.6 and 21.1, 192 rows (29 MiB) 26.5 and 24.3; bf16 64 x 131072 19.8 and 23.7, 128
+// rows (32 MiB) 28.9 and 29.3, 256 rows 47.7 and 46.8, 512 rows 83 and 73; 256 x 80000 (39 MiB) 32.1
+// and 33.2, 384 rows 42.7 and 39.3.  Rows that take two passes have more than 128 KiB, so that no more
+// than kJoinRows of them are in kJoinBytes.
+constexpr int64_t kJoinRows = 256, kJoinBytes = int64_t{32} << 20;
 static_assert(kWantUnits / kJoinRows >= 2, "rows whose parts the gradient joins are cut");
 
 // The sets of the rows' parts.
@@ -1000,10 +1002,9 @@ extern "C" int distill_topk_loss_grad(const fsdpshard_logits* logits,
     if (whole.kernel)
         return launch_units(whole.kernel, rows, p, whole.map_bytes, stream, whole.threads);
     // Otherwise two passes.  The second finds the logits in the last-level cache if that holds them.
-    // Few rows, unless in place: the parts' sets, which the gradient joins by itself.
+    // A small matrix, unless in place: the parts' sets, which the gradient joins by itself.
     if (rows <= kJoinRows && !in_place &&
-        (rows * logits->vocab * element_bytes(logits->dtype) <= kJoinBytes ||
-         whole_kernel<false>(p, logits->dtype, false).kernel != nullptr)) {
+        rows * logits->vocab * element_bytes(logits->dtype) <= kJoinBytes) {
         rc = launch_parts(p, logits->dtype, false, workspace, stream);
         if (rc != FSDPSHARD_OK) return rc;
         return launch_distill_grad(p, logits->dtype, true, stream);
