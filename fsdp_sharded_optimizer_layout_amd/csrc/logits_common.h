@@ -702,8 +702,13 @@ const void* by_dtype(int32_t dtype, Get get) {
 // How rows are cut into parts.  Vectors a row may have, whatever its phase: ceil((vocab + E - 1) /
 // E).  A part has at most kMaxPartVecs (what a work-group keeps for its part in LDS is sized for
 // that), and where rows are few they are cut further, for about kWantUnits work-groups, but not
-// below kMinPartVecs vectors.
-constexpr int64_t kWantUnits = 1024;
+// below kMinPartVecs vectors.  Measured, us: for 256, 512 and 1024 work-groups, log probabilities with
+// 20 alternatives of bf16 16 x 262144 14.4, 15.3, 15.3, 64 rows 21.5, 20.0, 21.9, 128 rows 29.8, 26.4,
+// 26.8, 4 x 2097149 18.1, 19.8, 26.9, of fp32 64 x 131072 18.9, 18.3, 20.4; the distillation loss of
+// bf16 128 x 262144 22.4, 19.2, 20.9.  With at least 512, 1024 and 2048 vectors, log probabilities of
+// fp32 16 x 131072 16.7, 13.9, 13.3, bf16 1 x 131072 12.6, 13.0, 13.7; loss and gradient of bf16 16 x
+// 131072 12.6, 12.3, 13.2.
+constexpr int64_t kWantUnits = 512;
 constexpr int64_t kMinPartVecs = 1024;
 
 struct Cut {
