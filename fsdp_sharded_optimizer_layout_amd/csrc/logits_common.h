@@ -746,10 +746,12 @@ Cut whole_rows(int64_t vocab, int elem) {
     return {1, static_cast<int32_t>((vocab + 2 * per - 2) / per)};
 }
 
-// Matrices of at least this size are loaded without keeping them in a cache (stream).  Measured, with
-// three inputs in turn: 8192 x 32000 bf16 (524 MB) 97 us with plain loads, 87 without keeping;
-// 4096 x 32000 (262 MB) 58 and 53.  On one input again and again, which the 256 MB last-level cache
-// then holds, the second is 46 and 47, and below 100 MB the two are alike.
+// Matrices of at least this size are loaded without keeping them in a cache (stream).  Measured on bf16
+// with three inputs in turn, us with plain loads and without keeping: log probabilities, 8192 x 32000
+// (524 MB) 95.3 and 87.8, 4096 x 32000 (262 MB) 50.7 and 46.3, 2200 x 32000 (141 MB) 30.5 and 27.8, 2000
+// x 32000 (128 MB) 27.5 and 25.7, 1024 x 32000 (66 MB) 14.3 and 15.1; 4096 x 131072 with 64 alternatives
+// 206 and 183; distillation, loss of 4096 x 32000 53.1 and 49.0, loss and gradient of 8192 x 32000 192
+// and 186.
 constexpr int64_t kOnceBytes = int64_t{1} << 27;
 constexpr int64_t kLastLevelBytes = int64_t{1} << 28;
 

@@ -579,9 +579,11 @@ __global__ __launch_bounds__(kBlock) void logprobs_grad_kernel(LogprobGradParams
 
 // A row that a work-group could take whole is cut all the same where very few long rows leave most
 // CUs idle: one CU needs 10 us for the arithmetic of 131,072 elements.  Joining the parts' lists costs
-// more the longer they are.  Measured on 131,072 bf16: 1 row with 20 alternatives 16.1 us whole, 13.0
-// cut, 16 rows 16.8 and 13.8, 64 rows 16.9 and 18.5; with 100 alternatives 17.0 and 21.5; on 65,536
-// elements 11.7 and 12.5.
+// more the longer they are.  Measured, us whole and cut: 131,072 bf16 with 20 alternatives, 1 row 15.7
+// and 13.0, 16 rows 16.2 and 13.7, 32 rows 16.4 and 15.8, 64 rows 16.7 and 16.8; 32 rows with 32
+// alternatives 16.4 and 16.2, with 40 16.4 and 16.7, with 64 16.7 and 19.9, with none 11.3 and 10.3; 16
+// rows with 20 of 100,000 16.2 and 13.4, of 80,000 14.1 and 13.4, of 65,536 11.9 and 12.8 (with none of
+// 80,000 9.4 and 10.2); fp32 16 rows with 20 of 66,000 14.2 and 12.4, of 50,000 11.8 and 12.1.
 bool worth_splitting(int64_t rows, int64_t vocab, int32_t top_k) {
     return rows <= 32 && vocab > 65536 && top_k <= 32;
 }
