@@ -13,7 +13,8 @@ and in include/fsdpshard_logits.h:
   token_logprobs    log probabilities of given tokens, entropies, top alternatives (GPU)
   distill_topk      divergence from a teacher's top logits (GPU); both with their gradients
 bf16 tensors may be torch.bfloat16, torch.int16 or torch.uint16 (bit patterns); fp32 tensors
-are torch.float32.  All device tensors must be contiguous.
+are torch.float32.  All device tensors must be contiguous, but for the matrices of the operators over
+logits (logits, their gradients, a teacher's lists), whose rows may lie any distance apart.
 """
 
 import ctypes
@@ -717,8 +718,8 @@ def token_logprobs(logits, ids=None, logprob=None, entropy=None, stats=None, top
     distance apart): the log probability of its token into ``logprob`` (float32), the entropy into
     ``entropy`` (float32), the maximum and log-sum the gradient needs into ``stats`` (float32
     [rows, 2]) and the K largest into ``top_ids`` (int32 [rows, K]) and ``top_logprobs`` (float32
-    [rows, K]).  Outputs left out are not computed.  ``ids`` (int64): below 0 is a position
-    without a token.  ``scale``: inverse temperature.  ``workspace``: device tensor of at least
+    [rows, K]).  Any of them may be left out; a call without lists takes less time, one without the
+    others does not.  ``ids`` (int64): below 0 is a position without a token.  ``scale``: inverse temperature.  ``workspace``: device tensor of at least
     token_logprobs_workspace_bytes(rows, vocab, K) bytes (allocated here through PyTorch when
     omitted, and then safe to use with any ``stream``)."""
     import torch
