@@ -719,9 +719,10 @@ def token_logprobs(logits, ids=None, logprob=None, entropy=None, stats=None, top
     ``entropy`` (float32), the maximum and log-sum the gradient needs into ``stats`` (float32
     [rows, 2]) and the K largest into ``top_ids`` (int32 [rows, K]) and ``top_logprobs`` (float32
     [rows, K]).  Any of them may be left out; a call without lists takes less time, one without the
-    others does not.  ``ids`` (int64): below 0 is a position without a token.  ``scale``: inverse temperature.  ``workspace``: device tensor of at least
-    token_logprobs_workspace_bytes(rows, vocab, K) bytes (allocated here through PyTorch when
-    omitted, and then safe to use with any ``stream``)."""
+    others does not.  ``ids`` (int64): below 0 is a position without a token.  ``scale``: inverse
+    temperature.  ``workspace``: device tensor of at least token_logprobs_workspace_bytes(rows, vocab,
+    K) bytes (allocated here through PyTorch when omitted, and then safe to use with any
+    ``stream``)."""
     import torch
     x = _logits(logits, scale)
     f32, rows, dev, k, h = torch.float32, x.rows, logits.get_device(), 0, lib()

@@ -11,9 +11,10 @@
  * The conventions of fsdpshard.h hold: device pointers owned by the caller, no allocation, no
  * memset, no synchronisation (so every call can be captured in a HIP graph), argument errors found
  * before anything is enqueued, a status returned.  A call enqueues one to three kernels (each in
- * several launches where a matrix has more than 2^20 rows or parts of rows).  Results do not
- * depend on the launch: sums have a fixed order, and there are no atomic additions of
- * floating-point values.
+ * several launches where a matrix has more than 2^20 rows or parts of rows).  The same call gives the
+ * same bits each time: sums have a fixed order, and there are no atomic additions of floating-point
+ * values.  A row's last bits may differ between calls that differ in the number of rows, in
+ * alignment, or in whether the gradient is written in place, since they may take different kernels.
  *
  * Logits.  A matrix of `rows` rows of `vocab` values, `row_stride` elements apart, in bf16, fp16
  * or fp32.  With x a row, c = scale (an inverse temperature) and m = max x:
@@ -105,7 +106,9 @@ int token_logprobs(const fsdpshard_logits* logits, const int64_t* ids, float* lo
  * token_logprobs_grad -- dlogits for gradients of the log probability (g) and the entropy (h):
  *     dx_i = c (g ([i = token] - p_i) - h p_i (log p_i + H))
  * One rounding to the logits' type.  g counts only where the row has a token; a row whose g and h
- * are both 0 gets zeros whatever its logits hold.
+ * are both 0 gets zeros whatever its logits hold, and any other row whose id is >= vocab gets NaN.
+ * The products g c and h c are float32 and have to be finite: beyond that a row holds infinities and
+ * NaN (as in distill_topk_grad).
  *   stats, entropy  as token_logprobs wrote them for the same logits and scale; entropy may be
  *                   NULL when dentropy is
  *   dlogprob        device, rows floats (g), or NULL (0 everywhere; then ids may be NULL too)
@@ -138,6 +141,9 @@ int distill_topk(const fsdpshard_logits* logits, const fsdpshard_teacher* teache
  *     dx_i = g c ((Q + q_t) p_i - q_i)            for a token of the list
  *     dx_i = g c ((Q + q_t) p_i - q_t p_i / p_t)  for any other (q_t = 0 with tail = 0)
  * One rounding to the logits' type.  A row whose g is 0 gets zeros whatever its logits hold.
+ * The log-sums come from `stats` in float32, so that each p is off by up to 2^-24 L of itself, and
+ * p_i / p_t by as much of its own log-sum.  The two terms of a token outside the list cancel where the
+ * student's mass there is close to the teacher's, and what is left of them is that much less exact.
  *   stats    as distill_topk wrote them for the same logits, teacher and scale
  *   dloss    device, rows floats (g)
  *   dlogits  as for token_logprobs_grad
@@ -150,7 +156,10 @@ int distill_topk_grad(const fsdpshard_logits* logits, const fsdpshard_teacher* t
 /*
  * distill_topk_loss_grad -- distill_topk and distill_topk_grad in one call, for a loss whose
  * weights are known beforehand.  `stats` is required (it is written and read); the other
- * arguments and the errors are those of the two calls.
+ * arguments and the errors are those of the two calls.  Rows of up to 65,536 16-bit or 32,768 32-bit
+ * elements (a few less where rows do not start at 16 bytes) are read once; their log-sums, and those of
+ * longer rows of small matrices (up to 32 MiB, not in place), stay in float64 up to the gradient.  Any
+ * others go through `stats` as in the two calls.
  */
 int distill_topk_loss_grad(const fsdpshard_logits* logits, const fsdpshard_teacher* teacher,
                            const float* dloss, float* loss, float* stats, void* dlogits,
