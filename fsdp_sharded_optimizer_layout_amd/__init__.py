@@ -12,9 +12,15 @@ Calls (same names as the C ABI in include/fsdpshard.h):
 and in include/fsdpshard_logits.h:
   token_logprobs    log probabilities of given tokens, entropies, top alternatives (GPU)
   distill_topk      divergence from a teacher's top logits (GPU); both with their gradients
+and in include/fsdpshard_policy.h:
+  policy_loss       clipped policy loss over log probabilities (GPU), also straight over logits
+  preference_loss   loss over pairs of sequences (GPU); all with their gradients
+and in include/fsdpshard_embedding.h:
+  embedding_lookup  rows of a table for given tokens (GPU), and embedding_grad, its gradient
 bf16 tensors may be torch.bfloat16, torch.int16 or torch.uint16 (bit patterns); fp32 tensors
 are torch.float32.  All device tensors must be contiguous, but for the matrices of the operators over
-logits (logits, their gradients, a teacher's lists), whose rows may lie any distance apart.
+logits (logits, their gradients, a teacher's lists) and of the embedding, whose rows may lie any
+distance apart.
 """
 
 import ctypes
@@ -58,6 +64,22 @@ class _Logits(ctypes.Structure):
 class _Teacher(ctypes.Structure):
     _fields_ = [("ids", c_vp), ("values", c_vp), ("row_stride", c_i64), ("k", c_i32),
                 ("tail", c_i32)]
+
+
+class _Policy(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("dual_clip", ctypes.c_double), ("kl_coef", ctypes.c_double),
+                ("entropy_coef", ctypes.c_double)]
+
+
+class _Preference(ctypes.Structure):
+    _fields_ = [("kind", c_i32), ("length_normalised", c_i32), ("beta", ctypes.c_double),
+                ("margin", ctypes.c_double), ("label_smoothing", ctypes.c_double)]
+
+
+class _Matrix(ctypes.Structure):
+    _fields_ = [("data", c_vp), ("rows", c_i64), ("cols", c_i64), ("row_stride", c_i64),
+                ("dtype", c_i32)]
 
 
 class _Piece(ctypes.Structure):
@@ -146,6 +168,23 @@ def lib():
     h.distill_topk.argtypes = [pl, pt, c_vp, c_vp, c_vp, c_i64, c_vp]
     h.distill_topk_grad.argtypes = [pl, pt, c_vp, c_vp, c_vp, c_i64, c_vp]
     h.distill_topk_loss_grad.argtypes = [pl, pt, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]
+    pp, pm = ctypes.POINTER(_Policy), ctypes.POINTER(_Matrix)
+    h.policy_loss_workspace_bytes.argtypes = [c_i64, c_i64]
+    h.policy_loss_workspace_bytes.restype = c_i64
+    h.policy_loss.argtypes = [pp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp,
+                              c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]
+    h.preference_loss_workspace_bytes.argtypes = [c_i64, c_i64]
+    h.preference_loss_workspace_bytes.restype = c_i64
+    h.preference_loss.argtypes = [ctypes.POINTER(_Preference), c_i64, c_i64, c_vp, c_vp, c_vp,
+                                  c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]
+    h.policy_logits_loss_grad_workspace_bytes.argtypes = [c_i64, c_i64]
+    h.policy_logits_loss_grad_workspace_bytes.restype = c_i64
+    h.policy_logits_loss_grad.argtypes = [pl, c_vp, pp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                          c_vp, c_i64, c_vp, c_i64, c_vp]
+    h.embedding_lookup.argtypes = [pm, c_vp, pm, ctypes.c_float, c_vp]
+    h.embedding_grad_workspace_bytes.argtypes = [c_i64, c_i64, c_i64]
+    h.embedding_grad_workspace_bytes.restype = c_i64
+    h.embedding_grad.argtypes = [c_vp, pm, pm, ctypes.c_float, c_i32, c_vp, c_i64, c_vp]
     h.fsdpshard_strerror.argtypes = [ctypes.c_int]
     h.fsdpshard_strerror.restype = ctypes.c_char_p
     h.fsdpshard_abi_version.argtypes = []
@@ -172,7 +211,9 @@ def lib():
                  "reduce_shard_sumsq_interleaved",
                  "state_to_blocked", "state_from_blocked",
                  "token_logprobs", "token_logprobs_grad",
-                 "distill_topk", "distill_topk_grad", "distill_topk_loss_grad"):
+                 "distill_topk", "distill_topk_grad", "distill_topk_loss_grad",
+                 "policy_loss", "preference_loss", "policy_logits_loss_grad",
+                 "embedding_lookup", "embedding_grad"):
         getattr(h, name).restype = ctypes.c_int
     _lib_handle = h
     return h
@@ -815,6 +856,185 @@ def distill_topk_loss_grad(logits, teacher_ids, teacher_values, dloss, loss, sta
     _enqueue("distill_topk_loss_grad", h.distill_topk_loss_grad, dev, stream,
              (x, t, _of(dloss, "dloss", f32, rows, dev), _of(loss, "loss", f32, rows, dev),
               _of(stats, "stats", f32, 4 * rows, dev), out, ostride, ws, wbytes))
+
+
+# ------------------------------------------------------------------------------ policy, preferences
+
+PREFERENCE_KINDS = {"logistic": 0, "hinge": 1, "squared": 2}
+
+
+def _vector(t, what, dtype, device=None):
+    """(pointer, elements, device) of a contiguous 1-D device tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dim() != 1 or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous one-dimensional tensor of {dtype}")
+    if device is not None and t.get_device() != device:
+        raise ValueError("all tensors of a call must be on one device")
+    return t.data_ptr(), t.shape[0], t.get_device()
+
+
+def _given_workspace(workspace, need, device, stream):
+    """(pointer, bytes, tensor) of a call's workspace; allocated through PyTorch when omitted."""
+    if need < 0:
+        raise ValueError("sizes out of range")
+    return _row_workspace(workspace, need, device, stream)
+
+
+def policy_loss_workspace_bytes(tokens, sequences=0):
+    return int(lib().policy_loss_workspace_bytes(int(tokens), int(sequences)))
+
+
+def policy_loss(logprob, advantage, weight, dlogprob=None, loss=None, totals=None, counts=None,
+                old_logprob=None, ref_logprob=None, entropy=None, dentropy=None, offsets=None,
+                clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, entropy_coef=0.0,
+                workspace=None, stream=None):
+    """Clipped policy loss of packed tokens (see fsdpshard_policy.h): float32 tensors of one
+    element a token.  ``weight`` carries the mean's divisor, and 0 leaves a token out;
+    ``old_logprob`` omitted: the policy's own.  With ``offsets`` (int64, a sequence's start each and
+    the last one's end) a sequence's tokens share one ratio.  Written where given: ``loss``, the
+    gradients ``dlogprob`` and ``dentropy`` (what token_logprobs_grad takes), ``totals`` (float32 [4]:
+    loss, policy part, KL, entropy) and ``counts`` (int64 [2]: tokens counted, tokens clipped).
+    ``workspace``: at least policy_loss_workspace_bytes(tokens, sequences) bytes (allocated here
+    through PyTorch when omitted)."""
+    import torch
+    f32, h = torch.float32, lib()
+    lp, n, dev = _vector(logprob, "logprob", f32)
+    sequences, at = 0, None
+    if offsets is not None:
+        at, sequences, _ = _vector(offsets, "offsets", torch.int64, dev)
+        sequences -= 1
+        if sequences < 1:
+            raise ValueError("offsets needs an element more than there are sequences")
+    if kl_coef and ref_logprob is None:
+        raise ValueError("kl_coef needs ref_logprob")
+    if entropy_coef and entropy is None:
+        raise ValueError("entropy_coef needs entropy")
+    ws, wbytes, workspace = _given_workspace(
+        workspace, h.policy_loss_workspace_bytes(n, sequences), dev, stream)
+    terms = _Policy(clip_low, clip_high, dual_clip, kl_coef, entropy_coef)
+    _enqueue("policy_loss", h.policy_loss, dev, stream,
+             (terms, n, lp, _of(old_logprob, "old_logprob", f32, n, dev),
+              _of(ref_logprob, "ref_logprob", f32, n, dev), _of(entropy, "entropy", f32, n, dev),
+              _of(advantage, "advantage", f32, n, dev), _of(weight, "weight", f32, n, dev),
+              sequences, at, _of(loss, "loss", f32, n, dev),
+              _of(dlogprob, "dlogprob", f32, n, dev), _of(dentropy, "dentropy", f32, n, dev),
+              _of(totals, "totals", f32, 4, dev), _of(counts, "counts", torch.int64, 2, dev),
+              ws, wbytes))
+
+
+def preference_loss_workspace_bytes(tokens, pairs):
+    return int(lib().preference_loss_workspace_bytes(int(tokens), int(pairs)))
+
+
+def preference_loss(logprob, offsets, loss, rewards=None, ref_logprob=None, weight=None, dloss=None,
+                    dlogprob=None, kind="logistic", beta=0.1, margin=0.0, label_smoothing=0.0,
+                    length_normalised=False, workspace=None, stream=None):
+    """Loss over pairs of packed sequences (see fsdpshard_policy.h): pair p is the chosen sequence
+    2p and the rejected one 2p + 1 of ``offsets`` (int64 [2 pairs + 1]).  ``logprob``,
+    ``ref_logprob`` (omitted: 0), ``weight`` (omitted: 1; 0 leaves a token out) and the gradient
+    ``dlogprob`` have one float32 element a token, ``loss`` and its gradient ``dloss`` one a pair,
+    ``rewards`` [pairs, 2].  ``kind``: "logistic", "hinge" or "squared".  ``workspace``: at least
+    preference_loss_workspace_bytes(tokens, pairs) bytes (allocated here through PyTorch when
+    omitted)."""
+    import torch
+    f32, h = torch.float32, lib()
+    lp, n, dev = _vector(logprob, "logprob", f32)
+    at, entries, _ = _vector(offsets, "offsets", torch.int64, dev)
+    if entries % 2 == 0:
+        raise ValueError("offsets needs two elements for each pair and one more")
+    if kind not in PREFERENCE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(PREFERENCE_KINDS)}")
+    if (dloss is None) != (dlogprob is None):
+        raise ValueError("give both of dloss and dlogprob, or neither")
+    pairs = entries // 2
+    ws, wbytes, workspace = _given_workspace(
+        workspace, h.preference_loss_workspace_bytes(n, pairs), dev, stream)
+    terms = _Preference(PREFERENCE_KINDS[kind], 1 if length_normalised else 0, beta, margin,
+                        label_smoothing)
+    _enqueue("preference_loss", h.preference_loss, dev, stream,
+             (terms, n, pairs, at, lp, _of(ref_logprob, "ref_logprob", f32, n, dev),
+              _of(weight, "weight", f32, n, dev), _of(dloss, "dloss", f32, pairs, dev),
+              _of(loss, "loss", f32, pairs, dev), _of(rewards, "rewards", f32, 2 * pairs, dev),
+              _of(dlogprob, "dlogprob", f32, n, dev), ws, wbytes))
+
+
+def policy_logits_loss_grad_workspace_bytes(rows, vocab):
+    return int(lib().policy_logits_loss_grad_workspace_bytes(int(rows), int(vocab)))
+
+
+def policy_logits_loss_grad(logits, ids, advantage, weight, loss, dlogits, logprob=None,
+                            entropy=None, old_logprob=None, ref_logprob=None, clip_low=0.2,
+                            clip_high=0.2, dual_clip=0.0, kl_coef=0.0, entropy_coef=0.0, scale=1.0,
+                            workspace=None, stream=None):
+    """token_logprobs, policy_loss (a ratio for each token) and token_logprobs_grad in one call:
+    ``loss`` and, where given, ``logprob`` and ``entropy`` of every row of ``logits``, and the
+    gradient of the sum of the losses into ``dlogits`` (may be ``logits`` itself).  A row whose id
+    is below 0 or whose weight is 0 gives zeros.  ``workspace``: at least
+    policy_logits_loss_grad_workspace_bytes(rows, vocab) bytes (allocated here through PyTorch when
+    omitted)."""
+    import torch
+    x = _logits(logits, scale)
+    f32, rows, dev, h = torch.float32, x.rows, logits.get_device(), lib()
+    out, ostride = _dlogits(dlogits, logits, dev)
+    if kl_coef and ref_logprob is None:
+        raise ValueError("kl_coef needs ref_logprob")
+    ws, wbytes, workspace = _given_workspace(
+        workspace, h.policy_logits_loss_grad_workspace_bytes(rows, x.vocab), dev, stream)
+    terms = _Policy(clip_low, clip_high, dual_clip, kl_coef, entropy_coef)
+    _enqueue("policy_logits_loss_grad", h.policy_logits_loss_grad, dev, stream,
+             (x, _of(ids, "ids", torch.int64, rows, dev), terms,
+              _of(old_logprob, "old_logprob", f32, rows, dev),
+              _of(ref_logprob, "ref_logprob", f32, rows, dev),
+              _of(advantage, "advantage", f32, rows, dev), _of(weight, "weight", f32, rows, dev),
+              _of(loss, "loss", f32, rows, dev), _of(logprob, "logprob", f32, rows, dev),
+              _of(entropy, "entropy", f32, rows, dev), out, ostride, ws, wbytes))
+
+
+# ------------------------------------------------------------------------------ embedding
+
+def _matrix_arg(t, what, device=None):
+    ptr, rows, cols, stride = _matrix(t, what, _logits_dtypes(), device)
+    return _Matrix(ptr, rows, cols, stride, _LOGITS_DTYPES[t.dtype])
+
+
+def embedding_lookup(table, ids, out, scale=1.0, stream=None):
+    """out[t] = scale * table[ids[t]]: ``table`` [vocab, dim] and ``out`` [tokens, dim], each bf16,
+    fp16 or fp32, rows contiguous but any distance apart, at any alignment of the element (a
+    tensor's place in the flat vector).  ``ids`` (int64 [tokens]): below 0 gives zeros, past the
+    table NaN."""
+    import torch
+    x = _matrix_arg(table, "table")
+    dev = table.get_device()
+    y = _matrix_arg(out, "out", dev)
+    if y.cols != x.cols:
+        raise ValueError("table and out must have the same number of columns")
+    _enqueue("embedding_lookup", lib().embedding_lookup, dev, stream,
+             (x, _of(ids, "ids", torch.int64, y.rows, dev), y, scale))
+
+
+def embedding_grad_workspace_bytes(tokens, vocab, dim):
+    return int(lib().embedding_grad_workspace_bytes(int(tokens), int(vocab), int(dim)))
+
+
+def embedding_grad(ids, dout, dtable, scale=1.0, accumulate=False, workspace=None, stream=None):
+    """Gradient of embedding_lookup's table for the gradient ``dout`` [tokens, dim] of its result:
+    every row of ``dtable`` [vocab, dim] is set to scale times the sum of dout's rows of its tokens
+    (zeros without any), or with ``accumulate`` that sum is added to it.  Each bf16, fp16 or fp32,
+    rows contiguous but any distance apart.  ``ids`` (int64 [tokens]): outside the table, no part.
+    ``workspace``: at least embedding_grad_workspace_bytes(tokens, vocab, dim) bytes (allocated here
+    through PyTorch when omitted)."""
+    import torch
+    h, x = lib(), _matrix_arg(dout, "dout")
+    dev = dout.get_device()
+    y = _matrix_arg(dtable, "dtable", dev)
+    if y.cols != x.cols:
+        raise ValueError("dout and dtable must have the same number of columns")
+    ws, wbytes, workspace = _given_workspace(
+        workspace, h.embedding_grad_workspace_bytes(x.rows, y.rows, x.cols), dev, stream)
+    _enqueue("embedding_grad", h.embedding_grad, dev, stream,
+             (_of(ids, "ids", torch.int64, x.rows, dev), x, y, scale, 1 if accumulate else 0,
+              ws, wbytes))
 
 
 # ------------------------------------------------------------------------------ measurement aids

@@ -24,6 +24,8 @@ ARCH = "gfx950"
 
 HIP_SOURCES = [os.path.join(CSRC, "shard_step.hip"), os.path.join(CSRC, "reshard.hip"),
                os.path.join(CSRC, "token_logprobs.hip"), os.path.join(CSRC, "distill.hip"),
+               os.path.join(CSRC, "embedding.hip"), os.path.join(CSRC, "policy.hip"),
+               os.path.join(CSRC, "policy_logits.hip"),
                os.path.join(CSRC, "calib.hip")]
 HOST_SOURCES = [os.path.join(CSRC, "layout.cpp")]
 

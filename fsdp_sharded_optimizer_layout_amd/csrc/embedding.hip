@@ -1,0 +1,616 @@
+// Embedding of libfsdpshard.so on gfx950: lookup of a table's rows, and the table's gradient by
+// sorted tokens.
+
+#include "logits_common.h"
+
+#include "fsdpshard_embedding.h"
+
+namespace {
+
+// ------------------------------------------------------------------------------------------------
+// Groups of 8 elements: one 16-byte vector of a 16-bit type, two of float32.  Rows may start at any
+// element (a tensor's place in a flat vector): the hardware takes vector accesses at any alignment of
+// the element.
+
+constexpr int kGroup = 8;
+
+typedef u32x4 loose_vec __attribute__((aligned(2)));
+
+template <typename T>
+constexpr int kGroupVecs = kGroup / kElems<T>;
+
+template <typename T>
+struct Group {
+    u32x4 v[kGroupVecs<T>];
+};
+
+template <typename T>
+__device__ __forceinline__ Group<T> load_group(const T* p) {
+    Group<T> g;
+#pragma unroll
+    for (int i = 0; i < kGroupVecs<T>; ++i)
+        g.v[i] = *reinterpret_cast<const loose_vec*>(p + i * kElems<T>);
+    return g;
+}
+
+// The first n elements of a row's last group; zeros after them.
+template <typename T>
+__device__ __forceinline__ Group<T> load_some(const T* p, int n) {
+    using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+    constexpr int PerWord = 4 / static_cast<int>(sizeof(T)), W = kGroup / PerWord;
+    const Bits* b = reinterpret_cast<const Bits*>(p);
+    uint32_t w[W] = {};
+#pragma unroll
+    for (int e = 0; e < kGroup; ++e)
+        if (e < n) w[e / PerWord] |= static_cast<uint32_t>(b[e]) << (e % PerWord * 16);
+    Group<T> g;
+#pragma unroll
+    for (int i = 0; i < W; ++i) g.v[i / 4][i % 4] = w[i];
+    return g;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen_group(const Group<T>& g, float (&x)[kGroup]) {
+#pragma unroll
+    for (int i = 0; i < kGroupVecs<T>; ++i) unpack<T>(g.v[i], x + i * kElems<T>);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_group(T* p, const float (&x)[kGroup]) {
+#pragma unroll
+    for (int i = 0; i < kGroupVecs<T>; ++i)
+        *reinterpret_cast<loose_vec*>(p + i * kElems<T>) = pack<T>(x + i * kElems<T>);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, const float (&x)[kGroup], int n) {
+#pragma unroll
+    for (int e = 0; e < kGroup; ++e)
+        if (e < n) p[e] = narrow<T>(x[e]);
+}
+
+template <typename T>
+__device__ __forceinline__ Group<T> load_any(const T* p, int n) {
+    return n >= kGroup ? load_group(p) : load_some(p, n);
+}
+template <typename T>
+__device__ __forceinline__ void store_any(T* p, const float (&x)[kGroup], int n) {
+    if (n >= kGroup) store_group(p, x);
+    else store_some(p, x, n);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Lookup.  A work-group takes a row's part of kBlock * kLookupGroups groups, or several whole rows
+// where they are short: 2^shift threads a row.
+
+constexpr int kLookupGroups = 2;
+
+struct LookupParams {
+    const void* table;
+    int64_t vocab, tstride;
+    const int64_t* ids;
+    void* out;
+    int64_t tokens, ostride;
+    int32_t dim, splits, shift;
+    float scale;
+    int64_t unit0;
+};
+
+template <typename In, typename Out>
+__global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
+    const int tid = threadIdx.x;
+    const int64_t unit = p.unit0 + unit_of_group();
+    const int64_t first = row_of(unit, p.splits);
+    const int split = static_cast<int>(unit - first * p.splits);
+    const int64_t t = (first << (8 - p.shift)) + (tid >> p.shift);
+    if (t >= p.tokens) return;
+    const int lane = tid & ((1 << p.shift) - 1);
+    const int64_t id = p.ids[t];
+    const bool inside = id >= 0 && id < p.vocab;
+    const In* src = static_cast<const In*>(p.table) + (inside ? id : 0) * p.tstride;
+    Out* dst = static_cast<Out*>(p.out) + t * p.ostride;
+    Group<In> raw[kLookupGroups];
+    int at[kLookupGroups];
+#pragma unroll
+    for (int q = 0; q < kLookupGroups; ++q) {
+        at[q] = (((split * kLookupGroups + q) << p.shift) + lane) * kGroup;
+        if (inside && at[q] < p.dim) raw[q] = load_any(src + at[q], p.dim - at[q]);
+    }
+    const float other = id < 0 ? 0.0f : __builtin_nanf("");
+#pragma unroll
+    for (int q = 0; q < kLookupGroups; ++q) {
+        if (at[q] >= p.dim) break;
+        float x[kGroup];
+        if (inside) {
+            widen_group(raw[q], x);
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) x[e] *= p.scale;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) x[e] = other;
+        }
+        store_any(dst + at[q], x, p.dim - at[q]);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Sorting.  Tokens by their row of the table, equal ones in their order: two stable passes over half
+// of the bits each.  A token without a row gets the key `vocab` and comes last.  A work-group ranks
+// kSortTokens tokens, a wave a quarter of them: counts of its digits, then 64 tokens at a time.
+
+constexpr int kSortRounds = 16;
+constexpr int kSortTokens = kBlock * kSortRounds;
+constexpr int kWaves = kBlock / kWave;
+constexpr int kMaxDigitBits = 11;           // two digits hold 0 .. FSDPSHARD_MAX_VOCAB
+
+struct SortParams {
+    const int64_t* ids;
+    int64_t tokens, vocab;
+    int32_t blocks, shift, bits;            // of this pass
+    uint32_t* counts;                       // [2^bits, blocks]
+    uint32_t* totals;                       // [2^bits]
+    const uint2* in;                        // (key, token), null in the first pass
+    uint2* out;
+    uint32_t *keys, *order;                 // the last pass's results
+    uint8_t* seen;                          // rows that a token names, set to 0 by the first pass
+    int64_t unit0;
+};
+
+__device__ __forceinline__ uint2 sort_item(const SortParams& p, int64_t i) {
+    if (p.in) return p.in[i];
+    const int64_t id = p.ids[i];
+    return make_uint2(static_cast<uint32_t>(id >= 0 && id < p.vocab ? id : p.vocab),
+                      static_cast<uint32_t>(i));
+}
+
+__global__ __launch_bounds__(kBlock) void sort_count_kernel(SortParams p) {
+    __shared__ uint32_t count[1 << kMaxDigitBits];
+    const int tid = threadIdx.x, digits = 1 << p.bits;
+    const int64_t block = p.unit0 + blockIdx.x, base = block * kSortTokens;
+    for (int d = tid; d < digits; d += kBlock) count[d] = 0;
+    if (p.in == nullptr)
+        for (int64_t v = block * kBlock + tid; v < p.vocab;
+             v += static_cast<int64_t>(p.blocks) * kBlock)
+            p.seen[v] = 0;
+    __syncthreads();
+    for (int q = 0; q < kSortRounds; ++q) {
+        const int64_t i = base + q * kBlock + tid;
+        if (i < p.tokens) atomicAdd(&count[(sort_item(p, i).x >> p.shift) & (digits - 1)], 1u);
+    }
+    __syncthreads();
+    for (int d = tid; d < digits; d += kBlock)
+        p.counts[static_cast<int64_t>(d) * p.blocks + block] = count[d];
+}
+
+// Orders the LDS accesses of one wave's lanes (the hardware keeps a wave's in order: this is for the
+// compiler).
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The exclusive sum of x over the work-group's threads; `total` is the sum of all.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sh, uint32_t& total) {
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    uint32_t sum = x;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t y = __shfl_up(sum, d);
+        if (lane >= d) sum += y;
+    }
+    __syncthreads();
+    if (lane == kWave - 1) sh[wave] = sum;
+    __syncthreads();
+    uint32_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) before += sh[w];
+        total += sh[w];
+    }
+    return before + sum - x;
+}
+
+// Each digit's counts become its exclusive sums over the blocks.
+__global__ __launch_bounds__(kBlock) void sort_scan_kernel(SortParams p) {
+    __shared__ uint32_t sh[kWaves];
+    uint32_t* row = p.counts + static_cast<int64_t>(blockIdx.x) * p.blocks;
+    uint32_t run = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += kBlock) {
+        const int b = b0 + threadIdx.x;
+        uint32_t total;
+        const uint32_t x = b < p.blocks ? row[b] : 0, sum = block_scan(x, sh, total);
+        if (b < p.blocks) row[b] = run + sum;
+        run += total;
+    }
+    if (threadIdx.x == 0) p.totals[blockIdx.x] = run;
+}
+
+__global__ __launch_bounds__(kBlock) void sort_place_kernel(SortParams p) {
+    __shared__ uint32_t place[kWaves][1 << kMaxDigitBits];
+    __shared__ uint32_t sh[kWaves];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, digits = 1 << p.bits;
+    const int64_t block = p.unit0 + blockIdx.x;
+    const int64_t base = block * kSortTokens + wave * (kSortRounds * kWave);
+    for (int d = tid; d < digits; d += kBlock)
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) place[w][d] = 0;
+    __syncthreads();
+    uint2 item[kSortRounds];
+#pragma unroll
+    for (int q = 0; q < kSortRounds; ++q) {
+        const int64_t i = base + q * kWave + lane;
+        item[q] = make_uint2(0xFFFFFFFFu, 0);
+        if (i < p.tokens) {
+            item[q] = sort_item(p, i);
+            atomicAdd(&place[wave][(item[q].x >> p.shift) & (digits - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    // Where each wave's first token of each digit goes.
+    uint32_t run = 0;
+    for (int d0 = 0; d0 < digits; d0 += kBlock) {
+        const int d = d0 + tid;
+        uint32_t total;
+        const uint32_t sum = block_scan(d < digits ? p.totals[d] : 0, sh, total);
+        if (d < digits) {
+            uint32_t at = run + sum + p.counts[static_cast<int64_t>(d) * p.blocks + block];
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const uint32_t n = place[w][d];
+                place[w][d] = at;
+                at += n;
+            }
+        }
+        run += total;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSortRounds; ++q) {
+        const int64_t i = base + q * kWave + lane;
+        const bool there = i < p.tokens;
+        const uint32_t d = (item[q].x >> p.shift) & (digits - 1);
+        unsigned long long same = __ballot(there);      // lanes of this digit
+        for (int b = 0; b < p.bits; ++b) {
+            const unsigned long long ones = __ballot((d >> b) & 1);
+            same &= (d >> b) & 1 ? ones : ~ones;
+        }
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        uint32_t at = 0;
+        if (there) {
+            at = place[wave][d] + before;
+            if (p.order) {
+                p.keys[at] = item[q].x;
+                p.order[at] = item[q].y;
+                if (item[q].x < p.vocab) p.seen[item[q].x] = 1;
+            } else {
+                p.out[at] = item[q];
+            }
+        }
+        wave_fence();                                   // every lane has read its place
+        if (there && before == 0) place[wave][d] = at + __popcll(same);
+        wave_fence();
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Gradient.  The sorted tokens are cut into chunks of equal length, whatever rows they name, so that a
+// frequent token's sum is shared like any other's.  2^shift threads own 8 columns each of a chunk and
+// add up its runs of equal tokens: a run inside the chunk goes to the table, a run that comes from the
+// chunk before or goes on in the next one goes to the chunk's `head` or `tail`, which the joining
+// kernel adds up.  Rows without a token are set to zeros by work-groups of the same launch.
+
+constexpr int kAhead = 8;                   // rows of the gradient loaded at once
+constexpr int kFillRows = 16;
+
+struct GradParams {
+    const uint32_t *keys, *order;
+    const uint8_t* seen;
+    const void* dout;
+    int64_t dstride;
+    void* table;
+    int64_t tstride, tokens, vocab;
+    float *head, *tail;                     // [chunks, padded]
+    int32_t dim, padded, chunk, chunks, splits, shift;
+    float scale;
+    int32_t accumulate;
+    int64_t sum_units, unit0;
+};
+
+template <typename Out>
+__device__ __forceinline__ void put_sum(const GradParams& p, uint32_t key, int col,
+                                        float (&sum)[kGroup]) {
+    Out* at = static_cast<Out*>(p.table) + key * p.tstride + col;
+    const int n = p.dim - col;
+#pragma unroll
+    for (int e = 0; e < kGroup; ++e) sum[e] *= p.scale;
+    if (p.accumulate) {
+        float old[kGroup];
+        widen_group(load_any(at, n), old);
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) sum[e] += old[e];
+    }
+    store_any(at, sum, n);
+}
+
+template <typename Out>
+__device__ void fill_rows(const GradParams& p, int64_t unit) {
+    const float zero[kGroup] = {};
+    for (int i = 0; i < kFillRows; ++i) {
+        const int64_t v = unit * kFillRows + i;
+        if (v >= p.vocab) return;
+        if (p.seen[v]) continue;
+        Out* row = static_cast<Out*>(p.table) + v * p.tstride;
+        for (int col = threadIdx.x * kGroup; col < p.dim; col += kBlock * kGroup)
+            store_any(row + col, zero, p.dim - col);
+    }
+}
+
+template <typename In, typename Out>
+__global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
+    const int64_t unit = p.unit0 + blockIdx.x;
+    if (unit >= p.sum_units) {
+        fill_rows<Out>(p, unit - p.sum_units);
+        return;
+    }
+    const int tid = threadIdx.x;
+    const int64_t first = row_of(unit, p.splits);
+    const int split = static_cast<int>(unit - first * p.splits);
+    const int64_t c = (first << (8 - p.shift)) + (tid >> p.shift);
+    const int col = ((split << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
+    if (c >= p.chunks || col >= p.dim) return;
+    const int64_t begin = c * p.chunk;
+    const int64_t end = begin + p.chunk < p.tokens ? begin + p.chunk : p.tokens;
+    const In* src = static_cast<const In*>(p.dout) + col;
+    const uint32_t none = static_cast<uint32_t>(p.vocab);
+    bool comes = begin > 0 && p.keys[begin - 1] == p.keys[begin];
+    float sum[kGroup] = {};
+    for (int64_t j0 = begin; j0 < end; j0 += kAhead) {
+        uint32_t key[kAhead + 1];
+        Group<In> raw[kAhead];
+#pragma unroll
+        for (int q = 0; q <= kAhead; ++q) key[q] = j0 + q < p.tokens ? p.keys[j0 + q] : none;
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (j0 + q < end && key[q] < none)
+                raw[q] = load_any(src + p.order[j0 + q] * p.dstride, p.dim - col);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            if (j0 + q >= end) break;
+            if (key[q] >= none) return;
+            float x[kGroup];
+            widen_group(raw[q], x);
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) sum[e] += x[e];
+            const bool last = j0 + q + 1 == end, goes = key[q + 1] == key[q];
+            if (goes && !last) continue;
+            if (comes || goes) {
+                store_group((comes ? p.head : p.tail) + c * p.padded + col, sum);
+            } else {
+                put_sum<Out>(p, key[q], col, sum);
+            }
+            comes = false;
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) sum[e] = 0.0f;
+        }
+    }
+}
+
+// The sums of runs that cross chunks: the work-group of the chunk in which a run starts adds its tail
+// and the heads of the chunks that follow, in their order.
+template <typename Out>
+__global__ __launch_bounds__(kBlock) void embed_join_kernel(GradParams p) {
+    const int tid = threadIdx.x;
+    const int64_t unit = p.unit0 + blockIdx.x;
+    const int64_t first = row_of(unit, p.splits);
+    const int split = static_cast<int>(unit - first * p.splits);
+    const int64_t c = (first << (8 - p.shift)) + (tid >> p.shift);
+    const int col = ((split << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
+    if (c >= p.chunks || col >= p.dim) return;
+    const int64_t begin = c * p.chunk, end = begin + p.chunk;
+    if (end >= p.tokens) return;
+    const uint32_t key = p.keys[end];
+    if (key >= p.vocab || p.keys[end - 1] != key) return;
+    if (begin > 0 && p.keys[begin - 1] == key) return;      // an earlier chunk's run
+    double total[kGroup];
+    float x[kGroup];
+    widen_group(load_group(p.tail + c * p.padded + col), x);
+#pragma unroll
+    for (int e = 0; e < kGroup; ++e) total[e] = x[e];
+    for (int64_t n = c + 1; n < p.chunks && p.keys[n * p.chunk] == key; ++n) {
+        widen_group(load_group(p.head + n * p.padded + col), x);
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) total[e] += x[e];
+    }
+#pragma unroll
+    for (int e = 0; e < kGroup; ++e) x[e] = static_cast<float>(total[e]);
+    put_sum<Out>(p, key, col, x);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Host side.
+
+int check_matrix(const fsdpshard_matrix* m, int64_t* bytes) {
+    if (m == nullptr || m->rows < 0 || m->cols < 1 || m->dtype < FSDPSHARD_BF16 ||
+        m->dtype > FSDPSHARD_FP32 || (m->rows > 1 && m->row_stride < m->cols) ||
+        (m->rows > 0 && m->data == nullptr))
+        return FSDPSHARD_ERR_INVALID_ARG;
+    if (m->cols > FSDPSHARD_MAX_DIM) return FSDPSHARD_ERR_UNSUPPORTED;
+    if (!aligned_to(m->data, element_bytes(m->dtype))) return FSDPSHARD_ERR_ALIGNMENT;
+    *bytes = extent(m->rows, m->cols, m->row_stride, element_bytes(m->dtype));
+    return *bytes < 0 || m->rows > kMaxRows ? FSDPSHARD_ERR_OVERFLOW : FSDPSHARD_OK;
+}
+
+// Threads for a row: the power of two that covers its groups, `each` of them a thread, up to kBlock;
+// splits: work-groups for a row.
+struct Threads {
+    int32_t shift, splits;
+};
+
+Threads row_threads(int64_t dim, int each) {
+    const int64_t groups = (dim + kGroup - 1) / kGroup;
+    int32_t shift = 0;
+    while (shift < 8 && (int64_t{each} << shift) < groups) ++shift;
+    const int64_t per = int64_t{each} << shift;
+    return {shift, static_cast<int32_t>((groups + per - 1) / per)};
+}
+
+template <typename Get>
+const void* by_dtypes(int32_t in, int32_t out, Get get) {
+    return by_dtype(in, [&](auto a) { return by_dtype(out, [&](auto b) { return get(a, b); }); });
+}
+
+int digit_bits(int64_t vocab) {
+    int bits = 1;
+    while ((int64_t{1} << bits) <= vocab) ++bits;      // the key `vocab` too
+    return (bits + 1) / 2;
+}
+
+// Where the workspace's arrays start.
+struct GradLayout {
+    int64_t items, counts, totals, keys, order, seen, head, tail, bytes;
+    int32_t blocks, bits, chunk, chunks, padded;
+};
+
+constexpr int64_t kMinChunk = 32, kMaxChunks = 2048;
+
+GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t dim) {
+    GradLayout l{};
+    const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
+    // (Without tokens one work-group marks every row as unseen.)
+    l.blocks = static_cast<int32_t>((tokens > 0 ? tokens + kSortTokens - 1 : kSortTokens) / kSortTokens);
+    l.bits = digit_bits(vocab);
+    const int64_t even = (tokens + kMaxChunks - 1) / kMaxChunks;
+    l.chunk = static_cast<int32_t>(even > kMinChunk ? even : kMinChunk);
+    l.chunks = static_cast<int32_t>((tokens + l.chunk - 1) / l.chunk);
+    l.padded = static_cast<int32_t>((dim + kGroup - 1) / kGroup * kGroup);
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        const int64_t start = at;
+        at += up(bytes);
+        return start;
+    };
+    l.items = take(8 * tokens);
+    l.counts = take((int64_t{4} << l.bits) * l.blocks);
+    l.totals = take(int64_t{4} << l.bits);
+    l.keys = take(4 * tokens);
+    l.order = take(4 * tokens);
+    l.seen = take(vocab);
+    l.head = take(int64_t{4} * l.chunks * l.padded);
+    l.tail = take(int64_t{4} * l.chunks * l.padded);
+    l.bytes = at;
+    return l;
+}
+
+}  // namespace
+
+extern "C" int embedding_lookup(const fsdpshard_matrix* table, const int64_t* ids,
+                                const fsdpshard_matrix* out, float scale, void* stream) {
+    int64_t tbytes = 0, obytes = 0;
+    int rc = check_matrix(table, &tbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    rc = check_matrix(out, &obytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    if (table->cols != out->cols || !std::isfinite(scale) || (out->rows > 0 && ids == nullptr))
+        return FSDPSHARD_ERR_INVALID_ARG;
+    if (table->rows > FSDPSHARD_MAX_VOCAB) return FSDPSHARD_ERR_UNSUPPORTED;
+    if (!aligned_to(ids, 8)) return FSDPSHARD_ERR_ALIGNMENT;
+    const Span written[] = {{out->data, obytes}};
+    const Span read[] = {{table->data, tbytes}, {ids, 8 * out->rows}};
+    if (!disjoint(written, 1, read, 2)) return FSDPSHARD_ERR_INVALID_ARG;
+    if (out->rows == 0) return FSDPSHARD_OK;
+    const Threads th = row_threads(out->cols, kLookupGroups);
+    LookupParams p{table->data, table->rows, table->row_stride, ids, out->data, out->rows,
+                   out->row_stride, static_cast<int32_t>(out->cols), th.splits, th.shift, scale, 0};
+    const void* kernel = by_dtypes(table->dtype, out->dtype, [](auto a, auto b) {
+        return KERNEL(lookup_kernel<decltype(a), decltype(b)>);
+    });
+    const int64_t per = kBlock >> th.shift;
+    return launch_units(kernel, (out->rows + per - 1) / per * th.splits, p, 0, stream);
+}
+
+extern "C" int64_t embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) {
+    if (tokens < 0 || tokens > FSDPSHARD_MAX_TOKENS || vocab < 0 || vocab > FSDPSHARD_MAX_VOCAB ||
+        dim < 1 || dim > FSDPSHARD_MAX_DIM)
+        return -1;
+    return grad_layout(tokens, vocab, dim).bytes;
+}
+
+extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
+                              const fsdpshard_matrix* dtable, float scale, int32_t accumulate,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+    int64_t dbytes = 0, tbytes = 0;
+    int rc = check_matrix(dout, &dbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    rc = check_matrix(dtable, &tbytes);
+    if (rc != FSDPSHARD_OK) return rc;
+    const int64_t tokens = dout->rows, vocab = dtable->rows;
+    if (dout->cols != dtable->cols || !std::isfinite(scale) || (tokens > 0 && ids == nullptr) ||
+        (accumulate != 0 && accumulate != 1))
+        return FSDPSHARD_ERR_INVALID_ARG;
+    if (vocab > FSDPSHARD_MAX_VOCAB || tokens > FSDPSHARD_MAX_TOKENS)
+        return FSDPSHARD_ERR_UNSUPPORTED;
+    if (!aligned_to(ids, 8)) return FSDPSHARD_ERR_ALIGNMENT;
+    const GradLayout l = grad_layout(tokens, vocab, dout->cols);
+    if (!workspace_ok(workspace, workspace_bytes, l.bytes, &rc)) return rc;
+    const Span written[] = {{dtable->data, tbytes}, {workspace, workspace_bytes}};
+    const Span read[] = {{ids, 8 * tokens}, {dout->data, dbytes}};
+    if (!disjoint(written, 2, read, 2)) return FSDPSHARD_ERR_INVALID_ARG;
+    if (vocab == 0 || (tokens == 0 && accumulate)) return FSDPSHARD_OK;
+    char* ws = static_cast<char*>(workspace);
+    SortParams s{};
+    s.ids = ids;
+    s.tokens = tokens;
+    s.vocab = vocab;
+    s.blocks = l.blocks;
+    s.counts = reinterpret_cast<uint32_t*>(ws + l.counts);
+    s.totals = reinterpret_cast<uint32_t*>(ws + l.totals);
+    s.keys = reinterpret_cast<uint32_t*>(ws + l.keys);
+    s.seen = reinterpret_cast<uint8_t*>(ws + l.seen);
+    s.bits = l.bits;
+    uint2* items = reinterpret_cast<uint2*>(ws + l.items);
+    for (int pass = 0; pass < 2; ++pass) {
+        s.shift = pass * l.bits;
+        s.in = pass ? items : nullptr;
+        s.out = items;
+        s.order = pass ? reinterpret_cast<uint32_t*>(ws + l.order) : nullptr;
+        rc = launch_units(KERNEL(sort_count_kernel), s.blocks, s, 0, stream);
+        if (rc != FSDPSHARD_OK) return rc;
+        rc = launch_units(KERNEL(sort_scan_kernel), int64_t{1} << l.bits, s, 0, stream);
+        if (rc != FSDPSHARD_OK) return rc;
+        rc = launch_units(KERNEL(sort_place_kernel), s.blocks, s, 0, stream);
+        if (rc != FSDPSHARD_OK) return rc;
+    }
+    const Threads th = row_threads(dout->cols, 1);
+    GradParams p{};
+    p.keys = s.keys;
+    p.order = s.order;
+    p.seen = s.seen;
+    p.dout = dout->data;
+    p.dstride = dout->row_stride;
+    p.table = dtable->data;
+    p.tstride = dtable->row_stride;
+    p.tokens = tokens;
+    p.vocab = vocab;
+    p.head = reinterpret_cast<float*>(ws + l.head);
+    p.tail = reinterpret_cast<float*>(ws + l.tail);
+    p.dim = static_cast<int32_t>(dout->cols);
+    p.padded = l.padded;
+    p.chunk = l.chunk;
+    p.chunks = l.chunks;
+    p.splits = th.splits;
+    p.shift = th.shift;
+    p.scale = scale;
+    p.accumulate = accumulate;
+    const int64_t per = kBlock >> th.shift;
+    p.sum_units = (l.chunks + per - 1) / per * th.splits;
+    const int64_t fill = accumulate ? 0 : (vocab + kFillRows - 1) / kFillRows;
+    const void* kernel = by_dtypes(dout->dtype, dtable->dtype, [](auto a, auto b) {
+        return KERNEL(embed_grad_kernel<decltype(a), decltype(b)>);
+    });
+    rc = launch_units(kernel, p.sum_units + fill, p, 0, stream);
+    if (rc != FSDPSHARD_OK || l.chunks <= 1) return rc;
+    kernel = by_dtype(dtable->dtype,
+                      [](auto t) { return KERNEL(embed_join_kernel<decltype(t)>); });
+    return launch_units(kernel, p.sum_units, p, 0, stream);
+}
