@@ -134,53 +134,32 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Sorting.  Tokens by their row of the table, equal ones in their order: two stable passes over half
-// of the bits each.  A token without a row gets the key `vocab` and comes last.  A work-group ranks
-// kSortTokens tokens, a wave a quarter of them: counts of its digits, then 64 tokens at a time.
+// Sorting.  Tokens by their row of the table, equal ones in their order; a token without a row gets the
+// key `vocab` and comes last.
+//
+// Where tokens are not too many (kOneLaunchReads) each work-group sorts the tokens of a range of rows by itself, in one launch:
+// it counts the tokens of lower rows, which is where its own ones start, and those of each of its rows,
+// and goes through the tokens again to place its own.  All work-groups read all tokens twice, from the
+// caches.
 
-constexpr int kSortRounds = 16;
-constexpr int kSortTokens = kBlock * kSortRounds;
-constexpr int kWaves = kBlock / kWave;
-constexpr int kMaxDigitBits = 11;           // two digits hold 0 .. FSDPSHARD_MAX_VOCAB
+constexpr int kRangeThreads = 512, kRangeWaves = kRangeThreads / kWave;
+constexpr int kMaxRange = 1024;             // rows of a range; their counts, one a wave, fit the LDS
+constexpr int kRangeAhead = 4;              // tokens a lane loads at once
 
 struct SortParams {
     const int64_t* ids;
     int64_t tokens, vocab;
-    int32_t blocks, shift, bits;            // of this pass
+    uint32_t *keys, *order;                 // results
+    uint8_t* seen;                          // whether a token names the row
+    uint32_t* long_runs;                    // set to 0: see below
+    int32_t range, bits;                    // rows of a work-group's range and their bits; of a digit
+    int32_t blocks, shift;                  // of the two passes
     uint32_t* counts;                       // [2^bits, blocks]
     uint32_t* totals;                       // [2^bits]
     const uint2* in;                        // (key, token), null in the first pass
     uint2* out;
-    uint32_t *keys, *order;                 // the last pass's results
-    uint8_t* seen;                          // rows that a token names, set to 0 by the first pass
     int64_t unit0;
 };
-
-__device__ __forceinline__ uint2 sort_item(const SortParams& p, int64_t i) {
-    if (p.in) return p.in[i];
-    const int64_t id = p.ids[i];
-    return make_uint2(static_cast<uint32_t>(id >= 0 && id < p.vocab ? id : p.vocab),
-                      static_cast<uint32_t>(i));
-}
-
-__global__ __launch_bounds__(kBlock) void sort_count_kernel(SortParams p) {
-    __shared__ uint32_t count[1 << kMaxDigitBits];
-    const int tid = threadIdx.x, digits = 1 << p.bits;
-    const int64_t block = p.unit0 + blockIdx.x, base = block * kSortTokens;
-    for (int d = tid; d < digits; d += kBlock) count[d] = 0;
-    if (p.in == nullptr)
-        for (int64_t v = block * kBlock + tid; v < p.vocab;
-             v += static_cast<int64_t>(p.blocks) * kBlock)
-            p.seen[v] = 0;
-    __syncthreads();
-    for (int q = 0; q < kSortRounds; ++q) {
-        const int64_t i = base + q * kBlock + tid;
-        if (i < p.tokens) atomicAdd(&count[(sort_item(p, i).x >> p.shift) & (digits - 1)], 1u);
-    }
-    __syncthreads();
-    for (int d = tid; d < digits; d += kBlock)
-        p.counts[static_cast<int64_t>(d) * p.blocks + block] = count[d];
-}
 
 // Orders the LDS accesses of one wave's lanes (the hardware keeps a wave's in order: this is for the
 // compiler).
@@ -190,6 +169,7 @@ __device__ __forceinline__ void wave_fence() {
 }
 
 // The exclusive sum of x over the work-group's threads; `total` is the sum of all.
+template <int Waves>
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sh, uint32_t& total) {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     uint32_t sum = x;
@@ -204,11 +184,136 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sh, uint32_
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < Waves; ++w) {
         if (w < wave) before += sh[w];
         total += sh[w];
     }
     return before + sum - x;
+}
+
+// The lanes of `among` whose `bits` lowest bits of d are this lane's.
+__device__ __forceinline__ unsigned long long lanes_with(uint32_t d, int bits,
+                                                         unsigned long long among) {
+    for (int b = 0; b < bits; ++b) {
+        const unsigned long long ones = __ballot((d >> b) & 1);
+        among &= (d >> b) & 1 ? ones : ~ones;
+    }
+    return among;
+}
+
+__global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p) {
+    extern __shared__ uint32_t place[];     // [kRangeWaves][range]
+    __shared__ uint32_t sh[kRangeWaves];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int64_t low = (p.unit0 + blockIdx.x) * p.range;
+    const int rows = static_cast<int>(p.vocab - low < p.range ? p.vocab - low : p.range);
+    uint32_t* mine = place + wave * p.range;
+    for (int i = tid; i < kRangeWaves * p.range; i += kRangeThreads) place[i] = 0;
+    if (tid == 0 && blockIdx.x == 0) *p.long_runs = 0;
+    __syncthreads();
+    // A wave's tokens are consecutive.
+    const int64_t each = (p.tokens + kRangeThreads - 1) / kRangeThreads * kWave;
+    const int64_t begin = wave * each, end = begin + each < p.tokens ? begin + each : p.tokens;
+    const auto stream = [&](auto f) {
+        for (int64_t i0 = begin + lane; i0 - lane < end; i0 += kRangeAhead * kWave) {
+            int64_t id[kRangeAhead];
+#pragma unroll
+            for (int q = 0; q < kRangeAhead; ++q)
+                id[q] = i0 + q * kWave < end ? p.ids[i0 + q * kWave] : -1;
+#pragma unroll
+            for (int q = 0; q < kRangeAhead; ++q) f(id[q], i0 + q * kWave);
+        }
+    };
+    uint32_t lower = 0;
+    stream([&](int64_t id, int64_t) {
+        if (id >= 0 && id < low) ++lower;
+        if (id >= low && id - low < rows) atomicAdd(&mine[id - low], 1u);
+    });
+    uint32_t start;
+    block_scan<kRangeWaves>(lower, sh, start);
+    // Where each wave's first token of each row goes.
+    const int per = (p.range + kRangeThreads - 1) / kRangeThreads;
+    uint32_t sum = 0;
+    for (int r = tid * per; r < (tid + 1) * per && r < rows; ++r) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int w = 0; w < kRangeWaves; ++w) n += place[w * p.range + r];
+        p.seen[low + r] = n != 0;
+        sum += n;
+    }
+    uint32_t own;
+    uint32_t at = start + block_scan<kRangeWaves>(sum, sh, own);
+    for (int r = tid * per; r < (tid + 1) * per && r < rows; ++r) {
+#pragma unroll
+        for (int w = 0; w < kRangeWaves; ++w) {
+            const uint32_t n = place[w * p.range + r];
+            place[w * p.range + r] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    if (low + rows == p.vocab)              // the last range: tokens without a row
+        for (int64_t i = start + own + tid; i < p.tokens; i += kRangeThreads)
+            p.keys[i] = static_cast<uint32_t>(p.vocab);
+    stream([&](int64_t id, int64_t i) {
+        const bool here = id >= low && id - low < rows;
+        const unsigned long long some = __ballot(here);
+        if (some == 0) return;
+        const uint32_t d = here ? static_cast<uint32_t>(id - low) : 0;
+        const unsigned long long same = lanes_with(d, p.bits, some);
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        uint32_t to = 0;
+        if (here) {
+            to = mine[d] + before;
+            p.keys[to] = static_cast<uint32_t>(id);
+            p.order[to] = static_cast<uint32_t>(i);
+        }
+        wave_fence();                       // every lane has read its place
+        if (here && before == 0) mine[d] = to + __popcll(same);
+        wave_fence();
+    });
+}
+
+// More tokens take two stable passes over half of a key's bits each.  A work-group ranks kSortTokens
+// tokens, a wave a quarter of them: counts of its digits, then 64 tokens at a time.
+
+constexpr int kSortRounds = 16;
+constexpr int kSortTokens = kBlock * kSortRounds;
+constexpr int kWaves = kBlock / kWave;
+constexpr int kMaxDigitBits = 11;           // two digits hold 0 .. FSDPSHARD_MAX_VOCAB
+
+__device__ __forceinline__ uint2 sort_item(const SortParams& p, int64_t i) {
+    if (p.in) return p.in[i];
+    const int64_t id = p.ids[i];
+    return make_uint2(static_cast<uint32_t>(id >= 0 && id < p.vocab ? id : p.vocab),
+                      static_cast<uint32_t>(i));
+}
+
+__global__ __launch_bounds__(kBlock) void sort_count_kernel(SortParams p) {
+    __shared__ uint32_t count[1 << kMaxDigitBits];
+    const int tid = threadIdx.x, digits = 1 << p.bits;
+    const int64_t block = p.unit0 + blockIdx.x, base = block * kSortTokens;
+    for (int d = tid; d < digits; d += kBlock) count[d] = 0;
+    if (p.in == nullptr) {
+        for (int64_t v = block * kBlock + tid; v < p.vocab;
+             v += static_cast<int64_t>(p.blocks) * kBlock)
+            p.seen[v] = 0;
+        if (block == 0 && tid == 0) *p.long_runs = 0;
+    }
+    __syncthreads();
+    uint32_t key[kSortRounds];              // all loads first: the atomics would keep them apart
+#pragma unroll
+    for (int q = 0; q < kSortRounds; ++q) {
+        const int64_t i = base + q * kBlock + tid;
+        key[q] = i < p.tokens ? sort_item(p, i).x : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < kSortRounds; ++q)
+        if (base + q * kBlock + tid < p.tokens)
+            atomicAdd(&count[(key[q] >> p.shift) & (digits - 1)], 1u);
+    __syncthreads();
+    for (int d = tid; d < digits; d += kBlock)
+        p.counts[static_cast<int64_t>(d) * p.blocks + block] = count[d];
 }
 
 // Each digit's counts become its exclusive sums over the blocks.
@@ -219,7 +324,7 @@ __global__ __launch_bounds__(kBlock) void sort_scan_kernel(SortParams p) {
     for (int b0 = 0; b0 < p.blocks; b0 += kBlock) {
         const int b = b0 + threadIdx.x;
         uint32_t total;
-        const uint32_t x = b < p.blocks ? row[b] : 0, sum = block_scan(x, sh, total);
+        const uint32_t x = b < p.blocks ? row[b] : 0, sum = block_scan<kWaves>(x, sh, total);
         if (b < p.blocks) row[b] = run + sum;
         run += total;
     }
@@ -240,19 +345,19 @@ __global__ __launch_bounds__(kBlock) void sort_place_kernel(SortParams p) {
 #pragma unroll
     for (int q = 0; q < kSortRounds; ++q) {
         const int64_t i = base + q * kWave + lane;
-        item[q] = make_uint2(0xFFFFFFFFu, 0);
-        if (i < p.tokens) {
-            item[q] = sort_item(p, i);
-            atomicAdd(&place[wave][(item[q].x >> p.shift) & (digits - 1)], 1u);
-        }
+        item[q] = i < p.tokens ? sort_item(p, i) : make_uint2(0, 0);
     }
+#pragma unroll
+    for (int q = 0; q < kSortRounds; ++q)
+        if (base + q * kWave + lane < p.tokens)
+            atomicAdd(&place[wave][(item[q].x >> p.shift) & (digits - 1)], 1u);
     __syncthreads();
     // Where each wave's first token of each digit goes.
     uint32_t run = 0;
     for (int d0 = 0; d0 < digits; d0 += kBlock) {
         const int d = d0 + tid;
         uint32_t total;
-        const uint32_t sum = block_scan(d < digits ? p.totals[d] : 0, sh, total);
+        const uint32_t sum = block_scan<kWaves>(d < digits ? p.totals[d] : 0, sh, total);
         if (d < digits) {
             uint32_t at = run + sum + p.counts[static_cast<int64_t>(d) * p.blocks + block];
 #pragma unroll
@@ -270,11 +375,7 @@ __global__ __launch_bounds__(kBlock) void sort_place_kernel(SortParams p) {
         const int64_t i = base + q * kWave + lane;
         const bool there = i < p.tokens;
         const uint32_t d = (item[q].x >> p.shift) & (digits - 1);
-        unsigned long long same = __ballot(there);      // lanes of this digit
-        for (int b = 0; b < p.bits; ++b) {
-            const unsigned long long ones = __ballot((d >> b) & 1);
-            same &= (d >> b) & 1 ? ones : ~ones;
-        }
+        const unsigned long long same = lanes_with(d, p.bits, __ballot(there));
         const int before = __popcll(same & ((1ull << lane) - 1));
         uint32_t at = 0;
         if (there) {
@@ -296,12 +397,13 @@ __global__ __launch_bounds__(kBlock) void sort_place_kernel(SortParams p) {
 // ------------------------------------------------------------------------------------------------
 // Gradient.  The sorted tokens are cut into chunks of equal length, whatever rows they name, so that a
 // frequent token's sum is shared like any other's.  2^shift threads own 8 columns each of a chunk and
-// add up its runs of equal tokens: a run inside the chunk goes to the table, a run that comes from the
-// chunk before or goes on in the next one goes to the chunk's `head` or `tail`, which the joining
-// kernel adds up.  Rows without a token are set to zeros by work-groups of the same launch.
+// add up its runs of equal tokens.  A run belongs to the chunk in which it starts, and one that ends in
+// the next chunk is followed there; so most runs are summed by one unit.  A run over three chunks or
+// more (a long one) is summed in parts: the `tail` of the chunk in which it starts, and the `head` of
+// each chunk after it, which the joining kernel adds up.  Rows without a token are set to zeros by
+// work-groups of the same launch.
 
 constexpr int kAhead = 8;                   // rows of the gradient loaded at once
-constexpr int kFillRows = 16;
 
 struct GradParams {
     const uint32_t *keys, *order;
@@ -311,6 +413,7 @@ struct GradParams {
     void* table;
     int64_t tstride, tokens, vocab;
     float *head, *tail;                     // [chunks, padded]
+    uint32_t* long_runs;                    // their number, then the chunks in which they start
     int32_t dim, padded, chunk, chunks, splits, shift;
     float scale;
     int32_t accumulate;
@@ -333,20 +436,43 @@ __device__ __forceinline__ void put_sum(const GradParams& p, uint32_t key, int c
     store_any(at, sum, n);
 }
 
+// Zeros for the rows without a token, a wave each in turn.
+constexpr int kFillRows = 32, kFillEach = kFillRows / kWaves;
+
 template <typename Out>
 __device__ void fill_rows(const GradParams& p, int64_t unit) {
-    const float zero[kGroup] = {};
-    for (int i = 0; i < kFillRows; ++i) {
-        const int64_t v = unit * kFillRows + i;
-        if (v >= p.vocab) return;
-        if (p.seen[v]) continue;
-        Out* row = static_cast<Out*>(p.table) + v * p.tstride;
-        for (int col = threadIdx.x * kGroup; col < p.dim; col += kBlock * kGroup)
-            store_any(row + col, zero, p.dim - col);
+    constexpr int E = kElems<Out>;
+    const int lane = threadIdx.x % kWave;
+    const int64_t v0 = unit * kFillRows + threadIdx.x / kWave;
+    bool skip[kFillEach];
+#pragma unroll
+    for (int i = 0; i < kFillEach; ++i) {
+        const int64_t v = v0 + i * kWaves;
+        skip[i] = v >= p.vocab || p.seen[v] != 0;
+    }
+#pragma unroll 1
+    for (int i = 0; i < kFillEach; ++i) {
+        if (skip[i]) continue;
+        Out* row = static_cast<Out*>(p.table) + (v0 + i * kWaves) * p.tstride;
+        int col = lane * E;
+        for (; col + E <= p.dim; col += kWave * E)
+            *reinterpret_cast<loose_vec*>(row + col) = u32x4{0, 0, 0, 0};
+        for (; col < p.dim; ++col) row[col] = narrow<Out>(0.0f);
     }
 }
 
-template <typename In, typename Out>
+// A value of the sorted tokens.  Where a whole wave works on one chunk (Uniform), its loads are the
+// scalar unit's; the arrays are not written in this launch.
+template <bool Uniform>
+__device__ __forceinline__ uint32_t sorted(const uint32_t* p, int64_t i) {
+    if constexpr (Uniform)
+        return *reinterpret_cast<const __attribute__((address_space(4))) uint32_t*>(
+            reinterpret_cast<uintptr_t>(p + i));
+    else
+        return p[i];
+}
+
+template <typename In, typename Out, bool Uniform>
 __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
     const int64_t unit = p.unit0 + blockIdx.x;
     if (unit >= p.sum_units) {
@@ -356,39 +482,65 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
     const int tid = threadIdx.x;
     const int64_t first = row_of(unit, p.splits);
     const int split = static_cast<int>(unit - first * p.splits);
-    const int64_t c = (first << (8 - p.shift)) + (tid >> p.shift);
+    int c = static_cast<int>(first << (8 - p.shift)) + (tid >> p.shift);
+    if constexpr (Uniform) c = __builtin_amdgcn_readfirstlane(c);
     const int col = ((split << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
     if (c >= p.chunks || col >= p.dim) return;
-    const int64_t begin = c * p.chunk;
-    const int64_t end = begin + p.chunk < p.tokens ? begin + p.chunk : p.tokens;
-    const In* src = static_cast<const In*>(p.dout) + col;
     const uint32_t none = static_cast<uint32_t>(p.vocab);
-    bool comes = begin > 0 && p.keys[begin - 1] == p.keys[begin];
+    const int tokens = static_cast<int>(p.tokens), begin = c * p.chunk;
+    const int end = begin + p.chunk < tokens ? begin + p.chunk : tokens;
+    const int after = end + p.chunk < tokens ? end + p.chunk : tokens;    // of the next chunk
+    const auto key_at = [&](int i) { return i < tokens ? sorted<Uniform>(p.keys, i) : none; };
+    const In* src = static_cast<const In*>(p.dout) + col;
+    uint32_t skip = none;                   // the run before's, if that followed it here
+    bool comes = false;
+    if (const uint32_t k = key_at(begin); k >= none) {
+        return;
+    } else if (begin > 0 && key_at(begin - 1) == k) {
+        const int before = begin - p.chunk;
+        const bool starts = before == 0 || key_at(before - 1) != k;
+        if (starts && key_at(end) != k) skip = k;
+        else comes = true;
+    }
     float sum[kGroup] = {};
-    for (int64_t j0 = begin; j0 < end; j0 += kAhead) {
+    bool follows = false;                   // past the chunk's end
+    for (int j0 = begin; j0 < (follows ? after : end); j0 += kAhead) {
+        const int limit = follows ? after : end;
         uint32_t key[kAhead + 1];
         Group<In> raw[kAhead];
 #pragma unroll
-        for (int q = 0; q <= kAhead; ++q) key[q] = j0 + q < p.tokens ? p.keys[j0 + q] : none;
+        for (int q = 0; q <= kAhead; ++q) key[q] = key_at(j0 + q);
+        const uint32_t current = key[0];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q)
-            if (j0 + q < end && key[q] < none)
-                raw[q] = load_any(src + p.order[j0 + q] * p.dstride, p.dim - col);
+            if (j0 + q < limit && (follows ? key[q] == current : key[q] < none && key[q] != skip))
+                raw[q] = load_any(src + sorted<Uniform>(p.order, j0 + q) * p.dstride, p.dim - col);
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            if (j0 + q >= end) break;
+            const int j = j0 + q;
+            if (j >= limit) break;
             if (key[q] >= none) return;
+            if (key[q] == skip) continue;
             float x[kGroup];
             widen_group(raw[q], x);
 #pragma unroll
             for (int e = 0; e < kGroup; ++e) sum[e] += x[e];
-            const bool last = j0 + q + 1 == end, goes = key[q + 1] == key[q];
-            if (goes && !last) continue;
-            if (comes || goes) {
-                store_group((comes ? p.head : p.tail) + c * p.padded + col, sum);
-            } else {
-                put_sum<Out>(p, key[q], col, sum);
+            if (key[q + 1] == key[q]) {
+                if (j + 1 != end) continue;
+                if (!comes && key_at(after) != key[q]) {
+                    follows = true;
+                    continue;
+                }
+                store_group((comes ? p.head : p.tail) + static_cast<int64_t>(c) * p.padded + col,
+                            sum);
+                if (!comes && col == 0) p.long_runs[1 + atomicAdd(p.long_runs, 1u)] = c;
+                return;
             }
+            if (comes)
+                store_group(p.head + static_cast<int64_t>(c) * p.padded + col, sum);
+            else
+                put_sum<Out>(p, key[q], col, sum);
+            if (j + 1 >= end) return;
             comes = false;
 #pragma unroll
             for (int e = 0; e < kGroup; ++e) sum[e] = 0.0f;
@@ -396,35 +548,66 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
     }
 }
 
-// The sums of runs that cross chunks: the work-group of the chunk in which a run starts adds its tail
-// and the heads of the chunks that follow, in their order.
+// The long runs.  A work-group takes 64 groups of a run's columns; its waves take the heads in turn, and
+// their float64 sums are added up in the waves' order.
+constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave;
+constexpr int kJoinAhead = 4, kJoinGroups = 512;
+
 template <typename Out>
-__global__ __launch_bounds__(kBlock) void embed_join_kernel(GradParams p) {
-    const int tid = threadIdx.x;
-    const int64_t unit = p.unit0 + blockIdx.x;
-    const int64_t first = row_of(unit, p.splits);
-    const int split = static_cast<int>(unit - first * p.splits);
-    const int64_t c = (first << (8 - p.shift)) + (tid >> p.shift);
-    const int col = ((split << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
-    if (c >= p.chunks || col >= p.dim) return;
-    const int64_t begin = c * p.chunk, end = begin + p.chunk;
-    if (end >= p.tokens) return;
-    const uint32_t key = p.keys[end];
-    if (key >= p.vocab || p.keys[end - 1] != key) return;
-    if (begin > 0 && p.keys[begin - 1] == key) return;      // an earlier chunk's run
-    double total[kGroup];
-    float x[kGroup];
-    widen_group(load_group(p.tail + c * p.padded + col), x);
+__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(GradParams p) {
+    __shared__ double parts[kJoinWaves - 1][kWave][kGroup];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int splits = (p.dim + kWave * kGroup - 1) / (kWave * kGroup);
+    const int64_t units = static_cast<int64_t>(*p.long_runs) * splits;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t c = p.long_runs[1 + unit / splits];
+        const int col = (static_cast<int>(unit % splits) * kWave + lane) * kGroup;
+        const uint32_t key = p.keys[(c + 1) * p.chunk];
+        // How many chunks after c the run reaches.
+        int heads = 1;
+        for (bool all = true; all; ) {
+            const int64_t n = c + 1 + heads + lane;
+            const unsigned long long other = ~__ballot(n < p.chunks && p.keys[n * p.chunk] == key);
+            heads += other != 0 ? __builtin_ctzll(other) : kWave;
+            all = other == 0;
+        }
+        double total[kGroup] = {};
+        if (col < p.dim) {
+            const float* head = p.head + (c + 1) * p.padded + col;
+            for (int h0 = wave; h0 < heads; h0 += kJoinAhead * kJoinWaves) {
+                Group<float> raw[kJoinAhead];
 #pragma unroll
-    for (int e = 0; e < kGroup; ++e) total[e] = x[e];
-    for (int64_t n = c + 1; n < p.chunks && p.keys[n * p.chunk] == key; ++n) {
-        widen_group(load_group(p.head + n * p.padded + col), x);
+                for (int q = 0; q < kJoinAhead; ++q) {
+                    const int h = h0 + q * kJoinWaves;
+                    if (h < heads) raw[q] = load_group(head + static_cast<int64_t>(h) * p.padded);
+                }
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) total[e] += x[e];
+                for (int q = 0; q < kJoinAhead; ++q) {
+                    if (h0 + q * kJoinWaves >= heads) break;
+                    float x[kGroup];
+                    widen_group(raw[q], x);
+#pragma unroll
+                    for (int e = 0; e < kGroup; ++e) total[e] += x[e];
+                }
+            }
+        }
+        __syncthreads();                    // the unit before has read the parts
+        if (wave > 0)
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) parts[wave - 1][lane][e] = total[e];
+        __syncthreads();
+        if (wave == 0 && col < p.dim) {
+            float x[kGroup];
+            widen_group(load_group(p.tail + c * p.padded + col), x);
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) {
+                total[e] += x[e];
+                for (int w = 1; w < kJoinWaves; ++w) total[e] += parts[w - 1][lane][e];
+                x[e] = static_cast<float>(total[e]);
+            }
+            put_sum<Out>(p, key, col, x);
+        }
     }
-#pragma unroll
-    for (int e = 0; e < kGroup; ++e) x[e] = static_cast<float>(total[e]);
-    put_sum<Out>(p, key, col, x);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -468,20 +651,34 @@ int digit_bits(int64_t vocab) {
 
 // Where the workspace's arrays start.
 struct GradLayout {
-    int64_t items, counts, totals, keys, order, seen, head, tail, bytes;
+    int64_t keys, order, seen, long_runs, head, tail, items, counts, totals, bytes;
     int32_t blocks, bits, chunk, chunks, padded;
 };
+
+// Work-groups that sort the tokens of a range of rows each; more where a range would be too long.  All of
+// them read all tokens: up to kOneLaunchReads readings in all, tokens are sorted so.
+constexpr int64_t kRanges = 128;
+constexpr int64_t kOneLaunchReads = int64_t{1} << 24;
+
+int64_t range_rows(int64_t vocab) {
+    const int64_t even = (vocab + kRanges - 1) / kRanges;
+    return even < kMaxRange ? even : kMaxRange;
+}
+bool in_one_launch(int64_t tokens, int64_t vocab) {
+    if (vocab == 0) return true;
+    const int64_t rows = range_rows(vocab);
+    return tokens * ((vocab + rows - 1) / rows) <= kOneLaunchReads;
+}
 
 constexpr int64_t kMinChunk = 32, kMaxChunks = 2048;
 
 GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t dim) {
     GradLayout l{};
     const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
-    // (Without tokens one work-group marks every row as unseen.)
-    l.blocks = static_cast<int32_t>((tokens > 0 ? tokens + kSortTokens - 1 : kSortTokens) / kSortTokens);
+    l.blocks = static_cast<int32_t>((tokens + kSortTokens - 1) / kSortTokens);
     l.bits = digit_bits(vocab);
     const int64_t even = (tokens + kMaxChunks - 1) / kMaxChunks;
-    l.chunk = static_cast<int32_t>(even > kMinChunk ? even : kMinChunk);
+    l.chunk = static_cast<int32_t>(even > kMinChunk ? (even + kAhead - 1) / kAhead * kAhead : kMinChunk);
     l.chunks = static_cast<int32_t>((tokens + l.chunk - 1) / l.chunk);
     l.padded = static_cast<int32_t>((dim + kGroup - 1) / kGroup * kGroup);
     int64_t at = 0;
@@ -490,16 +687,49 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t dim) {
         at += up(bytes);
         return start;
     };
-    l.items = take(8 * tokens);
-    l.counts = take((int64_t{4} << l.bits) * l.blocks);
-    l.totals = take(int64_t{4} << l.bits);
     l.keys = take(4 * tokens);
     l.order = take(4 * tokens);
     l.seen = take(vocab);
+    l.long_runs = take(4 * (int64_t{1} + l.chunks));
     l.head = take(int64_t{4} * l.chunks * l.padded);
     l.tail = take(int64_t{4} * l.chunks * l.padded);
+    if (!in_one_launch(tokens, vocab)) {
+        l.items = take(8 * tokens);
+        l.counts = take((int64_t{4} << l.bits) * l.blocks);
+        l.totals = take(int64_t{4} << l.bits);
+    }
     l.bytes = at;
     return l;
+}
+
+int sort_ranges(SortParams& s, void* stream) {
+    s.range = static_cast<int32_t>(range_rows(s.vocab));
+    s.bits = 0;
+    while ((1 << s.bits) < s.range) ++s.bits;
+    return launch_units(KERNEL(sort_range_kernel), (s.vocab + s.range - 1) / s.range, s,
+                        int64_t{4} * kRangeWaves * s.range, stream, kRangeThreads);
+}
+
+int sort_digits(SortParams& s, const GradLayout& l, char* ws, void* stream) {
+    uint32_t* order = s.order;
+    uint2* items = reinterpret_cast<uint2*>(ws + l.items);
+    s.blocks = l.blocks;
+    s.bits = l.bits;
+    s.counts = reinterpret_cast<uint32_t*>(ws + l.counts);
+    s.totals = reinterpret_cast<uint32_t*>(ws + l.totals);
+    s.out = items;
+    for (int pass = 0; pass < 2; ++pass) {
+        s.shift = pass * l.bits;
+        s.in = pass ? items : nullptr;
+        s.order = pass ? order : nullptr;
+        int rc = launch_units(KERNEL(sort_count_kernel), s.blocks, s, 0, stream);
+        if (rc != FSDPSHARD_OK) return rc;
+        rc = launch_units(KERNEL(sort_scan_kernel), int64_t{1} << l.bits, s, 0, stream);
+        if (rc != FSDPSHARD_OK) return rc;
+        rc = launch_units(KERNEL(sort_place_kernel), s.blocks, s, 0, stream);
+        if (rc != FSDPSHARD_OK) return rc;
+    }
+    return FSDPSHARD_OK;
 }
 
 }  // namespace
@@ -562,25 +792,12 @@ extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
     s.ids = ids;
     s.tokens = tokens;
     s.vocab = vocab;
-    s.blocks = l.blocks;
-    s.counts = reinterpret_cast<uint32_t*>(ws + l.counts);
-    s.totals = reinterpret_cast<uint32_t*>(ws + l.totals);
     s.keys = reinterpret_cast<uint32_t*>(ws + l.keys);
+    s.order = reinterpret_cast<uint32_t*>(ws + l.order);
     s.seen = reinterpret_cast<uint8_t*>(ws + l.seen);
-    s.bits = l.bits;
-    uint2* items = reinterpret_cast<uint2*>(ws + l.items);
-    for (int pass = 0; pass < 2; ++pass) {
-        s.shift = pass * l.bits;
-        s.in = pass ? items : nullptr;
-        s.out = items;
-        s.order = pass ? reinterpret_cast<uint32_t*>(ws + l.order) : nullptr;
-        rc = launch_units(KERNEL(sort_count_kernel), s.blocks, s, 0, stream);
-        if (rc != FSDPSHARD_OK) return rc;
-        rc = launch_units(KERNEL(sort_scan_kernel), int64_t{1} << l.bits, s, 0, stream);
-        if (rc != FSDPSHARD_OK) return rc;
-        rc = launch_units(KERNEL(sort_place_kernel), s.blocks, s, 0, stream);
-        if (rc != FSDPSHARD_OK) return rc;
-    }
+    s.long_runs = reinterpret_cast<uint32_t*>(ws + l.long_runs);
+    rc = in_one_launch(tokens, vocab) ? sort_ranges(s, stream) : sort_digits(s, l, ws, stream);
+    if (rc != FSDPSHARD_OK) return rc;
     const Threads th = row_threads(dout->cols, 1);
     GradParams p{};
     p.keys = s.keys;
@@ -594,6 +811,7 @@ extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
     p.vocab = vocab;
     p.head = reinterpret_cast<float*>(ws + l.head);
     p.tail = reinterpret_cast<float*>(ws + l.tail);
+    p.long_runs = s.long_runs;
     p.dim = static_cast<int32_t>(dout->cols);
     p.padded = l.padded;
     p.chunk = l.chunk;
@@ -605,12 +823,15 @@ extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
     const int64_t per = kBlock >> th.shift;
     p.sum_units = (l.chunks + per - 1) / per * th.splits;
     const int64_t fill = accumulate ? 0 : (vocab + kFillRows - 1) / kFillRows;
-    const void* kernel = by_dtypes(dout->dtype, dtable->dtype, [](auto a, auto b) {
-        return KERNEL(embed_grad_kernel<decltype(a), decltype(b)>);
+    const void* kernel = by_dtypes(dout->dtype, dtable->dtype, [&](auto a, auto b) {
+        using In = decltype(a);
+        using Out = decltype(b);
+        return th.shift >= 6 ? KERNEL(embed_grad_kernel<In, Out, true>)
+                             : KERNEL(embed_grad_kernel<In, Out, false>);
     });
     rc = launch_units(kernel, p.sum_units + fill, p, 0, stream);
-    if (rc != FSDPSHARD_OK || l.chunks <= 1) return rc;
+    if (rc != FSDPSHARD_OK || l.chunks < 3) return rc;      // no run is long
     kernel = by_dtype(dtable->dtype,
                       [](auto t) { return KERNEL(embed_join_kernel<decltype(t)>); });
-    return launch_units(kernel, p.sum_units, p, 0, stream);
+    return launch_units(kernel, kJoinGroups, p, 0, stream, kJoinThreads);
 }

@@ -1,8 +1,9 @@
 """Embedding lookup and its gradient on the GPU.  The lookup is one float32 product and one rounding,
 so it is compared bit for bit.  The gradient's bound: with u = 2^-24 a row's float32 sums are chains of
-at most `chunk` additions of terms of total size S (max(32, tokens / 2048) tokens are summed in a run),
-their float64 sum is rounded once, and the product with the scale, the sum with what was there and the
-rounding to the type come last: u S (chunk + 1) + u |d| + u |result| + half a step of the type."""
+at most 2 chunk additions of terms of total size S (a chunk is max(32, tokens / 2048) tokens, rounded up
+to 8, and a run's sum goes on into the next one), their float64 sum is rounded once, and the product with
+the scale, the sum with what was there and the rounding to the type come last: u S (2 chunk + 1) + u |d| +
+u |result| + half a step of the type."""
 
 import numpy as np
 import pytest
@@ -77,7 +78,7 @@ def test_lookup_special_values():
 
 
 def _chunk(tokens):
-    return max(32, -(-tokens // 2048))
+    return max(32, (-(-tokens // 2048) + 7) // 8 * 8)
 
 
 def _check_grad(ids, dev, vocab, dtype, scale, got, what, before=None):
@@ -88,7 +89,7 @@ def _check_grad(ids, dev, vocab, dtype, scale, got, what, before=None):
     if before is not None:
         untouched = count == 0
         assert np.array_equal(got[untouched], before[untouched]), what + ": rows without a token"
-    tol = U * (size * (_chunk(tokens) + 1) + np.abs(d) + np.abs(want))
+    tol = U * (size * (2 * _chunk(tokens) + 1) + np.abs(d) + np.abs(want))
     info = torch.finfo(T[dtype])
     tol += np.maximum((np.abs(want) + tol) * info.eps / 2, info.tiny * info.eps / 2)
     C.close(got, want, tol, what)
@@ -119,12 +120,14 @@ def test_grad(shape, dtype, out):
         C.assert_between_rows_untouched(got, whole, f"{shape}")
 
 
-# Around a chunk of 32 tokens, a sorting work-group's 4096, chunks of more than 32 tokens (65,537
-# and up), one and two digits, the largest digits.
-@pytest.mark.parametrize("tokens,vocab,dim", [(31, 9, 16), (32, 9, 16), (33, 9, 16), (4095, 300, 8),
-                                              (4096, 300, 8), (4097, 300, 8), (20000, 32000, 24),
-                                              (65537, 1000, 8), (150001, 131072, 8),
-                                              (3000, 1 << 21, 8)])
+# Around a chunk of 32 tokens, chunks of more than 32 tokens (65,537 and up), tokens sorted in one
+# launch (up to 131,072, or fewer for a large vocabulary) and by digits, around a sorting work-group's
+# 4096, the largest digits, rows narrower and wider than a wave.
+@pytest.mark.parametrize("tokens,vocab,dim", [(31, 9, 16), (32, 9, 16), (33, 9, 16), (4097, 300, 8),
+                                              (20000, 32000, 24), (65537, 1000, 8), (20001, 700, 520),
+                                              (131072, 32000, 8), (131073, 300, 8),
+                                              (135168, 131072, 8), (135169, 70000, 8),
+                                              (3000, 1 << 21, 8), (9001, 1 << 21, 8)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_grad_of_many_tokens(tokens, vocab, dim, accumulate):
     rng = _seed(tokens, vocab)
