@@ -33,22 +33,6 @@ __device__ __forceinline__ Group<T> load_group(const T* p) {
     return g;
 }
 
-// The first n elements of a row's last group; zeros after them.
-template <typename T>
-__device__ __forceinline__ Group<T> load_some(const T* p, int n) {
-    using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
-    constexpr int PerWord = 4 / static_cast<int>(sizeof(T)), W = kGroup / PerWord;
-    const Bits* b = reinterpret_cast<const Bits*>(p);
-    uint32_t w[W] = {};
-#pragma unroll
-    for (int e = 0; e < kGroup; ++e)
-        if (e < n) w[e / PerWord] |= static_cast<uint32_t>(b[e]) << (e % PerWord * 16);
-    Group<T> g;
-#pragma unroll
-    for (int i = 0; i < W; ++i) g.v[i / 4][i % 4] = w[i];
-    return g;
-}
-
 template <typename T>
 __device__ __forceinline__ void widen_group(const Group<T>& g, float (&x)[kGroup]) {
 #pragma unroll
@@ -62,21 +46,50 @@ __device__ __forceinline__ void store_group(T* p, const float (&x)[kGroup]) {
         *reinterpret_cast<loose_vec*>(p + i * kElems<T>) = pack<T>(x + i * kElems<T>);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_some(T* p, const float (&x)[kGroup], int n) {
+// A thread's columns.  The group that a row's end cuts short is loaded as the row's last 8 elements, so
+// that every load is whole and none needs a branch (a branch around a load makes the compiler wait for
+// it at the branch's end); of it, elements from `own` on are the thread's.  Rows of fewer than 8
+// elements (Narrow) are loaded element by element, the last one for the places past it.
+struct Columns {
+    int at, own, end;      // first column loaded, first and past the last place that count
+
+    __device__ __forceinline__ Columns(int col, int dim) {
+        at = col + kGroup <= dim ? col : dim >= kGroup ? dim - kGroup : 0;
+        own = col - at;
+        end = dim < kGroup ? dim : kGroup;
+    }
+    __device__ __forceinline__ bool whole() const { return own == 0 && end == kGroup; }
+};
+
+template <bool Narrow, typename T>
+__device__ __forceinline__ Group<T> load_columns(const T* row, const Columns& c) {
+    if constexpr (!Narrow) {
+        return load_group(row + c.at);
+    } else {
+        using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+        constexpr int PerWord = 4 / static_cast<int>(sizeof(T)), W = kGroup / PerWord;
+        const Bits* b = reinterpret_cast<const Bits*>(row);
+        uint32_t w[W] = {};
 #pragma unroll
-    for (int e = 0; e < kGroup; ++e)
-        if (e < n) p[e] = narrow<T>(x[e]);
+        for (int e = 0; e < kGroup; ++e)
+            w[e / PerWord] |= static_cast<uint32_t>(b[e < c.end ? e : c.end - 1])
+                              << (e % PerWord * 16);
+        Group<T> g;
+#pragma unroll
+        for (int i = 0; i < W; ++i) g.v[i / 4][i % 4] = w[i];
+        return g;
+    }
 }
 
 template <typename T>
-__device__ __forceinline__ Group<T> load_any(const T* p, int n) {
-    return n >= kGroup ? load_group(p) : load_some(p, n);
-}
-template <typename T>
-__device__ __forceinline__ void store_any(T* p, const float (&x)[kGroup], int n) {
-    if (n >= kGroup) store_group(p, x);
-    else store_some(p, x, n);
+__device__ __forceinline__ void store_columns(T* row, const Columns& c, const float (&x)[kGroup]) {
+    if (c.whole()) {
+        store_group(row + c.at, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e)
+            if (e >= c.own && e < c.end) row[c.at + e] = narrow<T>(x[e]);
+    }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -103,33 +116,41 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
     const int64_t first = row_of(unit, p.splits);
     const int split = static_cast<int>(unit - first * p.splits);
     const int64_t t = (first << (8 - p.shift)) + (tid >> p.shift);
-    if (t >= p.tokens) return;
-    const int lane = tid & ((1 << p.shift) - 1);
+    const int col = ((split * kLookupGroups << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
+    if (t >= p.tokens || col >= p.dim) return;
     const int64_t id = p.ids[t];
     const bool inside = id >= 0 && id < p.vocab;
-    const In* src = static_cast<const In*>(p.table) + (inside ? id : 0) * p.tstride;
     Out* dst = static_cast<Out*>(p.out) + t * p.ostride;
-    Group<In> raw[kLookupGroups];
-    int at[kLookupGroups];
-#pragma unroll
-    for (int q = 0; q < kLookupGroups; ++q) {
-        at[q] = (((split * kLookupGroups + q) << p.shift) + lane) * kGroup;
-        if (inside && at[q] < p.dim) raw[q] = load_any(src + at[q], p.dim - at[q]);
-    }
-    const float other = id < 0 ? 0.0f : __builtin_nanf("");
-#pragma unroll
-    for (int q = 0; q < kLookupGroups; ++q) {
-        if (at[q] >= p.dim) break;
+    if (!inside) {
         float x[kGroup];
-        if (inside) {
-            widen_group(raw[q], x);
 #pragma unroll
-            for (int e = 0; e < kGroup; ++e) x[e] *= p.scale;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kGroup; ++e) x[e] = other;
+        for (int e = 0; e < kGroup; ++e) x[e] = id < 0 ? 0.0f : __builtin_nanf("");
+        for (int q = 0; q < kLookupGroups; ++q) {
+            const int at = col + (q << p.shift) * kGroup;
+            if (at < p.dim) store_columns(dst, Columns(at, p.dim), x);
         }
-        store_any(dst + at[q], x, p.dim - at[q]);
+        return;
+    }
+    const In* src = static_cast<const In*>(p.table) + id * p.tstride;
+    Group<In> raw[kLookupGroups];
+    const auto load = [&](auto narrow) {
+#pragma unroll
+        for (int q = 0; q < kLookupGroups; ++q) {
+            const int at = col + (q << p.shift) * kGroup;
+            raw[q] = load_columns<decltype(narrow)::value>(src, Columns(at < p.dim ? at : col, p.dim));
+        }
+    };
+    if (p.dim < kGroup) load(std::true_type{});
+    else load(std::false_type{});
+#pragma unroll
+    for (int q = 0; q < kLookupGroups; ++q) {
+        const int at = col + (q << p.shift) * kGroup;
+        if (at >= p.dim) break;
+        float x[kGroup];
+        widen_group(raw[q], x);
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) x[e] *= p.scale;
+        store_columns(dst, Columns(at, p.dim), x);
     }
 }
 
@@ -142,9 +163,9 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
 // and goes through the tokens again to place its own.  All work-groups read all tokens twice, from the
 // caches.
 
-constexpr int kRangeThreads = 512, kRangeWaves = kRangeThreads / kWave;
-constexpr int kMaxRange = 1024;             // rows of a range; their counts, one a wave, fit the LDS
-constexpr int kRangeAhead = 4;              // tokens a lane loads at once
+constexpr int kRangeThreads = 1024, kRangeWaves = kRangeThreads / kWave;
+constexpr int kMaxRange = 1000;             // rows of a range; their counts, one a wave, fit the LDS
+constexpr int kRangeAhead = 16;             // tokens a lane loads at once
 
 struct SortParams {
     const int64_t* ids;
@@ -420,20 +441,20 @@ struct GradParams {
     int64_t sum_units, unit0;
 };
 
+// A row's sum goes to the table; `old` is what is there, where sums are added to it.
 template <typename Out>
-__device__ __forceinline__ void put_sum(const GradParams& p, uint32_t key, int col,
-                                        float (&sum)[kGroup]) {
-    Out* at = static_cast<Out*>(p.table) + key * p.tstride + col;
-    const int n = p.dim - col;
+__device__ __forceinline__ void put_sum(const GradParams& p, uint32_t key, const Columns& cols,
+                                        const float (&sum)[kGroup], const Group<Out>* old) {
+    float x[kGroup];
 #pragma unroll
-    for (int e = 0; e < kGroup; ++e) sum[e] *= p.scale;
-    if (p.accumulate) {
-        float old[kGroup];
-        widen_group(load_any(at, n), old);
+    for (int e = 0; e < kGroup; ++e) x[e] = sum[e] * p.scale;
+    if (old) {
+        float y[kGroup];
+        widen_group(*old, y);
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) sum[e] += old[e];
+        for (int e = 0; e < kGroup; ++e) x[e] += y[e];
     }
-    store_any(at, sum, n);
+    store_columns(static_cast<Out*>(p.table) + key * p.tstride, cols, x);
 }
 
 // Zeros for the rows without a token, a wave each in turn.
@@ -472,10 +493,10 @@ __device__ __forceinline__ uint32_t sorted(const uint32_t* p, int64_t i) {
         return p[i];
 }
 
-template <typename In, typename Out, bool Uniform>
+template <typename In, typename Out, bool Uniform, bool Add>
 __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
     const int64_t unit = p.unit0 + blockIdx.x;
-    if (unit >= p.sum_units) {
+    if (!Add && unit >= p.sum_units) {
         fill_rows<Out>(p, unit - p.sum_units);
         return;
     }
@@ -486,12 +507,15 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
     if constexpr (Uniform) c = __builtin_amdgcn_readfirstlane(c);
     const int col = ((split << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
     if (c >= p.chunks || col >= p.dim) return;
+    const Columns cols(col, p.dim);
     const uint32_t none = static_cast<uint32_t>(p.vocab);
     const int tokens = static_cast<int>(p.tokens), begin = c * p.chunk;
     const int end = begin + p.chunk < tokens ? begin + p.chunk : tokens;
     const int after = end + p.chunk < tokens ? end + p.chunk : tokens;    // of the next chunk
-    const auto key_at = [&](int i) { return i < tokens ? sorted<Uniform>(p.keys, i) : none; };
-    const In* src = static_cast<const In*>(p.dout) + col;
+    const auto key_at = [&](int i) {
+        const uint32_t k = sorted<Uniform>(p.keys, i < tokens ? i : tokens - 1);
+        return i < tokens ? k : none;
+    };
     uint32_t skip = none;                   // the run before's, if that followed it here
     bool comes = false;
     if (const uint32_t k = key_at(begin); k >= none) {
@@ -502,19 +526,38 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
         if (starts && key_at(end) != k) skip = k;
         else comes = true;
     }
+    // Loads are unconditional; for a place that is not wanted, of the chunk's first row.
+    const In* src = static_cast<const In*>(p.dout);
+    const Out* table = static_cast<const Out*>(p.table);
+    const uint32_t idle = sorted<Uniform>(p.order, begin), idle_key = key_at(begin);
     float sum[kGroup] = {};
     bool follows = false;                   // past the chunk's end
     for (int j0 = begin; j0 < (follows ? after : end); j0 += kAhead) {
         const int limit = follows ? after : end;
-        uint32_t key[kAhead + 1];
+        uint32_t key[kAhead + 1], order[kAhead];
         Group<In> raw[kAhead];
+        Group<Out> old[Add ? kAhead : 1];
 #pragma unroll
         for (int q = 0; q <= kAhead; ++q) key[q] = key_at(j0 + q);
-        const uint32_t current = key[0];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q)
-            if (j0 + q < limit && (follows ? key[q] == current : key[q] < none && key[q] != skip))
-                raw[q] = load_any(src + sorted<Uniform>(p.order, j0 + q) * p.dstride, p.dim - col);
+            order[q] = sorted<Uniform>(p.order, j0 + q < limit ? j0 + q : begin);
+        const auto load = [&](auto narrow) {
+            constexpr bool Narrow = decltype(narrow)::value;
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const bool want = j0 + q < limit &&
+                                  (follows ? key[q] == key[0] : key[q] < none && key[q] != skip);
+                raw[q] = load_columns<Narrow>(src + (want ? order[q] : idle) * p.dstride, cols);
+                if constexpr (Add) {
+                    const bool ends = want && key[q + 1] != key[q];
+                    old[q] = load_columns<Narrow>(table + (ends ? key[q] : idle_key) * p.tstride,
+                                                  cols);
+                }
+            }
+        };
+        if (!Uniform && p.dim < kGroup) load(std::true_type{});
+        else load(std::false_type{});
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
             const int j = j0 + q;
@@ -539,7 +582,7 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
             if (comes)
                 store_group(p.head + static_cast<int64_t>(c) * p.padded + col, sum);
             else
-                put_sum<Out>(p, key[q], col, sum);
+                put_sum<Out>(p, key[q], cols, sum, Add ? &old[q] : nullptr);
             if (j + 1 >= end) return;
             comes = false;
 #pragma unroll
@@ -600,12 +643,19 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(GradParams p) 
             float x[kGroup];
             widen_group(load_group(p.tail + c * p.padded + col), x);
 #pragma unroll
-            for (int e = 0; e < kGroup; ++e) {
-                total[e] += x[e];
-                for (int w = 1; w < kJoinWaves; ++w) total[e] += parts[w - 1][lane][e];
-                x[e] = static_cast<float>(total[e]);
-            }
-            put_sum<Out>(p, key, col, x);
+            for (int e = 0; e < kGroup; ++e) total[e] += x[e];
+#pragma unroll 1
+            for (int w = 1; w < kJoinWaves; ++w)
+#pragma unroll
+                for (int e = 0; e < kGroup; ++e) total[e] += parts[w - 1][lane][e];
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) x[e] = static_cast<float>(total[e]);
+            const Columns cols(col, p.dim);
+            Group<Out> old;
+            const Out* row = static_cast<const Out*>(p.table) + key * p.tstride;
+            if (p.accumulate)
+                old = p.dim < kGroup ? load_columns<true>(row, cols) : load_columns<false>(row, cols);
+            put_sum<Out>(p, key, cols, x, p.accumulate ? &old : nullptr);
         }
     }
 }
@@ -670,16 +720,25 @@ bool in_one_launch(int64_t tokens, int64_t vocab) {
     return tokens * ((vocab + rows - 1) / rows) <= kOneLaunchReads;
 }
 
-constexpr int64_t kMinChunk = 32, kMaxChunks = 2048;
+
+// Tokens of a chunk: as many as give kFewChunks of them, but at least kAhead and at most kChunk, unless
+// that makes more than kMostChunks, whose parts take workspace.
+constexpr int64_t kChunk = 32, kFewChunks = 512, kMostChunks = 2048;
+
+int64_t chunk_of(int64_t tokens) {
+    const int64_t few = (tokens + kFewChunks - 1) / kFewChunks;
+    const int64_t most = (tokens + kMostChunks - 1) / kMostChunks;
+    const int64_t n = few < kChunk ? few : kChunk;
+    return ((n > most ? n : most) + kAhead - 1) / kAhead * kAhead;
+}
 
 GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t dim) {
     GradLayout l{};
     const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
     l.blocks = static_cast<int32_t>((tokens + kSortTokens - 1) / kSortTokens);
     l.bits = digit_bits(vocab);
-    const int64_t even = (tokens + kMaxChunks - 1) / kMaxChunks;
-    l.chunk = static_cast<int32_t>(even > kMinChunk ? (even + kAhead - 1) / kAhead * kAhead : kMinChunk);
-    l.chunks = static_cast<int32_t>((tokens + l.chunk - 1) / l.chunk);
+    l.chunk = static_cast<int32_t>(chunk_of(tokens));
+    l.chunks = tokens > 0 ? static_cast<int32_t>((tokens + l.chunk - 1) / l.chunk) : 0;
     l.padded = static_cast<int32_t>((dim + kGroup - 1) / kGroup * kGroup);
     int64_t at = 0;
     const auto take = [&](int64_t bytes) {
@@ -700,6 +759,12 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t dim) {
     }
     l.bytes = at;
     return l;
+}
+
+template <typename In, typename Out, bool Add>
+const void* grad_form(const GradParams& p) {
+    return p.shift < 6 ? KERNEL(embed_grad_kernel<In, Out, false, Add>)
+                       : KERNEL(embed_grad_kernel<In, Out, true, Add>);
 }
 
 int sort_ranges(SortParams& s, void* stream) {
@@ -826,8 +891,7 @@ extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
     const void* kernel = by_dtypes(dout->dtype, dtable->dtype, [&](auto a, auto b) {
         using In = decltype(a);
         using Out = decltype(b);
-        return th.shift >= 6 ? KERNEL(embed_grad_kernel<In, Out, true>)
-                             : KERNEL(embed_grad_kernel<In, Out, false>);
+        return accumulate ? grad_form<In, Out, true>(p) : grad_form<In, Out, false>(p);
     });
     rc = launch_units(kernel, p.sum_units + fill, p, 0, stream);
     if (rc != FSDPSHARD_OK || l.chunks < 3) return rc;      // no run is long

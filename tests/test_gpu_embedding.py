@@ -1,6 +1,6 @@
 """Embedding lookup and its gradient on the GPU.  The lookup is one float32 product and one rounding,
 so it is compared bit for bit.  The gradient's bound: with u = 2^-24 a row's float32 sums are chains of
-at most 2 chunk additions of terms of total size S (a chunk is max(32, tokens / 2048) tokens, rounded up
+at most 2 chunk additions of terms of total size S (a chunk is at most max(32, tokens / 2048) tokens, rounded up
 to 8, and a run's sum goes on into the next one), their float64 sum is rounded once, and the product with
 the scale, the sum with what was there and the rounding to the type come last: u S (2 chunk + 1) + u |d| +
 u |result| + half a step of the type."""
