@@ -160,11 +160,11 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
 //
 // Where tokens are not too many (kOneLaunchReads) each work-group sorts the tokens of a range of rows by itself, in one launch:
 // it counts the tokens of lower rows, which is where its own ones start, and those of each of its rows,
-// and goes through the tokens again to place its own.  All work-groups read all tokens twice, from the
-// caches.
+// and places them.  A wave that finds too many for its list goes through its tokens again.
 
 constexpr int kRangeThreads = 1024, kRangeWaves = kRangeThreads / kWave;
-constexpr int kMaxRange = 1000;             // rows of a range; their counts, one a wave, fit the LDS
+constexpr int kMaxRange = 512;              // rows of a range; their counts, one a wave, fit the LDS
+constexpr int kRangeList = 256;             // tokens of a range that a wave keeps in the LDS
 constexpr int kRangeAhead = 16;             // tokens a lane loads at once
 
 struct SortParams {
@@ -224,6 +224,7 @@ __device__ __forceinline__ unsigned long long lanes_with(uint32_t d, int bits,
 
 __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p) {
     extern __shared__ uint32_t place[];     // [kRangeWaves][range]
+    __shared__ uint32_t list[kRangeWaves][kRangeList];
     __shared__ uint32_t sh[kRangeWaves];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int64_t low = (p.unit0 + blockIdx.x) * p.range;
@@ -235,23 +236,50 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p)
     // A wave's tokens are consecutive.
     const int64_t each = (p.tokens + kRangeThreads - 1) / kRangeThreads * kWave;
     const int64_t begin = wave * each, end = begin + each < p.tokens ? begin + each : p.tokens;
+    // f(row of the range, whether the lane's token is in it, the token counted from `begin`)
     const auto stream = [&](auto f) {
         for (int64_t i0 = begin + lane; i0 - lane < end; i0 += kRangeAhead * kWave) {
             int64_t id[kRangeAhead];
 #pragma unroll
-            for (int q = 0; q < kRangeAhead; ++q)
-                id[q] = i0 + q * kWave < end ? p.ids[i0 + q * kWave] : -1;
+            for (int q = 0; q < kRangeAhead; ++q) {
+                const int64_t i = i0 + q * kWave;
+                id[q] = p.ids[i < end ? i : end - 1];
+                if (i >= end) id[q] = -1;
+            }
 #pragma unroll
-            for (int q = 0; q < kRangeAhead; ++q) f(id[q], i0 + q * kWave);
+            for (int q = 0; q < kRangeAhead; ++q) {
+                const uint64_t row = static_cast<uint64_t>(id[q]) - static_cast<uint64_t>(low);
+                f(id[q], static_cast<uint32_t>(row), row < static_cast<uint64_t>(rows),
+                  static_cast<uint32_t>(i0 + q * kWave - begin));
+            }
         }
     };
+    const auto before_me = [](unsigned long long lanes) {
+        return static_cast<int>(__builtin_amdgcn_mbcnt_hi(
+            static_cast<uint32_t>(lanes >> 32),
+            __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(lanes), 0)));
+    };
+    // The range's tokens, in their order; all that the tokens of other rows cost is a comparison.
     uint32_t lower = 0;
-    stream([&](int64_t id, int64_t) {
-        if (id >= 0 && id < low) ++lower;
-        if (id >= low && id - low < rows) atomicAdd(&mine[id - low], 1u);
+    int found = 0;
+    stream([&](int64_t id, uint32_t row, bool here, uint32_t i) {
+        lower += __popcll(__ballot(static_cast<uint64_t>(id) < static_cast<uint64_t>(low)));
+        const unsigned long long some = __ballot(here);
+        if (some == 0) return;
+        const int at = found + before_me(some);
+        if (here && at < kRangeList) list[wave][at] = row << 16 | i;
+        found += __popcll(some);
     });
+    const bool listed = found <= kRangeList;           // of the whole wave
+    if (listed) {
+        for (int k = lane; k < found; k += kWave) atomicAdd(&mine[list[wave][k] >> 16], 1u);
+    } else {
+        stream([&](int64_t, uint32_t row, bool here, uint32_t) {
+            if (here) atomicAdd(&mine[row], 1u);
+        });
+    }
     uint32_t start;
-    block_scan<kRangeWaves>(lower, sh, start);
+    block_scan<kRangeWaves>(lane == 0 ? lower : 0, sh, start);
     // Where each wave's first token of each row goes.
     const int per = (p.range + kRangeThreads - 1) / kRangeThreads;
     uint32_t sum = 0;
@@ -276,23 +304,29 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p)
     if (low + rows == p.vocab)              // the last range: tokens without a row
         for (int64_t i = start + own + tid; i < p.tokens; i += kRangeThreads)
             p.keys[i] = static_cast<uint32_t>(p.vocab);
-    stream([&](int64_t id, int64_t i) {
-        const bool here = id >= low && id - low < rows;
+    const auto put = [&](uint32_t row, bool here, uint32_t i) {
         const unsigned long long some = __ballot(here);
         if (some == 0) return;
-        const uint32_t d = here ? static_cast<uint32_t>(id - low) : 0;
-        const unsigned long long same = lanes_with(d, p.bits, some);
-        const int before = __popcll(same & ((1ull << lane) - 1));
+        const unsigned long long same = lanes_with(here ? row : 0, p.bits, some);
+        const int before = before_me(same);
         uint32_t to = 0;
         if (here) {
-            to = mine[d] + before;
-            p.keys[to] = static_cast<uint32_t>(id);
-            p.order[to] = static_cast<uint32_t>(i);
+            to = mine[row] + before;
+            p.keys[to] = static_cast<uint32_t>(low) + row;
+            p.order[to] = static_cast<uint32_t>(begin) + i;
         }
         wave_fence();                       // every lane has read its place
-        if (here && before == 0) mine[d] = to + __popcll(same);
+        if (here && before == 0) mine[row] = to + __popcll(same);
         wave_fence();
-    });
+    };
+    if (listed) {
+        for (int k = lane; k - lane < found; k += kWave) {
+            const uint32_t x = k < found ? list[wave][k] : 0;
+            put(x >> 16, k < found, x & 0xFFFF);
+        }
+    } else {
+        stream([&](int64_t, uint32_t row, bool here, uint32_t i) { put(row, here, i); });
+    }
 }
 
 // More tokens take two stable passes over half of a key's bits each.  A work-group ranks kSortTokens
@@ -709,6 +743,7 @@ struct GradLayout {
 // them read all tokens: up to kOneLaunchReads readings in all, tokens are sorted so.
 constexpr int64_t kRanges = 128;
 constexpr int64_t kOneLaunchReads = int64_t{1} << 24;
+static_assert(kOneLaunchReads / kRanges / kRangeWaves < 1 << 16, "a wave's tokens take 16 bits");
 
 int64_t range_rows(int64_t vocab) {
     const int64_t even = (vocab + kRanges - 1) / kRanges;
@@ -716,10 +751,9 @@ int64_t range_rows(int64_t vocab) {
 }
 bool in_one_launch(int64_t tokens, int64_t vocab) {
     if (vocab == 0) return true;
-    const int64_t rows = range_rows(vocab);
-    return tokens * ((vocab + rows - 1) / rows) <= kOneLaunchReads;
+    const int64_t rows = range_rows(vocab), ranges = (vocab + rows - 1) / rows;
+    return tokens * (ranges > kRanges ? ranges : kRanges) <= kOneLaunchReads;
 }
-
 
 // Tokens of a chunk: as many as give kFewChunks of them, but at least kAhead and at most kChunk, unless
 // that makes more than kMostChunks, whose parts take workspace.
