@@ -39,11 +39,15 @@ __device__ __forceinline__ void widen_group(const Group<T>& g, float (&x)[kGroup
     for (int i = 0; i < kGroupVecs<T>; ++i) unpack<T>(g.v[i], x + i * kElems<T>);
 }
 
-template <typename T>
+// Once: without keeping it in a cache.
+template <bool Once = false, typename T>
 __device__ __forceinline__ void store_group(T* p, const float (&x)[kGroup]) {
 #pragma unroll
-    for (int i = 0; i < kGroupVecs<T>; ++i)
-        *reinterpret_cast<loose_vec*>(p + i * kElems<T>) = pack<T>(x + i * kElems<T>);
+    for (int i = 0; i < kGroupVecs<T>; ++i) {
+        loose_vec* at = reinterpret_cast<loose_vec*>(p + i * kElems<T>);
+        if constexpr (Once) __builtin_nontemporal_store(pack<T>(x + i * kElems<T>), at);
+        else *at = pack<T>(x + i * kElems<T>);
+    }
 }
 
 // A thread's columns.  The group that a row's end cuts short is loaded as the row's last 8 elements, so
@@ -471,7 +475,7 @@ struct GradParams {
     uint32_t* long_runs;                    // their number, then the chunks in which they start
     int32_t dim, padded, chunk, chunks, splits, shift;
     float scale;
-    int32_t accumulate;
+    int32_t accumulate, once;
     int64_t sum_units, unit0;
 };
 
@@ -488,7 +492,9 @@ __device__ __forceinline__ void put_sum(const GradParams& p, uint32_t key, const
 #pragma unroll
         for (int e = 0; e < kGroup; ++e) x[e] += y[e];
     }
-    store_columns(static_cast<Out*>(p.table) + key * p.tstride, cols, x);
+    Out* row = static_cast<Out*>(p.table) + key * p.tstride;
+    if (p.once) store_group<true>(row + cols.at, x);       // (whole lines are whole groups)
+    else store_columns(row, cols, x);
 }
 
 // Zeros for the rows without a token, a wave each in turn.
@@ -510,6 +516,12 @@ __device__ void fill_rows(const GradParams& p, int64_t unit) {
         if (skip[i]) continue;
         Out* row = static_cast<Out*>(p.table) + (v0 + i * kWaves) * p.tstride;
         int col = lane * E;
+        if (p.once) {
+            for (; col < p.dim; col += kWave * E)
+                __builtin_nontemporal_store(u32x4{0, 0, 0, 0},
+                                            reinterpret_cast<loose_vec*>(row + col));
+            continue;
+        }
         for (; col + E <= p.dim; col += kWave * E)
             *reinterpret_cast<loose_vec*>(row + col) = u32x4{0, 0, 0, 0};
         for (; col < p.dim; ++col) row[col] = narrow<Out>(0.0f);
@@ -801,6 +813,14 @@ const void* grad_form(const GradParams& p) {
                        : KERNEL(embed_grad_kernel<In, Out, true, Add>);
 }
 
+// Whether rows start and end with the caches' lines.
+constexpr int kLine = 128;
+bool whole_lines(const fsdpshard_matrix* m) {
+    const int64_t elem = element_bytes(m->dtype);
+    return reinterpret_cast<uintptr_t>(m->data) % kLine == 0 && m->cols * elem % kLine == 0 &&
+           (m->rows <= 1 || m->row_stride * elem % kLine == 0);
+}
+
 int sort_ranges(SortParams& s, void* stream) {
     s.range = static_cast<int32_t>(range_rows(s.vocab));
     s.bits = 0;
@@ -919,6 +939,7 @@ extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
     p.shift = th.shift;
     p.scale = scale;
     p.accumulate = accumulate;
+    p.once = !accumulate && whole_lines(dtable);
     const int64_t per = kBlock >> th.shift;
     p.sum_units = (l.chunks + per - 1) / per * th.splits;
     const int64_t fill = accumulate ? 0 : (vocab + kFillRows - 1) / kFillRows;
