@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
 
 constexpr int kRangeThreads = 1024, kRangeWaves = kRangeThreads / kWave;
 constexpr int kMaxRange = 512;              // rows of a range; their counts, one a wave, fit the LDS
-constexpr int kRangeList = 256;             // tokens of a range that a wave keeps in the LDS
+constexpr int kRangeList = 1024;            // tokens of a range that a wave keeps in the LDS
 constexpr int kRangeAhead = 16;             // tokens a lane loads at once
 
 struct SortParams {
@@ -227,13 +227,13 @@ __device__ __forceinline__ unsigned long long lanes_with(uint32_t d, int bits,
 }
 
 __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p) {
-    extern __shared__ uint32_t place[];     // [kRangeWaves][range]
-    __shared__ uint32_t list[kRangeWaves][kRangeList];
+    extern __shared__ uint32_t place[];     // [kRangeWaves][range], then the lists
     __shared__ uint32_t sh[kRangeWaves];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int64_t low = (p.unit0 + blockIdx.x) * p.range;
     const int rows = static_cast<int>(p.vocab - low < p.range ? p.vocab - low : p.range);
     uint32_t* mine = place + wave * p.range;
+    uint32_t* list = place + kRangeWaves * p.range + wave * kRangeList;
     for (int i = tid; i < kRangeWaves * p.range; i += kRangeThreads) place[i] = 0;
     if (tid == 0 && blockIdx.x == 0) *p.long_runs = 0;
     __syncthreads();
@@ -271,12 +271,12 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p)
         const unsigned long long some = __ballot(here);
         if (some == 0) return;
         const int at = found + before_me(some);
-        if (here && at < kRangeList) list[wave][at] = row << 16 | i;
+        if (here && at < kRangeList) list[at] = row << 16 | i;
         found += __popcll(some);
     });
     const bool listed = found <= kRangeList;           // of the whole wave
     if (listed) {
-        for (int k = lane; k < found; k += kWave) atomicAdd(&mine[list[wave][k] >> 16], 1u);
+        for (int k = lane; k < found; k += kWave) atomicAdd(&mine[list[k] >> 16], 1u);
     } else {
         stream([&](int64_t, uint32_t row, bool here, uint32_t) {
             if (here) atomicAdd(&mine[row], 1u);
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p)
     };
     if (listed) {
         for (int k = lane; k - lane < found; k += kWave) {
-            const uint32_t x = k < found ? list[wave][k] : 0;
+            const uint32_t x = k < found ? list[k] : 0;
             put(x >> 16, k < found, x & 0xFFFF);
         }
     } else {
@@ -640,7 +640,7 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
 // The long runs.  A work-group takes 64 groups of a run's columns; its waves take the heads in turn, and
 // their float64 sums are added up in the waves' order.
 constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave;
-constexpr int kJoinAhead = 4, kJoinGroups = 512;
+constexpr int kJoinAhead = 4, kJoinGroups = 1024;
 
 template <typename Out>
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(GradParams p) {
@@ -826,7 +826,7 @@ int sort_ranges(SortParams& s, void* stream) {
     s.bits = 0;
     while ((1 << s.bits) < s.range) ++s.bits;
     return launch_units(KERNEL(sort_range_kernel), (s.vocab + s.range - 1) / s.range, s,
-                        int64_t{4} * kRangeWaves * s.range, stream, kRangeThreads);
+                        int64_t{4} * kRangeWaves * (s.range + kRangeList), stream, kRangeThreads);
 }
 
 int sort_digits(SortParams& s, const GradLayout& l, char* ws, void* stream) {
