@@ -109,12 +109,6 @@ __device__ __forceinline__ Place open_list(const DistillParams& p, int64_t r, co
 __device__ __forceinline__ bool list_some(const List& list) { return list.some[0] || list.some[1]; }
 __device__ __forceinline__ bool list_bad(const List& list) { return list.bad[0] || list.bad[1]; }
 
-// The bits of element e of a vector in its word.
-template <typename T>
-__device__ __forceinline__ uint32_t element_bits(int e) {
-    return sizeof(T) == 4 ? ~0u : e % 2 ? 0xFFFF0000u : 0xFFFFu;
-}
-
 // Enters a token into the map of vectors [lo, hi): map[v - lo] becomes 1 + the slot of its vector,
 // which is the number of the place that came first.  Whichever that is, the results are the same.
 // `map` and the slots' masks are clear; before the next step: a barrier.
@@ -362,14 +356,6 @@ __device__ __forceinline__ void clear_map(uint8_t* map, int bytes, int threads) 
 //              hide each other's work on the lists.
 // A launch has a work-group for each row and no loop over rows: in a loop the compiler would keep
 // the constants of the float64 functions in registers, twice as many as the rest needs.
-
-// Keeps the compiler from holding the floats of an earlier unpacking of the row (two registers for
-// each one of 16-bit elements) instead of unpacking it again.
-template <int N>
-__device__ __forceinline__ void forget_floats(u32x4 (&raw)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(raw[i]));
-}
 
 struct WholeScratch {
     float wave_top[kMaxWaves], wave_rest[kMaxWaves];

@@ -431,6 +431,20 @@ __device__ __forceinline__ void mask_out(u32x4& raw, u32x4 drop) {
     raw = (raw & ~drop) | (drop & kMinusInfBits<T>);
 }
 
+// The bits of element e of a vector in its word.
+template <typename T>
+__device__ __forceinline__ uint32_t element_bits(int e) {
+    return sizeof(T) == 4 ? ~0u : e % 2 ? 0xFFFF0000u : 0xFFFFu;
+}
+
+// Keeps the compiler from holding the floats of an earlier unpacking of the row (two registers for
+// each one of 16-bit elements) instead of unpacking it again.
+template <int N>
+__device__ __forceinline__ void forget_floats(u32x4 (&raw)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(raw[i]));
+}
+
 // Streams a part: calls fix(raw, v) for each whole vector (it may mask elements out), batch(x, b)
 // with kBatch floats of this thread's b-th batch of whole vectors (-inf past the end), and edge(x, v)
 // with the kElems floats of a partial vector v.  Once: the matrix is too large to be found in a cache

@@ -51,7 +51,7 @@ struct RowScratch {
 };
 
 template <typename T, int Threads, int Vecs, bool Entropy, bool Once>
-__global__ __launch_bounds__(Threads) void policy_whole_kernel(PolicyLogitsParams p) {
+__global__ __launch_bounds__(Threads, 4) void policy_whole_kernel(PolicyLogitsParams p) {
     constexpr int E = kElems<T>, W = Threads / kWave;
     __shared__ BlockScratch bs;
     __shared__ RowScratch sh;
@@ -76,24 +76,40 @@ __global__ __launch_bounds__(Threads) void policy_whole_kernel(PolicyLogitsParam
     u32x4 raw[Vecs];
 #pragma unroll
     for (int i = 0; i < Vecs; ++i) {
-        const int v = tid + i * Threads, at = v < row.nvec ? v : 0;
-        raw[i] = Once ? row.load_once(at) : row.load(at);
+        const int v = tid + i * Threads;
+        if (v < row.nvec) raw[i] = Once ? row.load_once(v) : row.load(v);
+        else raw[i] = u32x4{kMinusInfBits<T>, kMinusInfBits<T>, kMinusInfBits<T>,
+                            kMinusInfBits<T>};
     }
     const float token_logit = row.at(static_cast<int>(y));
+    // The first and the last vector's elements that are not the row's become -inf.
+    const int end = row.phase + row.vocab - (row.nvec - 1) * E;    // of the last vector
+    u32x4 first_mask = {0, 0, 0, 0}, last_mask = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e < row.phase) first_mask[e * 4 / E] |= element_bits<T>(e);
+        if (e >= end) last_mask[e * 4 / E] |= element_bits<T>(e);
+    }
     Acc acc;
     constexpr int Step = Vecs < kLoads<T> ? Vecs : kLoads<T>;
 #pragma unroll
     for (int i0 = 0; i0 < Vecs; i0 += Step) {
         float x[Step * E];
 #pragma unroll
-        for (int i = 0; i < Step; ++i) unpack<T>(raw[i0 + i], x + i * E);
+        for (int i = 0; i < Step; ++i) {
+            const int v = tid + (i0 + i) * Threads;
+            if (v == 0) mask_out<T>(raw[i0 + i], first_mask);
+            if (v == row.nvec - 1) mask_out<T>(raw[i0 + i], last_mask);
+        }
 #pragma unroll
-        for (int i = 0; i < Step * E; ++i) {
-            const int at = (tid + (i0 + i / E) * Threads) * E + i % E - row.phase;
-            if (at < 0 || at >= row.vocab) x[i] = -kInf;
+        for (int i = 0; i < Step; ++i) {
+            asm volatile("" : "+v"(raw[i0 + i]));      // one batch's floats at a time
+            unpack<T>(raw[i0 + i], x + i * E);
         }
         add_batch<Step * E, Entropy>(acc, x, max_of<Step * E>(x), c2);
+        asm volatile("" : "+v"(acc.m), "+v"(acc.s), "+v"(acc.t));
     }
+    forget_floats(raw);
     const Set set = join_threads<Entropy, W>(acc, c2, bs, [&](int j, float m) {
         float2 rest = make_float2(0.0f, 0.0f);
         if (tid == j) {
@@ -101,16 +117,12 @@ __global__ __launch_bounds__(Threads) void policy_whole_kernel(PolicyLogitsParam
             for (int i = 0; i < Vecs; ++i) {
                 float x[E];
                 unpack<T>(raw[i], x);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int at = (tid + i * Threads) * E + e - row.phase;
-                    if (at < 0 || at >= row.vocab) x[e] = -kInf;
-                }
                 add_rest<E, Entropy>(rest, x, m, c2);
             }
         }
         return rest;
     });
+    forget_floats(raw);
     // -p_i (g + h (log p_i + H)) c = 2^u (coef + tilt u) with u = c2 (x_i - m): log p_i + H is
     // ln 2 (u - t / s).
     if (tid < kWave) {
@@ -150,6 +162,13 @@ __global__ __launch_bounds__(Threads) void policy_whole_kernel(PolicyLogitsParam
     const float m = set.m, coef = sh.coef, tilt = sh.tilt, token = sh.token;
     const int token_vec = (static_cast<int>(y) + row.phase) / E;
     const int token_elem = (static_cast<int>(y) + row.phase) % E;
+    const auto with_token = [&](float* x, int v) {
+        if (v == token_vec) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = e == token_elem ? token : x[e];
+        }
+        return pack<T>(x);
+    };
     const auto gradient = [&](float* x, int v) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -157,24 +176,42 @@ __global__ __launch_bounds__(Threads) void policy_whole_kernel(PolicyLogitsParam
             x[e] = exp2_fast(u) *
                    (Entropy ? __builtin_fmaf(tilt, fmaxf(u, kNegligible), coef) : coef);
         }
-        if (v == token_vec) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = e == token_elem ? token : x[e];
-        }
-        return pack<T>(x);
+        return with_token(x, v);
     };
+    // 2^u by one fused multiply-add, as in add_batch: of u' = c2 x - b, which is u - delta.  Far from 0
+    // the difference is taken first, and the row is read again.
+    const float base = c2 * m, delta = __builtin_fmaf(c2, m, -base), up = exp2_fast(-delta);
+    if (fabsf(base) < 0x1p20f) {
+        const float near_tilt = tilt * up, near_coef = __builtin_fmaf(-tilt, delta, coef) * up;
+        int t = tid;                       // not the first pass's indices, kept in registers
+        asm volatile("" : "+v"(t));
 #pragma unroll
-    for (int i = 0; i < Vecs; ++i) {
-        const int v = tid + i * Threads;
-        if (v < part.va || v >= part.vb) continue;
-        float x[E];
-        unpack<T>(raw[i], x);
-        out.put(v, gradient(x, v));
+        for (int i = 0; i < Vecs; ++i) {
+            const int v = t + i * Threads;
+            if (v < part.va || v >= part.vb) continue;
+            float x[E];
+            unpack<T>(raw[i], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float u = __builtin_fmaf(c2, x[e], -base);
+                x[e] = exp2_fast(u) *
+                       (Entropy ? __builtin_fmaf(near_tilt, fmaxf(u, kNegligible), near_coef)
+                                : near_coef);
+            }
+            out.put(v, with_token(x, v));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {
+        for (int v = part.va + tid; v < part.vb; v += Threads) {
+            float x[E];
+            unpack<T>(row.load(v), x);
+            out.put(v, gradient(x, v));
+        }
     }
     if ((part.first && tid == 0) || (part.last && tid == 1)) {
         const int v = tid == 0 ? part.lo : part.hi - 1;
         float x[E];
-        row.get_masked(v, x);          // not written yet, also in place
+        row.get_masked(v, x);              // not written yet, also in place
         out.put_masked(row, v, gradient(x, v));
     }
 }
