@@ -14,9 +14,14 @@ from oracle import policy as OP
 
 pytestmark = pytest.mark.gpu
 
-# around a lane's four tokens, a wave's 256, the one work-group's 16,384, and beyond it
-SIZES = [1, 2, 3, 5, 63, 255, 256, 257, 1023, 4099, 16384, 16385, 70001]
+# around a lane's four tokens, a wave's 256, the one work-group's 4,096, and beyond it
+SIZES = [1, 2, 3, 4, 5, 63, 255, 256, 257, 1023, 4095, 4096, 4097, 16385, 70001]
 FULL = OP.constants(0.2, 0.28, 1.4, 0.1, 0.02)
+
+
+VARIANTS = [dict(), dict(kind="hinge", beta=0.5, margin=0.2), dict(kind="squared", beta=0.5),
+            dict(beta=2.0, margin=0.5, label_smoothing=0.1, length_normalised=True),
+            dict(kind="squared", beta=0.1, length_normalised=True, margin=0.1)]
 
 
 def _seed(*key):
@@ -35,6 +40,7 @@ def test_policy_of_tokens(n):
 
 
 @pytest.mark.parametrize("n,sequences,behind", [(1, 1, 0), (5, 2, 1), (300, 9, 7), (300, 300, 0),
+                                                (3, 2, 0), (4096, 64, 1), (4096, 65, 0), (4097, 64, 0),
                                                 (4099, 1, 0), (16384, 70, 300), (16385, 70, 0),
                                                 (2000, 600, 3), (70001, 33, 5000),
                                                 (70001, 5000, 1)])
@@ -48,6 +54,45 @@ def test_policy_of_sequences(n, sequences, behind):
         x = P.rollout(rng, n, offsets, **kw)
         P.check_policy(c, x, offsets, P.run_policy(c, x, offsets, shift=(i + 1) % 4),
                        f"n={n} sequences={sequences} variant {i}")
+
+
+# Sequences around the chunks of a team of 64 or 256 threads (256 and 1,024 tokens) and that start
+# and end where its chunks do or next to it; means on both sides of 256 tokens.
+LENGTHS = [[256, 257, 1, 255], [1024, 1025, 1023, 4096, 1], [1, 511, 1024, 512, 1536], [5000],
+           [0, 257, 0, 0, 600, 3], [100, 9000, 100, 1, 1], [1023, 1, 1025, 9000, 7, 1024],
+           [3] * 300 + [600, 5, 2500] + [2] * 200, [10] * 500 + [9000, 1], [513] * 9, [1025] * 9]
+
+
+def _offsets(lengths, first=0):
+    return np.concatenate([[0], np.cumsum(lengths)]) + first
+
+
+@pytest.mark.parametrize("lengths", LENGTHS, ids=range(len(LENGTHS)))
+@pytest.mark.parametrize("first,behind", [(0, 0), (3, 2), (600, 700)])
+def test_policy_of_long_sequences(lengths, first, behind):
+    offsets = _offsets(lengths, first)
+    n = int(offsets[-1]) + behind
+    rng = _seed(n, len(lengths))
+    x = P.rollout(rng, n, offsets)
+    say(f"policy of {len(lengths)} sequences, {n} tokens")
+    P.check_policy(FULL, x, offsets, P.run_policy(FULL, x, offsets, shift=first % 4), f"{n}")
+
+
+@pytest.mark.parametrize("lengths", LENGTHS, ids=range(len(LENGTHS)))
+@pytest.mark.parametrize("first,behind", [(0, 0), (3, 2), (600, 700)])
+def test_preference_of_long_sequences(lengths, first, behind):
+    lengths = lengths + [77] * (len(lengths) % 2)
+    offsets = _offsets(lengths, first)
+    n, pairs = int(offsets[-1]) + behind, len(lengths) // 2
+    rng = _seed(n, len(lengths), 1)
+    x = P.rollout(rng, n)
+    g = rng.standard_normal(pairs).astype(np.float32)
+    say(f"preference of {pairs} pairs, {n} tokens")
+    for v in (VARIANTS[0], VARIANTS[3]):
+        got = P.run_preference(x, offsets, g, shift=first % 4, **v)
+        P.check_preference(x, offsets, g, got, f"{n}", **v)
+    got = P.run_preference(x, offsets, None)
+    P.check_preference(x, offsets, None, got, f"{n} loss only")
 
 
 def test_policy_sequences_that_start_late():
@@ -171,12 +216,8 @@ def test_policy_offsets_past_the_tokens():
         assert np.array_equal(got[name], want[name]), name
 
 
-VARIANTS = [dict(), dict(kind="hinge", beta=0.5, margin=0.2), dict(kind="squared", beta=0.5),
-            dict(beta=2.0, margin=0.5, label_smoothing=0.1, length_normalised=True),
-            dict(kind="squared", beta=0.1, length_normalised=True, margin=0.1)]
-
-
 @pytest.mark.parametrize("n,pairs,behind", [(2, 1, 0), (7, 1, 2), (300, 4, 9), (300, 200, 0),
+                                            (3, 1, 0), (4096, 32, 1), (4096, 33, 0), (4097, 32, 0),
                                             (5000, 3, 0), (16384, 256, 1), (16384, 257, 0),
                                             (16385, 5, 100), (70001, 37, 0), (90000, 2, 80000)])
 def test_preference(n, pairs, behind):
