@@ -97,10 +97,14 @@ __device__ __forceinline__ void store_columns(T* row, const Columns& c, const fl
 }
 
 // ------------------------------------------------------------------------------------------------
-// Lookup.  A work-group takes a row's part of kBlock * kLookupGroups groups, or several whole rows
+// Lookup.  A work-group takes a row's part of kLookupGroups groups a thread, or several whole rows
 // where they are short: 2^shift threads a row.
 
-constexpr int kLookupGroups = 2;
+// Groups a thread loads at once, then stores.  Measured, us with 1, 2 and 4: 16384 x 8192 bf16 84, 64 and
+// 59, 8192 x 4099 fp32 -> bf16 24, 32 (the last group has a work-group to itself) and 24, 16384 x 4096
+// bf16 -> fp32 76, 68 and 82.
+template <typename Out>
+constexpr int kLookupGroups = sizeof(Out) == 4 ? 2 : 4;
 
 struct LookupParams {
     const void* table;
@@ -108,19 +112,20 @@ struct LookupParams {
     const int64_t* ids;
     void* out;
     int64_t tokens, ostride;
-    int32_t dim, splits, shift;
+    int32_t dim, splits, shift, once;
     float scale;
     int64_t unit0;
 };
 
 template <typename In, typename Out>
 __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
+    constexpr int Each = kLookupGroups<Out>;
     const int tid = threadIdx.x;
     const int64_t unit = p.unit0 + unit_of_group();
     const int64_t first = row_of(unit, p.splits);
     const int split = static_cast<int>(unit - first * p.splits);
     const int64_t t = (first << (8 - p.shift)) + (tid >> p.shift);
-    const int col = ((split * kLookupGroups << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
+    const int col = ((split * Each << p.shift) + (tid & ((1 << p.shift) - 1))) * kGroup;
     if (t >= p.tokens || col >= p.dim) return;
     const int64_t id = p.ids[t];
     const bool inside = id >= 0 && id < p.vocab;
@@ -129,17 +134,17 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
         float x[kGroup];
 #pragma unroll
         for (int e = 0; e < kGroup; ++e) x[e] = id < 0 ? 0.0f : __builtin_nanf("");
-        for (int q = 0; q < kLookupGroups; ++q) {
+        for (int q = 0; q < Each; ++q) {
             const int at = col + (q << p.shift) * kGroup;
             if (at < p.dim) store_columns(dst, Columns(at, p.dim), x);
         }
         return;
     }
     const In* src = static_cast<const In*>(p.table) + id * p.tstride;
-    Group<In> raw[kLookupGroups];
+    Group<In> raw[Each];
     const auto load = [&](auto narrow) {
 #pragma unroll
-        for (int q = 0; q < kLookupGroups; ++q) {
+        for (int q = 0; q < Each; ++q) {
             const int at = col + (q << p.shift) * kGroup;
             raw[q] = load_columns<decltype(narrow)::value>(src, Columns(at < p.dim ? at : col, p.dim));
         }
@@ -147,14 +152,16 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
     if (p.dim < kGroup) load(std::true_type{});
     else load(std::false_type{});
 #pragma unroll
-    for (int q = 0; q < kLookupGroups; ++q) {
+    for (int q = 0; q < Each; ++q) {
         const int at = col + (q << p.shift) * kGroup;
         if (at >= p.dim) break;
         float x[kGroup];
         widen_group(raw[q], x);
 #pragma unroll
         for (int e = 0; e < kGroup; ++e) x[e] *= p.scale;
-        store_columns(dst, Columns(at, p.dim), x);
+        const Columns cols(at, p.dim);
+        if (p.once && cols.whole()) store_group<true>(dst + cols.at, x);
+        else store_columns(dst, cols, x);
     }
 }
 
@@ -493,7 +500,7 @@ __device__ __forceinline__ void put_sum(const GradParams& p, uint32_t key, const
         for (int e = 0; e < kGroup; ++e) x[e] += y[e];
     }
     Out* row = static_cast<Out*>(p.table) + key * p.tstride;
-    if (p.once) store_group<true>(row + cols.at, x);       // (whole lines are whole groups)
+    if (p.once && cols.whole()) store_group<true>(row + cols.at, x);
     else store_columns(row, cols, x);
 }
 
@@ -517,13 +524,13 @@ __device__ void fill_rows(const GradParams& p, int64_t unit) {
         Out* row = static_cast<Out*>(p.table) + (v0 + i * kWaves) * p.tstride;
         int col = lane * E;
         if (p.once) {
-            for (; col < p.dim; col += kWave * E)
+            for (; col + E <= p.dim; col += kWave * E)
                 __builtin_nontemporal_store(u32x4{0, 0, 0, 0},
                                             reinterpret_cast<loose_vec*>(row + col));
-            continue;
+        } else {
+            for (; col + E <= p.dim; col += kWave * E)
+                *reinterpret_cast<loose_vec*>(row + col) = u32x4{0, 0, 0, 0};
         }
-        for (; col + E <= p.dim; col += kWave * E)
-            *reinterpret_cast<loose_vec*>(row + col) = u32x4{0, 0, 0, 0};
         for (; col < p.dim; ++col) row[col] = narrow<Out>(0.0f);
     }
 }
@@ -734,6 +741,27 @@ Threads row_threads(int64_t dim, int each) {
     return {shift, static_cast<int32_t>((groups + per - 1) / per)};
 }
 
+// Large results of 16 bits are stored without keeping them in a cache, where they would displace what is
+// read.  (A float32 group is two vectors, each instruction's 32 bytes apart: parts of lines, which only a
+// cache puts together.)  Measured, us kept and not: lookups 16384 x 8192 bf16 72.6 and 59.0, 8192 x 4099
+// fp32 -> bf16 (67 MB) 32.0 and 24.4, 8192 x 1001 fp16 (16 MB) 6.9 and 6.7, 16384 x 4096 bf16 -> fp32 82
+// and 114; gradients of 16384 tokens into 32000 x 4096 bf16 107 and 84.
+constexpr int64_t kOnceStores = int64_t{32} << 20;
+bool stored_once(const fsdpshard_matrix* m) {
+    return element_bytes(m->dtype) == 2 && m->rows * m->cols * 2 >= kOnceStores;
+}
+
+// Whether rows start and end with the caches' lines, or have so many that their cut ones hardly count.
+// Measured on gradients, us kept and not: 16384 tokens into 32000 x 4099 bf16 (rows of 64 lines) 117 and
+// 99, 8192 into 50021 x 1001 fp16 (16 lines) 33 and 40.
+constexpr int kLine = 128, kManyLines = 64;
+bool whole_lines(const fsdpshard_matrix* m) {
+    const int64_t elem = element_bytes(m->dtype);
+    if (m->cols * elem >= kManyLines * kLine) return true;
+    return reinterpret_cast<uintptr_t>(m->data) % kLine == 0 && m->cols * elem % kLine == 0 &&
+           (m->rows <= 1 || m->row_stride * elem % kLine == 0);
+}
+
 template <typename Get>
 const void* by_dtypes(int32_t in, int32_t out, Get get) {
     return by_dtype(in, [&](auto a) { return by_dtype(out, [&](auto b) { return get(a, b); }); });
@@ -813,14 +841,6 @@ const void* grad_form(const GradParams& p) {
                        : KERNEL(embed_grad_kernel<In, Out, true, Add>);
 }
 
-// Whether rows start and end with the caches' lines.
-constexpr int kLine = 128;
-bool whole_lines(const fsdpshard_matrix* m) {
-    const int64_t elem = element_bytes(m->dtype);
-    return reinterpret_cast<uintptr_t>(m->data) % kLine == 0 && m->cols * elem % kLine == 0 &&
-           (m->rows <= 1 || m->row_stride * elem % kLine == 0);
-}
-
 int sort_ranges(SortParams& s, void* stream) {
     s.range = static_cast<int32_t>(range_rows(s.vocab));
     s.bits = 0;
@@ -868,9 +888,11 @@ extern "C" int embedding_lookup(const fsdpshard_matrix* table, const int64_t* id
     const Span read[] = {{table->data, tbytes}, {ids, 8 * out->rows}};
     if (!disjoint(written, 1, read, 2)) return FSDPSHARD_ERR_INVALID_ARG;
     if (out->rows == 0) return FSDPSHARD_OK;
-    const Threads th = row_threads(out->cols, kLookupGroups);
+    const Threads th = row_threads(
+        out->cols, out->dtype == FSDPSHARD_FP32 ? kLookupGroups<float> : kLookupGroups<Bf16>);
     LookupParams p{table->data, table->rows, table->row_stride, ids, out->data, out->rows,
-                   out->row_stride, static_cast<int32_t>(out->cols), th.splits, th.shift, scale, 0};
+                   out->row_stride, static_cast<int32_t>(out->cols), th.splits, th.shift, stored_once(out),
+                   scale, 0};
     const void* kernel = by_dtypes(table->dtype, out->dtype, [](auto a, auto b) {
         return KERNEL(lookup_kernel<decltype(a), decltype(b)>);
     });
@@ -939,7 +961,7 @@ extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
     p.shift = th.shift;
     p.scale = scale;
     p.accumulate = accumulate;
-    p.once = !accumulate && whole_lines(dtable);
+    p.once = !accumulate && stored_once(dtable) && whole_lines(dtable);
     const int64_t per = kBlock >> th.shift;
     p.sum_units = (l.chunks + per - 1) / per * th.splits;
     const int64_t fill = accumulate ? 0 : (vocab + kFillRows - 1) / kFillRows;
