@@ -14,8 +14,8 @@ from oracle import policy as OP
 
 pytestmark = pytest.mark.gpu
 
-# around a lane's four tokens, a wave's 256, the one work-group's 4,096, and beyond it
-SIZES = [1, 2, 3, 4, 5, 63, 255, 256, 257, 1023, 4095, 4096, 4097, 16385, 70001]
+# around a lane's four tokens, a wave's 256, the one work-group's 2,560, and beyond it
+SIZES = [1, 2, 3, 4, 5, 63, 255, 256, 257, 1023, 2559, 2560, 2561, 16385, 70001]
 FULL = OP.constants(0.2, 0.28, 1.4, 0.1, 0.02)
 
 
@@ -40,9 +40,9 @@ def test_policy_of_tokens(n):
 
 
 @pytest.mark.parametrize("n,sequences,behind", [(1, 1, 0), (5, 2, 1), (300, 9, 7), (300, 300, 0),
-                                                (3, 2, 0), (4096, 64, 1), (4096, 65, 0), (4097, 64, 0),
+                                                (3, 2, 0), (2560, 16, 1), (2560, 17, 0), (2561, 16, 0),
                                                 (4099, 1, 0), (16384, 70, 300), (16385, 70, 0),
-                                                (2000, 600, 3), (70001, 33, 5000),
+                                                (2000, 600, 3), (70001, 130, 5000),
                                                 (70001, 5000, 1)])
 def test_policy_of_sequences(n, sequences, behind):
     rng = _seed(n, sequences, behind)
@@ -211,13 +211,13 @@ def test_policy_offsets_past_the_tokens():
     """The nearest valid value counts, so nothing outside the arrays is touched."""
     x = P.rollout(_seed(12), 1000)
     want = P.run_policy(FULL, x, [0, 400, 1000, 1000])
-    got = P.run_policy(FULL, x, [-5, 400, 1 << 50, (1 << 50) + 1])
+    got = P.run_policy(FULL, x, [-(1 << 63), 400, 1 << 50, (1 << 63) - 1])
     for name in want:
         assert np.array_equal(got[name], want[name]), name
 
 
 @pytest.mark.parametrize("n,pairs,behind", [(2, 1, 0), (7, 1, 2), (300, 4, 9), (300, 200, 0),
-                                            (3, 1, 0), (4096, 32, 1), (4096, 33, 0), (4097, 32, 0),
+                                            (3, 1, 0), (2560, 8, 1), (2560, 9, 0), (2561, 8, 0),
                                             (5000, 3, 0), (16384, 256, 1), (16384, 257, 0),
                                             (16385, 5, 100), (70001, 37, 0), (90000, 2, 80000)])
 def test_preference(n, pairs, behind):
