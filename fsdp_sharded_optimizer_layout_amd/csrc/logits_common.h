@@ -1,5 +1,6 @@
-// Private header of libfsdpshard.so: pieces shared by the operators over logits
-// (token_logprobs.hip, distill.hip).  Not installed; the C ABI is include/fsdpshard_logits.h.
+// Private header of libfsdpshard.so: pieces shared by the operators over logits (token_logprobs.hip,
+// distill.hip, policy_logits.hip) and, of vectors and host checks, by embedding.hip and policy.hip.  Not
+// installed; the C ABI is include/fsdpshard_logits.h.
 //
 // Mathematics.  For a row x with maximum m and c = scale: d_i = c (x_i - m), s = sum exp d_i,
 // L = log s, log p_i = d_i - L.  The maximum's own term is exactly 1, so s = 1 + r and

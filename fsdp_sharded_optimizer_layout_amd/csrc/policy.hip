@@ -1,5 +1,11 @@
 // Losses of post-training over log probabilities of packed tokens, of libfsdpshard.so on gfx950: the
 // clipped policy loss with a KL term, and the loss over pairs of sequences, with their gradients.
+//
+// Bound by launches and the latency of a few dependent loads in each: a million tokens are 36 MB, 5.5 us
+// at the rate of a copy.  Measured, us: a policy loss of 1000003 tokens 11.7 with a ratio for each token
+// and 21 in 1024 sequences (sums 9, ratios 3, outputs 11, totals 4 in a trace), a preference loss of 512
+// pairs of 2000003 tokens 17.4 (10, 4, 6); sequences of ten tokens, of which a chunk goes through 25 one
+// after the other, take 115.
 
 #include "policy_common.h"
 
