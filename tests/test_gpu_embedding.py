@@ -239,3 +239,23 @@ def test_table_beyond_2_31_elements():
     assert float(table[vocab - 1].float().mean()) == 6.0
     assert float(table[vocab - 2].float().mean()) == 2.0
     assert float(table[:vocab - 2].float().abs().max()) == 0.0
+
+
+def test_tokens_beyond_2_31_elements():
+    """Offsets of the tokens' rows pass 32 bits, written and read."""
+    tokens, dim = 140000, 16384                          # 2.29e9 elements, 4.6 GB
+    table = torch.arange(4, device="cuda", dtype=torch.bfloat16)[:, None].expand(4, dim).contiguous()
+    ids = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+    ids[-2:] = torch.tensor([3, -1]).cuda()
+    ids[-70000] = 2
+    out = torch.full((tokens, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    say("lookup of 2.29e9 elements")
+    F.embedding_lookup(table, ids, out)
+    assert float(out[-2].float().min()) == 3.0 and float(out[-1].float().abs().max()) == 0.0
+    assert float(out[-70000].float().min()) == 2.0
+    assert float(out.sum(dtype=torch.float64)) == (3.0 + 2.0) * dim
+    ids[ids == 0] = -1
+    say("grad of 2.29e9 elements")
+    got = torch.empty(4, dim, device="cuda")
+    F.embedding_grad(ids, out, got)
+    assert [float(x) for x in got.sum(1)] == [0.0, 0.0, 2.0 * dim, 3.0 * dim]

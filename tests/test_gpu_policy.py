@@ -298,3 +298,35 @@ def test_repeated_calls_give_the_same_bits():
     a, b = P.run_preference(x, offsets, g), P.run_preference(x, offsets, g)
     for name in a:
         assert np.array_equal(a[name].view(np.uint8), b[name].view(np.uint8)), name
+
+
+def test_beyond_2_31_tokens():
+    """Places, chunks and counts pass 32 bits; all weight is on the last few tokens."""
+    n, last = (1 << 31) + 1001, 300
+    f = dict(dtype=torch.float32, device="cuda")
+    lp, w, d = (torch.zeros(n, **f) for _ in range(3))
+    lp[-last:] = -0.25
+    w[-last:] = 0.5
+    A = torch.ones(n, **f)
+    old = torch.zeros(n, **f)                            # ratio e^-0.25 at the end
+    totals, counts = torch.empty(4, **f), torch.empty(2, dtype=torch.int64, device="cuda")
+    r = np.exp(np.float64(-0.25))
+    for offsets in (None, torch.tensor([0, 7, n - 100, n]).cuda()):
+        d.fill_(3)
+        say(f"policy of {n} tokens, sequences: {offsets is not None}")
+        F.policy_loss(lp, A, w, d, totals=totals, counts=counts, old_logprob=old, offsets=offsets)
+        assert counts.tolist() == [last, 0]
+        assert abs(float(totals[0]) + 0.5 * last * r) <= 1e-5 * last
+        assert torch.allclose(d[-last:], torch.full((last,), float(-0.5 * r), **f), rtol=1e-6)
+        assert float(d[:-last].abs().max()) == 0.0
+    say(f"preference of {n} tokens")
+    loss, won = torch.empty(1, **f), torch.empty(1, 2, **f)
+    F.preference_loss(lp, torch.tensor([0, n - 100, n]).cuda(), loss, rewards=won, weight=w,
+                      dloss=torch.ones(1, **f), dlogprob=d, beta=1.0)
+    assert won.tolist() == [[-0.125 * 200, -0.125 * 100]]     # exact sums
+    h = -12.5
+    assert abs(float(loss) - np.log1p(np.exp(-h))) <= 1e-6 * abs(h)
+    slope = -1 / (1 + np.exp(h))
+    assert torch.allclose(d[-300:-100], torch.full((200,), float(0.5 * slope), **f), rtol=1e-6)
+    assert torch.allclose(d[-100:], torch.full((100,), float(-0.5 * slope), **f), rtol=1e-6)
+    assert float(d[:-300].abs().max()) == 0.0
