@@ -177,7 +177,9 @@ __global__ __launch_bounds__(kBlock) void lookup_kernel(LookupParams p) {
 // reading's latency and the comparisons: 9 us for 16384 tokens of 32000 rows, 21 for 65536, where two
 // passes by digits, each of three launches, take 36 and 45.
 
-constexpr int kRangeThreads = 1024, kRangeWaves = kRangeThreads / kWave;
+// Up to this many tokens, work-groups of 512 threads, whose barriers and counts cost less; more take 1024.
+// Measured on gradients, us with 512 and 1024: 1021 tokens 20.8 and 22.6, 4096 21.0 and 23.2, 16384 alike.
+constexpr int64_t kFewTokens = 16384;
 constexpr int kMaxRange = 512;              // rows of a range; their counts, one a wave, fit the LDS
 constexpr int kRangeList = 1024;            // tokens of a range that a wave keeps in the LDS
 constexpr int kRangeAhead = 16;             // tokens a lane loads at once
@@ -237,19 +239,21 @@ __device__ __forceinline__ unsigned long long lanes_with(uint32_t d, int bits,
     return among;
 }
 
-__global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p) {
-    extern __shared__ uint32_t place[];     // [kRangeWaves][range], then the lists
-    __shared__ uint32_t sh[kRangeWaves];
+template <int Threads>
+__global__ __launch_bounds__(Threads) void sort_range_kernel(SortParams p) {
+    constexpr int W = Threads / kWave;
+    extern __shared__ uint32_t place[];     // [W][range], then the lists
+    __shared__ uint32_t sh[W];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int64_t low = (p.unit0 + blockIdx.x) * p.range;
     const int rows = static_cast<int>(p.vocab - low < p.range ? p.vocab - low : p.range);
     uint32_t* mine = place + wave * p.range;
-    uint32_t* list = place + kRangeWaves * p.range + wave * kRangeList;
-    for (int i = tid; i < kRangeWaves * p.range; i += kRangeThreads) place[i] = 0;
+    uint32_t* list = place + W * p.range + wave * kRangeList;
+    for (int i = tid; i < W * p.range; i += Threads) place[i] = 0;
     if (tid == 0 && blockIdx.x == 0) *p.long_runs = 0;
     __syncthreads();
     // A wave's tokens are consecutive.
-    const int64_t each = (p.tokens + kRangeThreads - 1) / kRangeThreads * kWave;
+    const int64_t each = (p.tokens + Threads - 1) / Threads * kWave;
     const int64_t begin = wave * each, end = begin + each < p.tokens ? begin + each : p.tokens;
     // f(row of the range, whether the lane's token is in it, the token counted from `begin`)
     const auto stream = [&](auto f) {
@@ -295,22 +299,22 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p)
         });
     }
     uint32_t start;
-    block_scan<kRangeWaves>(lane == 0 ? lower : 0, sh, start);
+    block_scan<W>(lane == 0 ? lower : 0, sh, start);
     // Where each wave's first token of each row goes.
-    const int per = (p.range + kRangeThreads - 1) / kRangeThreads;
+    const int per = (p.range + Threads - 1) / Threads;
     uint32_t sum = 0;
     for (int r = tid * per; r < (tid + 1) * per && r < rows; ++r) {
         uint32_t n = 0;
 #pragma unroll
-        for (int w = 0; w < kRangeWaves; ++w) n += place[w * p.range + r];
+        for (int w = 0; w < W; ++w) n += place[w * p.range + r];
         p.seen[low + r] = n != 0;
         sum += n;
     }
     uint32_t own;
-    uint32_t at = start + block_scan<kRangeWaves>(sum, sh, own);
+    uint32_t at = start + block_scan<W>(sum, sh, own);
     for (int r = tid * per; r < (tid + 1) * per && r < rows; ++r) {
 #pragma unroll
-        for (int w = 0; w < kRangeWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             const uint32_t n = place[w * p.range + r];
             place[w * p.range + r] = at;
             at += n;
@@ -318,7 +322,7 @@ __global__ __launch_bounds__(kRangeThreads) void sort_range_kernel(SortParams p)
     }
     __syncthreads();
     if (low + rows == p.vocab)              // the last range: tokens without a row
-        for (int64_t i = start + own + tid; i < p.tokens; i += kRangeThreads)
+        for (int64_t i = start + own + tid; i < p.tokens; i += Threads)
             p.keys[i] = static_cast<uint32_t>(p.vocab);
     const auto put = [&](uint32_t row, bool here, uint32_t i) {
         const unsigned long long some = __ballot(here);
@@ -786,7 +790,9 @@ struct GradLayout {
 // 406 and 190 (a frequent token's wave goes through all its tokens again).
 constexpr int64_t kRanges = 128;
 constexpr int64_t kOneLaunchReads = int64_t{1} << 24;
-static_assert(kOneLaunchReads / kRanges / kRangeWaves < 1 << 16, "a wave's tokens take 16 bits");
+static_assert(kOneLaunchReads / kRanges / (1024 / kWave) < 1 << 16 &&
+                  kFewTokens / (512 / kWave) < 1 << 16,
+              "a wave's tokens take 16 bits");
 
 int64_t range_rows(int64_t vocab) {
     const int64_t even = (vocab + kRanges - 1) / kRanges;
@@ -848,8 +854,11 @@ int sort_ranges(SortParams& s, void* stream) {
     s.range = static_cast<int32_t>(range_rows(s.vocab));
     s.bits = 0;
     while ((1 << s.bits) < s.range) ++s.bits;
-    return launch_units(KERNEL(sort_range_kernel), (s.vocab + s.range - 1) / s.range, s,
-                        int64_t{4} * kRangeWaves * (s.range + kRangeList), stream, kRangeThreads);
+    const bool few = s.tokens <= kFewTokens;
+    const int threads = few ? 512 : 1024;
+    return launch_units(few ? KERNEL(sort_range_kernel<512>) : KERNEL(sort_range_kernel<1024>),
+                        (s.vocab + s.range - 1) / s.range, s,
+                        int64_t{4} * (threads / kWave) * (s.range + kRangeList), stream, threads);
 }
 
 int sort_digits(SortParams& s, const GradLayout& l, char* ws, void* stream) {

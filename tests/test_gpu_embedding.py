@@ -121,10 +121,11 @@ def test_grad(shape, dtype, out):
 
 
 # Around a chunk of 32 tokens, chunks of more than 32 tokens (65,537 and up), tokens sorted in one
-# launch (up to 131,072, or fewer for a large vocabulary) and by digits, around a sorting work-group's
+# launch by smaller and larger work-groups (up to 16,384 and 131,072 tokens, or fewer for a large
+# vocabulary) and by digits, around a sorting work-group's
 # 4096, the largest digits, rows narrower and wider than a wave.
 @pytest.mark.parametrize("tokens,vocab,dim", [(31, 9, 16), (32, 9, 16), (33, 9, 16), (4097, 300, 8),
-                                              (20000, 32000, 24), (65537, 1000, 8), (20001, 700, 520),
+                                              (16384, 32000, 24), (16385, 32000, 24), (65537, 1000, 8), (20001, 700, 520),
                                               (131072, 32000, 8), (131073, 300, 8),
                                               (135168, 131072, 8), (135169, 70000, 8),
                                               (3000, 1 << 21, 8), (4097, 1 << 21, 8)])
