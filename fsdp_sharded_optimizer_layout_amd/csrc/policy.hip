@@ -215,22 +215,10 @@ struct PolicyParams {
     int64_t part_count, unit0;
 };
 
-// A quad of tokens of every array (those of arrays that are not there hold nothing).
+// A quad of tokens of every array (those of arrays that are not there, or not loaded, hold nothing).
 struct TokenQuad {
     loose_quad w, a, lp, old, ref, h;
 
-    __device__ __forceinline__ void load(const PolicyParams& p, const QuadPlace& q) {
-        const int64_t n = p.seq.tokens;
-        load_ratio(p, q);
-        if (p.ref) ref = load_quad(p.ref, q, n);
-        if (p.entropy) h = load_quad(p.entropy, q, n);
-    }
-    __device__ __forceinline__ void turn(const PolicyParams& p, const QuadPlace& q) {
-        turn_ratio(p, q);
-        if (q.turn == 0) return;
-        if (p.ref) turn_quad(ref, q);
-        if (p.entropy) turn_quad(h, q);
-    }
     // What the ratio and its slope are made of.
     __device__ __forceinline__ void load_ratio(const PolicyParams& p, const QuadPlace& q) {
         const int64_t n = p.seq.tokens;
@@ -245,6 +233,33 @@ struct TokenQuad {
         turn_quad(a, q);
         turn_quad(lp, q);
         if (p.old_logprob) turn_quad(old, q);
+    }
+    // Everything, but for what a shared ratio has already been made of.
+    template <bool Seq>
+    __device__ __forceinline__ void load(const PolicyParams& p, const QuadPlace& q) {
+        const int64_t n = p.seq.tokens;
+        if constexpr (!Seq) {
+            load_ratio(p, q);
+        } else {
+            w = load_quad(p.weight, q, n);
+            a = load_quad(p.advantage, q, n);
+            if (p.ref) lp = load_quad(p.logprob, q, n);
+        }
+        if (p.ref) ref = load_quad(p.ref, q, n);
+        if (p.entropy) h = load_quad(p.entropy, q, n);
+    }
+    template <bool Seq>
+    __device__ __forceinline__ void turn(const PolicyParams& p, const QuadPlace& q) {
+        if (q.turn == 0) return;
+        if constexpr (!Seq) {
+            turn_ratio(p, q);
+        } else {
+            turn_quad(w, q);
+            turn_quad(a, q);
+            if (p.ref) turn_quad(lp, q);
+        }
+        if (p.ref) turn_quad(ref, q);
+        if (p.entropy) turn_quad(h, q);
     }
     __device__ __forceinline__ double log_ratio(const PolicyParams& p, int e) const {
         return p.old_logprob ? static_cast<double>(lp[e]) - static_cast<double>(old[e]) : 0.0;
@@ -261,8 +276,8 @@ __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x,
         t.n += 1;
         t.a += x.log_ratio(p, e);
         const double flow = static_cast<double>(x.w[e]) * static_cast<double>(x.a[e]);
-        if (x.a[e] < 0.0f) t.c += flow;
-        else t.b += flow;
+        if (!(x.a[e] < 0.0f)) t.b += flow;           // (a NaN goes to both)
+        if (!(x.a[e] > 0.0f)) t.c += flow;
     }
     return t;
 }
@@ -351,7 +366,7 @@ __device__ void policy_put(const PolicyParams& p, int64_t wave, int64_t waves, T
         const Window w(p.seq, window_behind(p.seq, c.begin), fetch);
         __builtin_amdgcn_sched_barrier(0);
         TokenQuad x;
-        x.load(p, q);
+        x.load<true>(p, q);
         Ratio ratio[kQuad];
         unsigned mask = 0;
         for_sequences(p.seq, w, c.begin, c.n, fetch, [&](int64_t, int l, int lo, int hi) {
@@ -362,7 +377,7 @@ __device__ void policy_put(const PolicyParams& p, int64_t wave, int64_t waves, T
             for (int e = 0; e < kQuad; ++e)
                 if (here >> e & 1) ratio[e] = of;
         });
-        x.turn(p, q);
+        x.turn<true>(p, q);
         put_tokens<true>(p, x, c.begin + c.mine, mask, ratio, sum);
     }
 }
@@ -410,8 +425,8 @@ __device__ void policy_tokens(const PolicyParams& p, int64_t first, int64_t step
     for (int64_t i = first * kQuad; i < p.seq.tokens; i += step * kQuad) {
         const QuadPlace q(i, p.seq.tokens);
         TokenQuad x;
-        x.load(p, q);
-        x.turn(p, q);
+        x.load<false>(p, q);
+        x.turn<false>(p, q);
         const int64_t left = p.seq.tokens - i;
         put_tokens<false>(p, x, i, left >= kQuad ? 0xFu : (1u << left) - 1, nullptr, sum);
     }
@@ -441,8 +456,7 @@ __global__ __launch_bounds__(kOneGroup) void policy_small_kernel(PolicyParams p)
 
 __global__ __launch_bounds__(kBlock) void policy_tokens_kernel(PolicyParams p) {
     Totals t{};
-    policy_tokens(p, blockIdx.x * int64_t{kBlock} + threadIdx.x,
-                          gridDim.x * int64_t{kBlock}, t);
+    policy_tokens(p, blockIdx.x * int64_t{kBlock} + threadIdx.x, gridDim.x * int64_t{kBlock}, t);
     put_part(p, t, blockIdx.x);
 }
 

@@ -146,6 +146,21 @@ def test_policy_bad_values_of_counted_tokens_stay_with_them():
     assert np.isnan(got["totals"][0]) and got["counts"][0] == 20000
 
 
+def test_policy_bad_advantage_reaches_its_whole_sequence():
+    """A sequence's slope is the sum over its tokens, so one NaN makes it NaN, and no other's."""
+    n, offsets = 3000, np.array([0, 700, 1500, 3000])
+    x = P.rollout(_seed(61), n, offsets, ignored=0.0, spread=0.01)
+    c = OP.constants()
+    clean = P.run_policy(c, x, offsets)
+    x["A"][900] = np.nan
+    got = P.run_policy(c, x, offsets)
+    assert np.isnan(got["dlogprob"][700:1500]).all() and np.isnan(got["loss"][900])
+    for a, b in ((0, 700), (1500, 3000)):
+        assert np.array_equal(got["dlogprob"][a:b], clean["dlogprob"][a:b])
+    keep = np.arange(n) != 900
+    assert np.array_equal(got["loss"][keep], clean["loss"][keep])
+
+
 def test_policy_far_ratios():
     lp = np.array([-60.0, 0.0, -1e-3, -80.0, -1.0, -30.0], np.float32)
     old = np.array([0.0, -60.0, -1e-3, 0.0, -1.0 + 1e-6, -70.0], np.float32)
