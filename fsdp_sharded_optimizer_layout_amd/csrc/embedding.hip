@@ -805,7 +805,9 @@ bool in_one_launch(int64_t tokens, int64_t vocab) {
 }
 
 // Tokens of a chunk: as many as give kFewChunks of them, but at least kAhead and at most kChunk, unless
-// that makes more than kMostChunks, whose parts take workspace.
+// that makes more than kMostChunks, whose parts take workspace.  Measured with chunks of 8, 16, 32 and 64:
+// 16384 tokens into 32000 x 4096 bf16 95, 86, 85 and 85 us, 65536 added to 32000 x 8192 fp32 613, 554, 535
+// and 534.
 constexpr int64_t kChunk = 32, kFewChunks = 512, kMostChunks = 2048;
 
 int64_t chunk_of(int64_t tokens) {

@@ -547,13 +547,13 @@ __device__ __forceinline__ Sum add_up(const ScoreQuad& x, unsigned mask) {
 }
 
 // A pair's loss, rewards, and what a token of weight 1 gets of the gradient.
-struct Verdict {
+struct PairResult {
     float loss, reward[2], slope[2];
 };
 
-__device__ __forceinline__ Verdict solve_pair(const PreferenceParams& p, int64_t pair,
+__device__ __forceinline__ PairResult solve_pair(const PreferenceParams& p, int64_t pair,
                                               const Sum& c, const Sum& r) {
-    Verdict v{};
+    PairResult v{};
     if (c.n == 0 || r.n == 0) return v;
     const double cs = p.normalised ? c.a / c.b : c.a, rs = p.normalised ? r.a / r.b : r.a;
     const double lead = cs - rs, h = p.beta * lead - p.margin;
@@ -604,7 +604,7 @@ __device__ void preference_solve(const PreferenceParams& p, int64_t wave, int64_
     for (int64_t pair = wave; pair < p.pairs; pair += waves) {
         const Sum c = sum_of<false>(p.seq, p.sums, 2 * pair);
         const Sum r = sum_of<false>(p.seq, p.sums, 2 * pair + 1);
-        const Verdict v = solve_pair(p, pair, c, r);
+        const PairResult v = solve_pair(p, pair, c, r);
         if (threadIdx.x % kWave != 0) continue;
         p.loss[pair] = v.loss;
         if (p.rewards) {

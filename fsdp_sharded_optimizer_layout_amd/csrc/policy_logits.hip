@@ -366,6 +366,9 @@ struct WholeKernel {
     int threads;
 };
 
+// The kernel that holds a row in registers, or null where a row is too long: 16 vectors of each of 512
+// threads.  Few rows take the largest work-group, for latency: 256 x 32000 bf16 12.0 us, 257 rows, with 256
+// threads each, 16.9.
 WholeKernel whole_kernel(const fsdpshard_logits* x, bool entropy, bool once) {
     const int64_t per = 16 / element_bytes(x->dtype);
     const bool in_phase = aligned16(x->data) && (x->rows <= 1 || x->row_stride % per == 0);
