@@ -130,25 +130,37 @@ __device__ __forceinline__ void for_sequences(const Sequences& q, Window w, int6
     }
 }
 
-// What is added up over a sequence.
+// What is added up over a sequence: sums, how many tokens count, and which of kKinds there are among them
+// (of the policy loss).
 struct Sum {
     double a, b, c;
-    int64_t n;
+    int64_t n : 56;
+    uint64_t kinds : 8;
 };
 
+// Advantages above 0, below it, and others, which no limit clips.
+enum Kind : unsigned { kRises = 1, kFalls = 2, kLevel = 4, kKinds = 7 };
+
 // The wave's sum, in every lane.  (A count below 2^53 is exact as a float64.)
-template <bool Three>
+template <bool Policy>
 __device__ __forceinline__ Sum wave_total(const Sum& t) {
-    return {wave_sum(t.a), wave_sum(t.b), Three ? wave_sum(t.c) : 0.0,
-            static_cast<int64_t>(wave_sum(static_cast<double>(t.n)))};
+    Sum all{wave_sum(t.a), wave_sum(t.b), 0.0,
+            static_cast<int64_t>(wave_sum(static_cast<double>(t.n))), 0};
+    if constexpr (Policy) {
+        all.c = wave_sum(t.c);
+#pragma unroll
+        for (unsigned k = 1; k <= kKinds; k *= 2)
+            if (__any(t.kinds & k)) all.kinds |= k;
+    }
+    return all;
 }
 
 // The sum of sequence s over its chunks, in every lane.
-template <bool Three>
+template <bool Policy>
 __device__ __forceinline__ Sum sum_of(const Sequences& q, const Sum* parts, int64_t s) {
     const int64_t lo = clamp_to(q.offsets[s], 0, q.tokens);
     const int64_t hi = clamp_to(q.offsets[s + 1], 0, q.tokens);
-    Sum t{0.0, 0.0, 0.0, 0};
+    Sum t{};
     if (lo < hi) {
         const int64_t last = (hi - 1) / kChunk;
 #pragma unroll 4
@@ -156,11 +168,14 @@ __device__ __forceinline__ Sum sum_of(const Sequences& q, const Sum* parts, int6
             const Sum x = parts[c + s];
             t.a += x.a;
             t.b += x.b;
-            if (Three) t.c += x.c;
+            if (Policy) {
+                t.c += x.c;
+                t.kinds |= x.kinds;
+            }
             t.n += x.n;
         }
     }
-    return wave_total<Three>(t);
+    return wave_total<Policy>(t);
 }
 
 // A chunk's tokens and a lane's place among them.
@@ -266,10 +281,10 @@ struct TokenQuad {
     }
 };
 
-// Counted tokens of a quad's places in `mask`, their log ratios, and the weights of those that a
-// gradient flows through where the ratio is not above, and not below, its limits.
+// Counted tokens of a quad's places in `mask`, their kinds, their log ratios, and the weights of those
+// that a gradient flows through where the ratio is not above, and not below, its limits.
 __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x, unsigned mask) {
-    Sum t{0.0, 0.0, 0.0, 0};
+    Sum t{};
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
         if (!(mask >> e & 1) || x.w[e] == 0.0f) continue;
@@ -278,6 +293,7 @@ __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x,
         const double flow = static_cast<double>(x.w[e]) * static_cast<double>(x.a[e]);
         if (!(x.a[e] < 0.0f)) t.b += flow;           // (a NaN goes to both)
         if (!(x.a[e] > 0.0f)) t.c += flow;
+        t.kinds |= x.a[e] > 0.0f ? kRises : x.a[e] < 0.0f ? kFalls : kLevel;
     }
     return t;
 }
@@ -285,10 +301,13 @@ __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x,
 __device__ __forceinline__ Ratio solve_policy(const PolicyTerms& terms, const Sum& t) {
     if (t.n == 0) return {0.0, 1.0f, 0.0f};          // no token takes it
     const double share = 1.0 / static_cast<double>(t.n), d = t.a * share;
+    const bool up = !(d > terms.log_high), down = !(d < terms.log_low || d > terms.log_dual);
     double flow = 0.0;
-    if (!(d > terms.log_high)) flow += t.b;
-    if (!(d < terms.log_low || d > terms.log_dual)) flow += t.c;
+    if (up) flow += t.b;
+    if (down) flow += t.c;
     const float r = exp_of(d);
+    // Without a token that is not clipped there is no slope, also where r is inf.
+    if ((t.kinds & (kLevel | (up ? kRises : 0u) | (down ? kFalls : 0u))) == 0) return {d, r, 0.0f};
     return {d, r, static_cast<float>(-static_cast<double>(r) * flow * share)};
 }
 
@@ -533,7 +552,7 @@ struct ScoreQuad {
 
 // The places' weighted gaps (a), weights (b), and how many count.
 __device__ __forceinline__ Sum add_up(const ScoreQuad& x, unsigned mask) {
-    Sum t{0.0, 0.0, 0.0, 0};
+    Sum t{};
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
         const float w = x.w[e];

@@ -22,8 +22,9 @@
  *     dloss/dlp = w (-r A [f is not clipped] - kl_coef (exp(e) - 1)),  dloss/dH = -entropy_coef w
  * f counts as clipped where A > 0 and lp - old > log(1 + clip_high), where A < 0 and lp - old <
  * log(1 - clip_low), and where A < 0, dual_clip > 0 and lp - old > log(dual_clip), compared in
- * float64.  With one ratio for each sequence, lp - old is its mean over the sequence's counted
- * tokens: the tokens share r, and each takes 1 / count of the slope of all of them.
+ * float64; a clipped f has no slope, also where r is inf.  With one ratio for each sequence, lp - old
+ * is its mean over the sequence's counted tokens: the tokens share r, and each takes 1 / count of the
+ * slope of all of them.
  * A token whose weight is 0 is not counted: its loss and gradients are 0, whatever its other
  * values are.  Infinities and NaN of counted tokens go through these formulas as they are.
  */

@@ -64,13 +64,16 @@ def policy(c, lp, A, w, old=None, ref=None, H=None, offsets=None):
                        None if ref is None else float(ref[t]), None if H is None else float(H[t]))
             for name in ("loss", "f", "k", "less1", "r", "cut"):
                 out[name][t] = x[name]
-            flows.append(0.0 if x["cut"] else float(w[t]) * float(A[t]))
+            if not x["cut"]:
+                flows.append(float(w[t]) * float(A[t]))
             out["dlogprob"][t] = -float(w[t]) * c["kl_coef"] * x["less1"]
             out["dentropy"][t] = -c["entropy_coef"] * float(w[t])
             totals += [x["loss"], -float(w[t]) * x["f"], float(w[t]) * x["k"],
                        0.0 if H is None else float(w[t]) * float(H[t])]
             counts += [1, int(x["cut"])]
         r = math.exp(d) if d < 700 else math.inf
+        if not flows:                           # 0, also where r is inf
+            continue
         for t in group:
             out["dlogprob"][t] -= r * math.fsum(flows) / len(group)
     out["totals"], out["counts"] = totals, counts

@@ -1,0 +1,81 @@
+"""Policy and preference losses where values leave float32's range: ratios far above and below their
+limits, log probabilities of -inf, advantages that are NaN beyond every limit.  What is finite is
+compared with the float64 oracle within policy_cases' bounds; infinities and NaN have to be where the
+definitions put them."""
+
+import numpy as np
+import pytest
+import torch
+
+import fsdp_sharded_optimizer_layout_amd as F
+import policy_cases as P
+from gpu_helpers import say
+from oracle import policy as OP
+
+pytestmark = pytest.mark.gpu
+INF = np.float32(np.inf)
+
+# One work-group, and three launches with several chunks a sequence.
+SIZES = [(12, [0, 3, 4, 9, 12]), (5000, [0, 700, 701, 2500, 5000])]
+
+
+def _rng(*key):
+    return np.random.default_rng([int(v) for v in key] + [37])
+
+
+def _clipped_everywhere(n, offsets, gaps, advantage):
+    """Sequence s has the mean log ratio gaps[s] (about), and advantages of the sign advantage[s]."""
+    rng = _rng(n)
+    x = P.rollout(rng, n, None, ignored=0.2, entropy=False)
+    old = x["lp"].copy()
+    A = x["A"].copy()
+    for a, b, gap, sign in zip(offsets, offsets[1:], gaps, advantage):
+        old[a:b] = (x["lp"][a:b] - np.float32(gap)).astype(np.float32)
+        A[a:b] = sign * np.abs(A[a:b])
+        x["w"][a] = 0.5
+    return dict(x, old=old, A=A)
+
+
+@pytest.mark.parametrize("n,offsets", SIZES)
+@pytest.mark.parametrize("kl", [0.0, 0.1])
+def test_a_sequence_clipped_at_an_infinite_ratio_has_no_slope(n, offsets, kl):
+    """exp of the mean log ratio is inf in float32; every token is clipped, so that what is left of
+    the slope is the KL term's."""
+    c = OP.constants(0.2, 0.2, 3.0, kl)
+    x = _clipped_everywhere(n, offsets, [100.0, 95.0, 1000.0, 0.01], [1, -1, 1, -1])
+    say(f"clipped sequences of {n} tokens, kl={kl}")
+    got = P.run_policy(c, x, offsets)
+    P.check_policy(c, x, offsets, got, "clipped")
+    assert np.isfinite(got["dlogprob"]).all() and np.isfinite(got["loss"]).all()
+    if kl == 0:
+        assert (got["dlogprob"][:offsets[3]] == 0).all()
+    # one token that the old policy gave no chance
+    x["old"][offsets[2]] = -INF
+    got = P.run_policy(c, x, offsets)
+    P.check_policy(c, x, offsets, got, "old -inf")
+    assert np.isfinite(got["dlogprob"]).all()
+
+
+@pytest.mark.parametrize("n,offsets", SIZES)
+def test_a_sequence_of_both_signs_clipped_at_an_infinite_ratio(n, offsets):
+    c = OP.constants(0.2, 0.2, 3.0)
+    x = _clipped_everywhere(n, offsets, [100.0, 95.0, 1000.0, 0.01], [1, 1, 1, 1])
+    x["A"] = (x["A"] * np.where(np.arange(n) % 2, -1, 1)).astype(np.float32)
+    got = P.run_policy(c, x, offsets)
+    P.check_policy(c, x, offsets, got, "both signs")
+    assert (got["dlogprob"][:offsets[3]] == 0).all()
+
+
+@pytest.mark.parametrize("n,offsets", SIZES)
+def test_what_an_infinite_ratio_does_not_clip_goes_on(n, offsets):
+    """Without a dual limit a negative advantage is not clipped above, so its slope is infinite;
+    positive ones of another sequence are clipped."""
+    c = OP.constants()
+    x = _clipped_everywhere(n, offsets, [100.0, 0.01, 1000.0, 0.02], [-1, 1, 1, -1])
+    got = P.run_policy(c, x, offsets)
+    counted = x["w"] != 0
+    a, b = offsets[0], offsets[1]
+    assert (got["dlogprob"][a:b] == np.where(counted[a:b], INF, 0)).all()
+    assert (got["loss"][a:b] == np.where(counted[a:b], INF, 0)).all()
+    assert (got["dlogprob"][offsets[2]:offsets[3]] == 0).all()
+    assert np.isfinite(got["dlogprob"][b:]).all()
