@@ -138,8 +138,9 @@ struct Sum {
     uint64_t kinds : 8;
 };
 
-// Advantages above 0, below it, and others, which no limit clips.
-enum Kind : unsigned { kRises = 1, kFalls = 2, kLevel = 4, kKinds = 7 };
+// Advantages above 0, below it, and others, which no limit clips: 0, and NaN (or what becomes NaN with the
+// token's weight).
+enum Kind : unsigned { kRises = 1, kFalls = 2, kLevel = 4, kBad = 8, kKinds = 15 };
 
 // The wave's sum, in every lane.  (A count below 2^53 is exact as a float64.)
 template <bool Policy>
@@ -281,8 +282,8 @@ struct TokenQuad {
     }
 };
 
-// Counted tokens of a quad's places in `mask`, their kinds, their log ratios, and the weights of those
-// that a gradient flows through where the ratio is not above, and not below, its limits.
+// Counted tokens of a quad's places in `mask`, their kinds, their log ratios, and the weighted advantages
+// of those that a gradient flows through where the ratio is not above, and not below, its limits.
 __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x, unsigned mask) {
     Sum t{};
 #pragma unroll
@@ -291,9 +292,9 @@ __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x,
         t.n += 1;
         t.a += x.log_ratio(p, e);
         const double flow = static_cast<double>(x.w[e]) * static_cast<double>(x.a[e]);
-        if (!(x.a[e] < 0.0f)) t.b += flow;           // (a NaN goes to both)
-        if (!(x.a[e] > 0.0f)) t.c += flow;
-        t.kinds |= x.a[e] > 0.0f ? kRises : x.a[e] < 0.0f ? kFalls : kLevel;
+        if (x.a[e] > 0.0f) t.b += flow;
+        if (x.a[e] < 0.0f) t.c += flow;
+        t.kinds |= x.a[e] > 0.0f ? kRises : x.a[e] < 0.0f ? kFalls : flow != flow ? kBad : kLevel;
     }
     return t;
 }
@@ -302,12 +303,13 @@ __device__ __forceinline__ Ratio solve_policy(const PolicyTerms& terms, const Su
     if (t.n == 0) return {0.0, 1.0f, 0.0f};          // no token takes it
     const double share = 1.0 / static_cast<double>(t.n), d = t.a * share;
     const bool up = !(d > terms.log_high), down = !(d < terms.log_low || d > terms.log_dual);
-    double flow = 0.0;
+    double flow = t.kinds & kBad ? __builtin_nan("") : 0.0;
     if (up) flow += t.b;
     if (down) flow += t.c;
     const float r = exp_of(d);
     // Without a token that is not clipped there is no slope, also where r is inf.
-    if ((t.kinds & (kLevel | (up ? kRises : 0u) | (down ? kFalls : 0u))) == 0) return {d, r, 0.0f};
+    if ((t.kinds & (kLevel | kBad | (up ? kRises : 0u) | (down ? kFalls : 0u))) == 0)
+        return {d, r, 0.0f};
     return {d, r, static_cast<float>(-static_cast<double>(r) * flow * share)};
 }
 

@@ -79,3 +79,25 @@ def test_what_an_infinite_ratio_does_not_clip_goes_on(n, offsets):
     assert (got["loss"][a:b] == np.where(counted[a:b], INF, 0)).all()
     assert (got["dlogprob"][offsets[2]:offsets[3]] == 0).all()
     assert np.isfinite(got["dlogprob"][b:]).all()
+
+
+@pytest.mark.parametrize("n,offsets", SIZES)
+@pytest.mark.parametrize("gap", [2.0, 100.0, -2.0])
+def test_a_bad_advantage_reaches_its_sequence_beyond_every_limit(n, offsets, gap):
+    """A NaN is clipped by no limit, so that it is in the sequence's slope whatever the ratio is."""
+    c = OP.constants(0.2, 0.2, 3.0)
+    x = _clipped_everywhere(n, offsets, [0.01, 0.02, gap, 0.03], [1, -1, 1, 1])
+    clean = P.run_policy(c, x, offsets)
+    at = offsets[2]
+    x["A"][at] = np.nan
+    got = P.run_policy(c, x, offsets)
+    a, b = offsets[2], offsets[3]
+    counted = x["w"][a:b] != 0
+    assert np.isnan(got["dlogprob"][a:b][counted]).all()
+    assert (got["dlogprob"][a:b][~counted] == 0).all()
+    assert np.isnan(got["loss"][at]) and np.isnan(got["totals"][0])
+    for lo, hi in ((0, a), (b, n)):
+        assert np.array_equal(got["dlogprob"][lo:hi], clean["dlogprob"][lo:hi])
+    want = OP.policy(c, x["lp"], x["A"], x["w"], x["old"], x["ref"], None, offsets)
+    assert got["counts"].tolist() == want["counts"].tolist()
+    assert np.array_equal(np.isnan(got["dlogprob"]), np.isnan(want["dlogprob"]))

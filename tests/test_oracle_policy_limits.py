@@ -17,3 +17,9 @@ def test_a_clipped_sequence_has_no_slope_at_an_infinite_ratio():
     out = OP.policy(OP.constants(), [-1.0, -1.0], [-1.0, 1.0], [0.5, 0.5], [-1000.0, -900.0],
                     offsets=[0, 2])
     assert out["dlogprob"].tolist() == [INF, INF]            # A < 0 is not clipped above
+
+
+def test_a_bad_advantage_is_in_its_sequences_slope():
+    out = OP.policy(OP.constants(dual_clip=3.0), [-1.0] * 3, [np.nan, 1.0, 1.0], [1.0] * 3,
+                    [-5.0, -5.0, -1.0], offsets=[0, 2, 3])
+    assert np.isnan(out["dlogprob"][:2]).all() and out["dlogprob"][2] == -1.0
