@@ -28,9 +28,10 @@ __device__ __forceinline__ Split split(double d) {
     const float h = static_cast<float>(d);
     return {h, fabsf(h) < 1e30f ? static_cast<float>(d - static_cast<double>(h)) : 0.0f};
 }
+// Beyond 128 exp(h) is 0 or inf already, and from 2^25 on l is no small part of 1 any more.
 __device__ __forceinline__ float exp_of(double d) {
     const Split s = split(d);
-    return expf(s.h) * (1.0f + s.l);
+    return expf(s.h) * (1.0f + (fabsf(s.h) < 128.0f ? s.l : 0.0f));
 }
 
 // exp(d) - 1, and exp(d) - 1 - d: near 0 the series d^2 (1/2 + d/6 + ...), whose first term left out

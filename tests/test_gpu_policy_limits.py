@@ -101,3 +101,41 @@ def test_a_bad_advantage_reaches_its_sequence_beyond_every_limit(n, offsets, gap
     want = OP.policy(c, x["lp"], x["A"], x["w"], x["old"], x["ref"], None, offsets)
     assert got["counts"].tolist() == want["counts"].tolist()
     assert np.array_equal(np.isnan(got["dlogprob"]), np.isnan(want["dlogprob"]))
+
+
+# Log ratios past 2^25, whose float32 rounding leaves a rest of a whole or more.
+FAR = [(-3.0, -1e9), (-1.0, -1e8), (-5.0, -3e7), (-7.0, -1e29), (-0.5, -3e38), (-1.0, -200.0)]
+
+
+@pytest.mark.parametrize("offsets", [None, list(range(len(FAR) + 1))])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_ratios_of_a_filled_in_log_probability(offsets, sign):
+    """An old (or a new) log probability of a large negative value: the ratio is inf, or 0."""
+    lp, old = (np.array(v, np.float32) for v in zip(*FAR))
+    n = len(lp)
+    x = dict(lp=lp, old=old, A=np.full(n, sign, np.float32), w=np.full(n, 0.5, np.float32), ref=None,
+             H=None)
+    got = P.run_policy(OP.constants(), x, offsets)
+    if sign > 0:                                         # clipped
+        assert (got["loss"] == np.float32(-0.5) * np.float32(1.2)).all()
+        assert (got["dlogprob"] == 0).all() and got["counts"].tolist() == [n, n]
+    else:
+        assert (got["loss"] == INF).all() and (got["dlogprob"] == INF).all()
+    got = P.run_policy(OP.constants(clip_low=1.0, clip_high=np.inf), x, offsets)
+    assert (got["loss"] == -sign * INF).all() and (got["dlogprob"] == -sign * INF).all()
+    x = dict(x, lp=old, old=lp)                          # the ratio is 0
+    got = P.run_policy(OP.constants(clip_low=1.0), x, offsets)
+    assert (got["loss"] == 0).all() and (got["dlogprob"] == 0).all()
+
+
+def test_ratios_of_a_filled_in_log_probability_over_logits():
+    rows, vocab = len(FAR), 1000
+    x = torch.zeros(rows, vocab, device="cuda")
+    f = dict(dtype=torch.float32, device="cuda")
+    old = torch.tensor([o for _, o in FAR], **f)
+    loss, out = torch.empty(rows, **f), torch.empty_like(x)
+    ids = torch.arange(rows, device="cuda")
+    for sign, want in ((1.0, -1.2), (-1.0, float("inf"))):
+        F.policy_logits_loss_grad(x, ids, torch.full((rows,), sign, **f), torch.ones(rows, **f), loss,
+                                  out, old_logprob=old)
+        assert torch.equal(loss.cpu(), torch.full((rows,), want)), loss
