@@ -580,9 +580,11 @@ __device__ __forceinline__ PairResult solve_pair(const PreferenceParams& p, int6
     const double lead = cs - rs, h = p.beta * lead - p.margin;
     double value, slope;                           // slope: in `lead`
     if (p.kind == FSDPSHARD_LOGISTIC) {
-        // log(1 + e^-h) and its slope from e^-|h|, which does not overflow
-        const double e = exp(-fabs(h));
-        value = log1p(e) + (h < 0.0 ? -h : 0.0) + p.smoothing * h;
+        // log(1 + e^-h) and its slope from e^-|h|, which does not overflow; no 0 inf and no inf - inf
+        // where h is infinite
+        const double e = exp(-fabs(h)), kept = h < 0.0 ? p.smoothing - 1.0 : p.smoothing;
+        value = log1p(e);
+        if (kept != 0.0) value += kept * h;
         slope = p.beta * (p.smoothing - (h < 0.0 ? 1.0 : e) / (1.0 + e));
     } else if (p.kind == FSDPSHARD_HINGE) {
         value = h < 1.0 || h != h ? 1.0 - h : 0.0;

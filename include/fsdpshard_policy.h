@@ -57,7 +57,8 @@ typedef enum fsdpshard_preference_kind {
  * divided by the sum of w where length_normalised is 1.  With d = s of the chosen sequence - s of
  * the rejected one and h = beta d - margin, the kinds above give a pair's loss.  The logistic
  * one's label_smoothing is the chance that the pair is labelled the wrong way round:
- * -(1 - label_smoothing) log sigmoid(h) - label_smoothing log sigmoid(-h).
+ * -(1 - label_smoothing) log sigmoid(h) - label_smoothing log sigmoid(-h), of which a factor of 0 leaves
+ * its term out, also where h is infinite.
  */
 typedef struct fsdpshard_preference {
     int32_t kind;                 /* fsdpshard_preference_kind                                */

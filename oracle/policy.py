@@ -104,8 +104,11 @@ def preference(lp, offsets, ref=None, w=None, dloss=None, kind="logistic", beta=
         lead = score[0] - score[1]
         h = beta * lead - margin
         if kind == "logistic":
-            soft = math.log1p(math.exp(-abs(h))) + max(-h, 0.0)
-            loss = soft + smoothing * h
+            # -(1 - smoothing) log sigmoid(h) - smoothing log sigmoid(-h); a factor of 0 leaves its
+            # term out, also where h is infinite
+            small = math.log1p(math.exp(-abs(h)))
+            loss = sum(a * (small + max(z, 0.0))
+                       for a, z in ((1 - smoothing, -h), (smoothing, h)) if a)
             slope = beta * (smoothing - 1 / (1 + math.exp(min(h, 700))))
         elif kind == "hinge":
             loss, slope = max(0.0, 1 - h), -beta if h < 1 else 0.0

@@ -139,3 +139,26 @@ def test_ratios_of_a_filled_in_log_probability_over_logits():
         F.policy_logits_loss_grad(x, ids, torch.full((rows,), sign, **f), torch.ones(rows, **f), loss,
                                   out, old_logprob=old)
         assert torch.equal(loss.cpu(), torch.full((rows,), want)), loss
+
+
+# pairs (chosen, rejected) of one token each
+ENDS = np.array([-1.0, -np.inf, -np.inf, -1.0, -1.0, -2.0], np.float32)
+
+
+@pytest.mark.parametrize("tokens", [6, 4000])
+@pytest.mark.parametrize("smoothing", [0.0, 0.25])
+def test_preference_of_a_sequence_without_a_chance(tokens, smoothing):
+    """log(1 + exp(-h)) and its slope at h = inf and -inf, where a product of 0 and inf must not
+    arise."""
+    lp = np.concatenate([ENDS, np.full(tokens - 6, -1.0, np.float32)])
+    x = dict(lp=lp, ref=np.zeros(tokens, np.float32), w=np.ones(tokens, np.float32))
+    g = np.array([2.0, 2.0, 2.0], np.float32)
+    say(f"preference at infinity, {tokens} tokens, smoothing {smoothing}")
+    got = P.run_preference(x, np.arange(7), g, beta=0.5, label_smoothing=smoothing)
+    assert got["loss"][0] == (INF if smoothing else 0) and got["loss"][1] == INF
+    assert np.isfinite(got["loss"][2])
+    up, down = 2 * 0.5 * smoothing, 2 * 0.5 * (smoothing - 1)
+    assert got["dlogprob"][:4].tolist() == [up, -up, down, -down]
+    assert got["rewards"][:2].tolist() == [[-0.5, -np.inf], [-np.inf, -0.5]]
+    want = OP.preference(lp, np.arange(7), x["ref"], x["w"], g, beta=0.5, smoothing=smoothing)
+    assert np.array_equal(want["loss"][:2], got["loss"][:2])

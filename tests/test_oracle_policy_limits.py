@@ -23,3 +23,12 @@ def test_a_bad_advantage_is_in_its_sequences_slope():
     out = OP.policy(OP.constants(dual_clip=3.0), [-1.0] * 3, [np.nan, 1.0, 1.0], [1.0] * 3,
                     [-5.0, -5.0, -1.0], offsets=[0, 2, 3])
     assert np.isnan(out["dlogprob"][:2]).all() and out["dlogprob"][2] == -1.0
+
+
+def test_preference_at_infinite_margins():
+    lp = [-1.0, -INF, -INF, -1.0]
+    for s in (0.0, 0.25):
+        out = OP.preference(lp, range(5), dloss=[1.0, 1.0], beta=0.5, smoothing=s)
+        assert out["loss"].tolist() == [INF if s else 0.0, INF]
+        np.testing.assert_allclose(out["dlogprob"],
+                                   [0.5 * s, -0.5 * s, 0.5 * (s - 1), -0.5 * (s - 1)], atol=1e-300)
