@@ -71,10 +71,13 @@ __device__ __forceinline__ float gain_of(const PolicyTerms& p, float a, float r,
     return (d < p.log_low ? p.low : p.dual) * a;
 }
 
+// Whether a factor is finite in float32, too: as inf it would make a term of 0 a NaN.
+bool finite_float(double x) { return std::isfinite(static_cast<float>(x)); }
+
 bool check_policy(const fsdpshard_policy* c, PolicyTerms* p) {
     if (c == nullptr || !(c->clip_low >= 0.0) || !(c->clip_high >= 0.0) ||
-        !(c->dual_clip == 0.0 || c->dual_clip >= 1.0) || !std::isfinite(c->dual_clip) ||
-        !(c->kl_coef >= 0.0) || !std::isfinite(c->kl_coef) || !std::isfinite(c->entropy_coef))
+        !(c->dual_clip == 0.0 || c->dual_clip >= 1.0) || !finite_float(c->dual_clip) ||
+        !(c->kl_coef >= 0.0) || !finite_float(c->kl_coef) || !finite_float(c->entropy_coef))
         return false;
     const double low = c->clip_low < 1.0 ? 1.0 - c->clip_low : 0.0;
     p->low = static_cast<float>(low);

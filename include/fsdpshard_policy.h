@@ -37,7 +37,7 @@
 extern "C" {
 #endif
 
-/* The policy loss's constants (float64 on the host). */
+/* The policy loss's constants (float64 on the host; "finite": in float32, too). */
 typedef struct fsdpshard_policy {
     double clip_low;       /* >= 0; from 1 on, and +inf: no lower limit                       */
     double clip_high;      /* >= 0; +inf: no upper limit                                      */
