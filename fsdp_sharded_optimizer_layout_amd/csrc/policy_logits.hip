@@ -12,6 +12,13 @@
 
 namespace {
 
+// What a row's gradient is made of: -p_i (g + h (log p_i + H)) c = 2^u (coef + tilt u) with u = c2 (x_i -
+// m), since log p_i + H is ln 2 (u - t / s); `token` is the token's own entry.
+struct RowScratch {
+    float coef, tilt, token, m;
+    int state;                 // what the row gets: 0 its gradient, 1 zeros, 2 NaN
+};
+
 struct PolicyLogitsParams {
     PolicyTerms terms;
     const void* x;
@@ -23,6 +30,7 @@ struct PolicyLogitsParams {
     void* out;
     int64_t ostride;
     float4* part_sets;                 // [rows, splits]: maximum, r, t of each part
+    RowScratch* scratch;               // [rows]
     int32_t splits, part_vecs, grad_splits, grad_vecs;
     int64_t unit0;
 };
@@ -63,14 +71,7 @@ __device__ __forceinline__ bool counted_row(const PolicyLogitsParams& p, int64_t
     return false;
 }
 
-// The gradient of a row: -p_i (g + h (log p_i + H)) c = 2^u (coef + tilt u) with u = c2 (x_i - m), since
-// log p_i + H is ln 2 (u - t / s); `token` is the token's own entry.
-struct RowScratch {
-    float coef, tilt, token, m;
-    int state;                 // what the row gets: 0 its gradient, 1 zeros, 2 NaN
-};
-
-// Works a row out from its set, in every lane of a wave.
+// Works a row out from its set, in every lane of a wave; its first lane writes.
 template <bool Entropy>
 __device__ __forceinline__ void solve_row(const PolicyLogitsParams& p, int64_t r, float w,
                                           const Set& set, float token_logit, bool writes,
@@ -100,6 +101,7 @@ __device__ __forceinline__ void solve_row(const PolicyLogitsParams& p, int64_t r
         if (lpf != -kInf) token -= h * expf(lpf) * (lpf + st.entropy);
     }
     sh.token = token;
+    sh.m = st.m;
     sh.state = (t.dlogprob == 0.0f && (!Entropy || t.dentropy == 0.0f)) || st.m == -kInf ? 1
                : st.m != st.m                                                         ? 2
                                                                                       : 0;
@@ -119,6 +121,19 @@ __device__ __forceinline__ u32x4 row_gradient(float* x, float c2, float m, float
         for (int e = 0; e < kElems<T>; ++e) x[e] = e == token_elem ? token : x[e];
     }
     return pack<T>(x);
+}
+
+// The gradient of a part that has been loaded.
+template <typename T, bool Entropy, int Loads>
+__device__ __forceinline__ void write_gradient(const Row<T>& row, const OutRow<T>& out,
+                                               const Part& part, const u32x4 (&raw)[Loads], float c2,
+                                               int64_t y, const RowScratch& of) {
+    const float m = of.m, coef = of.coef, tilt = of.tilt, token = of.token;
+    const int token_vec = (static_cast<int>(y) + row.phase) / kElems<T>;
+    const int token_elem = (static_cast<int>(y) + row.phase) % kElems<T>;
+    write_part(row, out, part, raw, [&](float* x, int v) {
+        return row_gradient<T, Entropy>(x, c2, m, coef, tilt, v == token_vec, token_elem, token);
+    });
 }
 
 template <typename T, int Threads, int Vecs, bool Entropy, bool Once>
@@ -246,20 +261,18 @@ __global__ __launch_bounds__(Threads, 4) void policy_whole_kernel(PolicyLogitsPa
 }
 
 // ------------------------------------------------------------------------------------------------
-// Rows too long for registers, small matrices: the sets of the rows' parts, then the gradient, each of
-// whose work-groups joins its row's parts and works out the loss by itself; the first of a row writes
-// the row's outputs.  The gradient needs the token's logit as it was, so not in place.
+// Rows too long for registers: first the sets of the rows' parts.
 
-template <typename T, bool Entropy>
+template <typename T, bool Entropy, bool Once>
 __global__ __launch_bounds__(kBlock) void policy_part_kernel(PolicyLogitsParams p) {
     __shared__ BlockScratch bs;
     const float c2 = in_log2(p.c);
     const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.splits);
-    if (p.ids[r] < 0 || p.weight[r] == 0.0f) return;
+    if (p.ids[r] < 0 || p.weight[r] == 0.0f) return;   // not counted, and not read
     const Row<T> row(p.x, r, p.stride, p.vocab);
     const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
     Acc acc;
-    stream<kBlock, false>(
+    stream<kBlock, Once>(
         row, part, [](u32x4&, int) {},
         [&](const float* x, int) {
             add_batch<kBatch, Entropy>(acc, x, max_of<kBatch>(x), c2);
@@ -277,12 +290,22 @@ __global__ __launch_bounds__(kBlock) void policy_part_kernel(PolicyLogitsParams 
     if (threadIdx.x == 0) p.part_sets[unit] = make_float4(set.m, set.r, set.t, 0.0f);
 }
 
+// The set of a row from its parts', in every lane.
+__device__ __forceinline__ Set join_parts(const PolicyLogitsParams& p, int64_t r, float c2) {
+    const float4* sets = p.part_sets + r * p.splits;
+    return join_sets(p.splits, c2, [&](int i) { return Set{sets[i].x, sets[i].y, sets[i].z}; });
+}
+
+// Small matrices: then the gradient, each of whose work-groups joins its row's parts and works out the
+// loss by itself; the first of a row writes the row's outputs.  The gradient needs the token's logit as it
+// was, so not in place.
+
 // Vectors a thread takes; each part works out its row's loss.  Measured with 2, 4 and 8 on fp32 64 x
 // 131072: 27.3, 25.2 and 23.7 us; 256 rows 79, 75 and 71.
-constexpr int kGradLoads = 8;
+constexpr int kJoinLoads = 8;
 
 template <typename T, bool Entropy>
-__global__ __launch_bounds__(kBlock) void policy_grad_kernel(PolicyLogitsParams p) {
+__global__ __launch_bounds__(kBlock) void policy_join_grad_kernel(PolicyLogitsParams p) {
     __shared__ RowScratch sh;
     const float c2 = in_log2(p.c);
     const int tid = threadIdx.x;
@@ -297,56 +320,55 @@ __global__ __launch_bounds__(kBlock) void policy_grad_kernel(PolicyLogitsParams 
         fill_part<kBlock>(row, out, part, y < 0 || w == 0.0f ? 0.0f : __builtin_nanf(""));
         return;
     }
-    u32x4 raw[kGradLoads];             // arrives while the loss is worked out
+    u32x4 raw[kJoinLoads];             // arrives while the loss is worked out
     load_part(row, part, raw);
-    if (tid < kWave) {
-        const float4* sets = p.part_sets + r * p.splits;
-        const Set set = join_sets(p.splits, c2,
-                                  [&](int i) { return Set{sets[i].x, sets[i].y, sets[i].z}; });
-        solve_row<Entropy>(p, r, w, set, row.at(static_cast<int>(y)), split == 0, sh);
-        if (tid == 0) sh.m = set.m;
-    }
+    if (tid < kWave)
+        solve_row<Entropy>(p, r, w, join_parts(p, r, c2), row.at(static_cast<int>(y)), split == 0, sh);
     __syncthreads();
     if (sh.state != 0) {
         fill_part<kBlock>(row, out, part, sh.state == 2 ? __builtin_nanf("") : 0.0f);
         return;
     }
-    const float m = sh.m, coef = sh.coef, tilt = sh.tilt, token = sh.token;
-    const int token_vec = (static_cast<int>(y) + row.phase) / kElems<T>;
-    const int token_elem = (static_cast<int>(y) + row.phase) % kElems<T>;
-    write_part(row, out, part, raw, [&](float* x, int v) {
-        return row_gradient<T, Entropy>(x, c2, m, coef, tilt, v == token_vec, token_elem, token);
-    });
+    write_gradient<T, Entropy>(row, out, part, raw, c2, y, sh);
 }
 
-// ------------------------------------------------------------------------------------------------
-// Others: the loss and its slopes between the log probabilities and the gradient.
+// Others, and in place: between the two a launch that works the rows out, a wave each, from the same
+// sets, so that a token falls on the same side of a limit whatever way its row takes.
 
-struct RowLossParams {
-    PolicyLogitsParams p;
-    float *logprob, *entropy, *dlogprob, *dentropy;
-    int64_t unit0;
-};
-
-__global__ __launch_bounds__(kBlock) void policy_rows_kernel(RowLossParams q) {
-    const PolicyLogitsParams& p = q.p;
-    const int64_t r = (q.unit0 + blockIdx.x) * kBlock + threadIdx.x;
-    if (r >= p.rows) return;
+template <typename T, bool Entropy>
+__global__ __launch_bounds__(kWave) void policy_rows_kernel(PolicyLogitsParams p) {
+    const int64_t r = p.unit0 + blockIdx.x, y = p.ids[r];
     const float w = p.weight[r];
-    const int64_t y = p.ids[r];
-    const bool counted = y >= 0 && w != 0.0f;
-    TokenLoss t{0.0f, 0.0f, 0.0f};
-    float lp = 0.0f, h = 0.0f;
-    if (counted) {
-        lp = q.logprob[r];                         // NaN where y >= vocab
-        h = y < p.vocab ? q.entropy[r] : lp;
-        t = token_loss(p, r, w, static_cast<double>(lp), h);
+    RowScratch& to = p.scratch[r];
+    if (!counted_row(p, r, y, w, threadIdx.x == 0)) {
+        if (threadIdx.x == 0) to.state = y < 0 || w == 0.0f ? 1 : 2;
+        return;
     }
-    p.loss[r] = t.loss;
-    q.dlogprob[r] = t.dlogprob;
-    q.dentropy[r] = t.dentropy;
-    if (p.logprob) p.logprob[r] = lp;
-    if (p.entropy) p.entropy[r] = h;
+    const float token_logit = Row<T>(p.x, r, p.stride, p.vocab).at(static_cast<int>(y));
+    solve_row<Entropy>(p, r, w, join_parts(p, r, in_log2(p.c)), token_logit, true, to);
+}
+
+// Vectors a thread takes.  Measured, us with 1, 2 and 4, without entropies: bf16 512 x 131072 76.5, 75.3 and
+// 75.6, 4096 x 131072 542, 516 and 537, fp32 512 x 65536 77.8, 77.8 and 79.0; with them: bf16 2048 x 151936
+// 342, 333 and 336, 4096 x 131072 582, 585 and 580, in place 586, 569 and 597, fp32 512 x 65536 79.3, 81.3
+// and 80.8, 2048 x 65536 276, 285 and 280.
+template <typename T, bool Entropy>
+constexpr int kGradLoads = sizeof(T) == 4 && Entropy ? 1 : 2;
+
+template <typename T, bool Entropy>
+__global__ __launch_bounds__(kBlock) void policy_grad_kernel(PolicyLogitsParams p) {
+    const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.grad_splits);
+    const Row<T> row(p.x, r, p.stride, p.vocab);
+    const OutRow<T> out(p.out, r, p.ostride, row);
+    const Part part(row, static_cast<int>(unit - r * p.grad_splits), p.grad_vecs);
+    const RowScratch from = p.scratch[r];
+    if (from.state != 0) {
+        fill_part<kBlock>(row, out, part, from.state == 2 ? __builtin_nanf("") : 0.0f);
+        return;
+    }
+    u32x4 raw[kGradLoads<T, Entropy>];
+    load_part(row, part, raw);
+    write_gradient<T, Entropy>(row, out, part, raw, in_log2(p.c), p.ids[r], from);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -387,46 +409,65 @@ WholeKernel whole_kernel(const fsdpshard_logits* x, bool entropy, bool once) {
 }
 
 // Small matrices, not in place: the gradient joins the rows' parts by itself, in two launches instead of
-// four.  Measured, us joined and apart: bf16 16 x 131072 13.3 and 19.5, fp32 32 x 131072 16.2 and 20.8, 64
-// rows 23.7 and 27.8, 128 rows 38 and 42, 256 rows (128 MiB) 71 and 79; bf16 256 rows 41.7 and 40.6.
+// three.  Measured, us joined and apart: bf16 16 x 131072 12.1 and 14.3, 64 rows 16.4 and 17.8, 128 rows
+// 23.8 and 25.3, 192 rows 32.9 and 32.9, 256 rows 39.3 and 39.4 (with entropies 40.8 and 42.0), 256 x 70001
+// 24.7 and 26.1; fp32 32 x 131072 14.9 and 17.3, 64 rows 22.6 and 24.5, 128 rows 37.1 and 38.6, 256 rows
+// (128 MiB) 70.1 and 74.5.
 constexpr int64_t kJoinRows = 256, kJoinBytes = int64_t{128} << 20;
 
-int launch_joined(PolicyLogitsParams& p, int32_t dtype, bool entropy, void* workspace,
-                  void* stream) {
+// A kernel by the matrix's type, and by whether entropies are wanted.
+template <typename Get>
+const void* long_form(int32_t dtype, bool entropy, Get get) {
+    return by_dtype(dtype, [&](auto t) {
+        return entropy ? get(t, std::true_type{}) : get(t, std::false_type{});
+    });
+}
+
+int launch_long(PolicyLogitsParams& p, int32_t dtype, bool entropy, bool joined, bool once,
+                void* workspace, void* stream) {
     const Cut cut = cut_rows(p.rows, p.vocab, element_bytes(dtype));
-    const Cut grad = cut_gradient(p.vocab, element_bytes(dtype), kGradLoads * kBlock);
+    const int loads = joined ? kJoinLoads
+                      : dtype != FSDPSHARD_FP32 ? (entropy ? kGradLoads<Bf16, true> : kGradLoads<Bf16, false>)
+                                                : (entropy ? kGradLoads<float, true> : kGradLoads<float, false>);
+    const Cut grad = cut_gradient(p.vocab, element_bytes(dtype), loads * kBlock);
     p.splits = cut.splits;
     p.part_vecs = cut.part_vecs;
     p.grad_splits = grad.splits;
     p.grad_vecs = grad.part_vecs;
     p.part_sets = static_cast<float4*>(workspace);
-    const void* kernel = by_dtype(dtype, [&](auto t) {
+    p.scratch = reinterpret_cast<RowScratch*>(p.part_sets + p.rows * p.splits);
+    const void* kernel = long_form(dtype, entropy, [&](auto t, auto e) {
         using T = decltype(t);
-        return entropy ? KERNEL(policy_part_kernel<T, true>) : KERNEL(policy_part_kernel<T, false>);
+        return once ? KERNEL(policy_part_kernel<T, decltype(e)::value, true>)
+                    : KERNEL(policy_part_kernel<T, decltype(e)::value, false>);
     });
-    const int rc = launch_units(kernel, p.rows * p.splits, p, 0, stream);
+    int rc = launch_units(kernel, p.rows * p.splits, p, 0, stream);
     if (rc != FSDPSHARD_OK) return rc;
-    kernel = by_dtype(dtype, [&](auto t) {
-        using T = decltype(t);
-        return entropy ? KERNEL(policy_grad_kernel<T, true>) : KERNEL(policy_grad_kernel<T, false>);
+    if (joined) {
+        kernel = long_form(dtype, entropy, [](auto t, auto e) {
+            return KERNEL(policy_join_grad_kernel<decltype(t), decltype(e)::value>);
+        });
+        return launch_units(kernel, p.rows * p.grad_splits, p, 0, stream);
+    }
+    kernel = long_form(dtype, entropy, [](auto t, auto e) {
+        return KERNEL(policy_rows_kernel<decltype(t), decltype(e)::value>);
+    });
+    rc = launch_units(kernel, p.rows, p, 0, stream, kWave);
+    if (rc != FSDPSHARD_OK) return rc;
+    kernel = long_form(dtype, entropy, [](auto t, auto e) {
+        return KERNEL(policy_grad_kernel<decltype(t), decltype(e)::value>);
     });
     return launch_units(kernel, p.rows * p.grad_splits, p, 0, stream);
 }
 
-int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
-
-// Bytes of a long matrix's log probabilities, entropies, statistics and slopes.
-int64_t row_floats(int64_t rows) { return up16(rows * 4 * 6); }
-
 }  // namespace
 
 extern "C" int64_t policy_logits_loss_grad_workspace_bytes(int64_t rows, int64_t vocab) {
-    const int64_t need = token_logprobs_workspace_bytes(rows, vocab, 0);
-    if (need < 0) return -1;
+    if (rows < 0 || rows > kMaxRows || vocab < 1 || vocab > FSDPSHARD_MAX_VOCAB) return -1;
     // Whether a row fits the registers depends on its type and place: 32 bits, out of phase.
     if ((vocab + 6) / 4 <= 16 * 512) return 0;
-    const int64_t sets = rows <= kJoinRows ? rows * most_splits(rows, vocab) * 16 : 0;
-    return row_floats(rows) + need > sets ? row_floats(rows) + need : sets;
+    return rows * (most_splits(rows, vocab) * static_cast<int64_t>(sizeof(float4)) +
+                   static_cast<int64_t>(sizeof(RowScratch)));
 }
 
 extern "C" int policy_logits_loss_grad(const fsdpshard_logits* logits, const int64_t* ids,
@@ -479,19 +520,8 @@ extern "C" int policy_logits_loss_grad(const fsdpshard_logits* logits, const int
     const bool wants_entropy = entropy != nullptr || policy->entropy_coef != 0.0;
     const WholeKernel whole = whole_kernel(logits, wants_entropy, xbytes >= kOnceBytes);
     if (whole.kernel) return launch_units(whole.kernel, rows, p, 0, stream, whole.threads);
-    if (rows <= kJoinRows && !in_place &&
-        rows * logits->vocab * element_bytes(logits->dtype) <= kJoinBytes)
-        return launch_joined(p, logits->dtype, wants_entropy, workspace, stream);
-    float* lp = static_cast<float*>(workspace);
-    RowLossParams q{p, lp, lp + rows, lp + 4 * rows, lp + 5 * rows, 0};
-    float* stats = lp + 2 * rows;
-    char* rest = static_cast<char*>(workspace) + row_floats(rows);
-    rc = token_logprobs(logits, ids, q.logprob, q.entropy, stats, 0, nullptr, nullptr, rest,
-                        workspace_bytes - row_floats(rows), stream);
-    if (rc != FSDPSHARD_OK) return rc;
-    rc = launch_units(KERNEL(policy_rows_kernel), (rows + kBlock - 1) / kBlock, q, 0, stream);
-    if (rc != FSDPSHARD_OK) return rc;
-    return token_logprobs_grad(logits, ids, stats, q.entropy, q.dlogprob,
-                               p.terms.entropy_coef != 0.0f ? q.dentropy : nullptr, dlogits,
-                               dlogits_stride, stream);
+    const bool joined = rows <= kJoinRows && !in_place &&
+                        rows * logits->vocab * element_bytes(logits->dtype) <= kJoinBytes;
+    return launch_long(p, logits->dtype, wants_entropy, joined, !joined && xbytes >= kOnceBytes, workspace,
+                       stream);
 }
