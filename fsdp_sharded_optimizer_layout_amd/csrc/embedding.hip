@@ -484,6 +484,20 @@ __global__ __launch_bounds__(kBlock) void sort_place_kernel(SortParams p) {
 
 constexpr int kAhead = 8;                   // rows of the gradient loaded at once
 
+// Tokens of a chunk: as many as give kFewChunks of them, but at least kAhead and at most kChunk, unless
+// that makes more than kMostChunks, whose parts take workspace.  Measured with chunks of 8, 16, 32 and 64:
+// 16384 tokens into 32000 x 4096 bf16 95, 86, 85 and 85 us, 65536 added to 32000 x 8192 fp32 613, 554, 535
+// and 534.  With at most 2048, 4096 and 8192 chunks: 262144 tokens into 32000 x 64 bf16 205, 140 and 110,
+// with half of them one token 235, 205 and 246, 2^20 into 32000 x 1024 656, 610 and 581, with half of them one
+// token 680, 672 and 731 (the longest run's parts are joined by a few work-groups).
+constexpr int64_t kChunk = 32, kFewChunks = 512, kMostChunks = 4096;
+
+// The most terms of one float32 sum: as a run has in a chunk of kChunk and the next one.  In longer chunks
+// (of more than 131072 tokens) such sums are added up by themselves, 128 of them at most, so that small terms
+// are not lost one by one next to a large sum.  As float64 sums in LDS they cost up to 20 % with rows of
+// 64 columns, and 8 registers cost nothing to 3 %.
+constexpr int kTerms = 2 * kChunk;
+
 struct GradParams {
     const uint32_t *keys, *order;
     const uint8_t* seen;
@@ -549,7 +563,7 @@ __device__ __forceinline__ uint32_t sorted(const uint32_t* p, int64_t i) {
         return p[i];
 }
 
-template <typename In, typename Out, bool Uniform, bool Add>
+template <typename In, typename Out, bool Uniform, bool Add, bool Long>
 __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
     const int64_t unit = p.unit0 + blockIdx.x;
     if (!Add && unit >= p.sum_units) {
@@ -587,8 +601,25 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
     const Out* table = static_cast<const Out*>(p.table);
     const uint32_t idle = sorted<Uniform>(p.order, begin), idle_key = key_at(begin);
     float sum[kGroup] = {};
+    float before[kGroup] = {};              // Long: of the run, without the last terms
+    const auto all_terms = [&]() {
+        if constexpr (Long) {
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) {
+                sum[e] += before[e];
+                before[e] = 0.0f;
+            }
+        }
+    };
     bool follows = false;                   // past the chunk's end
     for (int j0 = begin; j0 < (follows ? after : end); j0 += kAhead) {
+        if (Long && (j0 - begin) % kTerms == 0) {
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) {
+                before[e] += sum[e];
+                sum[e] = 0.0f;
+            }
+        }
         const int limit = follows ? after : end;
         uint32_t key[kAhead + 1], order[kAhead];
         Group<In> raw[kAhead];
@@ -630,11 +661,13 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
                     follows = true;
                     continue;
                 }
+                all_terms();
                 store_group((comes ? p.head : p.tail) + static_cast<int64_t>(c) * p.padded + col,
                             sum);
                 if (!comes && col == 0) p.long_runs[1 + atomicAdd(p.long_runs, 1u)] = c;
                 return;
             }
+            all_terms();
             if (comes)
                 store_group(p.head + static_cast<int64_t>(c) * p.padded + col, sum);
             else
@@ -804,12 +837,6 @@ bool in_one_launch(int64_t tokens, int64_t vocab) {
     return tokens * (ranges > kRanges ? ranges : kRanges) <= kOneLaunchReads;
 }
 
-// Tokens of a chunk: as many as give kFewChunks of them, but at least kAhead and at most kChunk, unless
-// that makes more than kMostChunks, whose parts take workspace.  Measured with chunks of 8, 16, 32 and 64:
-// 16384 tokens into 32000 x 4096 bf16 95, 86, 85 and 85 us, 65536 added to 32000 x 8192 fp32 613, 554, 535
-// and 534.
-constexpr int64_t kChunk = 32, kFewChunks = 512, kMostChunks = 2048;
-
 int64_t chunk_of(int64_t tokens) {
     const int64_t few = (tokens + kFewChunks - 1) / kFewChunks;
     const int64_t most = (tokens + kMostChunks - 1) / kMostChunks;
@@ -846,10 +873,10 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t dim) {
     return l;
 }
 
-template <typename In, typename Out, bool Add>
+template <typename In, typename Out, bool Add, bool Long>
 const void* grad_form(const GradParams& p) {
-    return p.shift < 6 ? KERNEL(embed_grad_kernel<In, Out, false, Add>)
-                       : KERNEL(embed_grad_kernel<In, Out, true, Add>);
+    return p.shift < 6 ? KERNEL(embed_grad_kernel<In, Out, false, Add, Long>)
+                       : KERNEL(embed_grad_kernel<In, Out, true, Add, Long>);
 }
 
 int sort_ranges(SortParams& s, void* stream) {
@@ -979,10 +1006,13 @@ extern "C" int embedding_grad(const int64_t* ids, const fsdpshard_matrix* dout,
     const int64_t per = kBlock >> th.shift;
     p.sum_units = (l.chunks + per - 1) / per * th.splits;
     const int64_t fill = accumulate ? 0 : (vocab + kFillRows - 1) / kFillRows;
+    const bool long_chunks = l.chunk > kChunk;
     const void* kernel = by_dtypes(dout->dtype, dtable->dtype, [&](auto a, auto b) {
         using In = decltype(a);
         using Out = decltype(b);
-        return accumulate ? grad_form<In, Out, true>(p) : grad_form<In, Out, false>(p);
+        if (long_chunks)
+            return accumulate ? grad_form<In, Out, true, true>(p) : grad_form<In, Out, false, true>(p);
+        return accumulate ? grad_form<In, Out, true, false>(p) : grad_form<In, Out, false, false>(p);
     });
     rc = launch_units(kernel, p.sum_units + fill, p, 0, stream);
     if (rc != FSDPSHARD_OK || l.chunks < 3) return rc;      // no run is long

@@ -55,7 +55,8 @@ int embedding_lookup(const fsdpshard_matrix* table, const int64_t* ids,
  *   accumulate = 0   dtable[v] = d[v] for every row v (zeros where no token is v)
  *   accumulate = 1   dtable[v] += d[v]; rows without a token are neither read nor written
  * Tokens with an id below 0 or >= dtable->rows take no part, whatever their rows of dout hold.
- * Sums are float32 in the order of the tokens, in runs that are joined in float64; one rounding to
+ * Sums are float32 in the order of the tokens, of at most 64 terms, of which at most tokens / 2^17 + 2 are
+ * added up in float32; what a row's tokens have beyond that is joined in float64.  One rounding to
  * dtable's type.
  *
  *   ids        device, dout->rows int64 tokens
