@@ -476,7 +476,8 @@ __global__ __launch_bounds__(kBlock) void sort_place_kernel(SortParams p) {
 // add up its runs of equal tokens.  A run belongs to the chunk in which it starts, and one that ends in
 // the next chunk is followed there; so most runs are summed by one unit.  A run over three chunks or
 // more (a long one) is summed in parts: the `tail` of the chunk in which it starts, and the `head` of
-// each chunk after it, which the joining kernel adds up.  Rows without a token are set to zeros by
+// each chunk after it, which the joining kernel adds up.  It fills the chunk after the one it starts in, so
+// that of two neighbours one has a tail at most.  Rows without a token are set to zeros by
 // work-groups of the same launch, behind those that sum: before them or in turn, they took 81 to 95 us
 // instead of 67 to 84 (16384 tokens into 32000 x 4096 bf16).  Bound by memory: that call's kernel moves 390 MB
 // in 57 us with tokens spread evenly, in 70 to 76 with a text's, and 65536 tokens added to 32000 x 8192
@@ -505,7 +506,7 @@ struct GradParams {
     int64_t dstride;
     void* table;
     int64_t tstride, tokens, vocab;
-    float *head, *tail;                     // [chunks, padded]
+    float *head, *tail;                     // [chunks, padded], [(chunks + 1) / 2, padded]
     uint32_t* long_runs;                    // their number, then the chunks in which they start
     int32_t dim, padded, chunk, chunks, splits, shift;
     float scale;
@@ -662,7 +663,8 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(GradParams p) {
                     continue;
                 }
                 all_terms();
-                store_group((comes ? p.head : p.tail) + static_cast<int64_t>(c) * p.padded + col,
+                store_group((comes ? p.head + static_cast<int64_t>(c) * p.padded
+                                   : p.tail + static_cast<int64_t>(c / 2) * p.padded) + col,
                             sum);
                 if (!comes && col == 0) p.long_runs[1 + atomicAdd(p.long_runs, 1u)] = c;
                 return;
@@ -731,7 +733,7 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(GradParams p) 
         __syncthreads();
         if (wave == 0 && col < p.dim) {
             float x[kGroup];
-            widen_group(load_group(p.tail + c * p.padded + col), x);
+            widen_group(load_group(p.tail + c / 2 * p.padded + col), x);
 #pragma unroll
             for (int e = 0; e < kGroup; ++e) total[e] += x[e];
 #pragma unroll 1
@@ -863,7 +865,7 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t dim) {
     l.seen = take(vocab);
     l.long_runs = take(4 * (int64_t{1} + l.chunks));
     l.head = take(int64_t{4} * l.chunks * l.padded);
-    l.tail = take(int64_t{4} * l.chunks * l.padded);
+    l.tail = take(int64_t{4} * ((l.chunks + 1) / 2) * l.padded);
     if (!in_one_launch(tokens, vocab)) {
         l.items = take(8 * tokens);
         l.counts = take((int64_t{4} << l.bits) * l.blocks);

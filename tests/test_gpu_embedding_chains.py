@@ -56,3 +56,20 @@ def test_a_frequent_token_among_a_million(dtype):
     _check(ids, dout, vocab, a)
     F.embedding_grad(torch.from_numpy(ids).cuda(), dout, b)
     assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+@pytest.mark.parametrize("lengths", [(64,), (65,), (66, 64), (95, 33, 97), (96,), (128, 1, 64), (63, 65)])
+@pytest.mark.parametrize("first", [0, 1, 31])
+def test_long_runs_next_to_each_other(lengths, first):
+    """Runs of about two and three parts of 32 tokens, one after the other, at every place in a part;
+    each part's sums have a place of their own."""
+    runs, dim = 300, 72
+    rows = np.repeat(np.arange(runs), np.resize(lengths, runs))
+    ids = np.concatenate([np.full(first, runs), rows]).astype(np.int64)
+    rng = np.random.default_rng([first, *lengths])
+    ids = ids[rng.permutation(len(ids))]
+    dout = torch.from_numpy(rng.standard_normal((len(ids), dim)).astype(np.float32)).cuda()
+    got = torch.full((runs + 1, dim), 3.0, device="cuda")
+    say(f"runs of {lengths} after {first}")
+    F.embedding_grad(torch.from_numpy(ids).cuda(), dout, got)
+    _check(ids, dout, runs + 1, got)
