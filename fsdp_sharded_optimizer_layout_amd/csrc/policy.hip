@@ -130,34 +130,21 @@ __device__ __forceinline__ void for_sequences(const Sequences& q, Window w, int6
     }
 }
 
-// What is added up over a sequence: sums, how many tokens count, and which of kKinds there are among them
-// (of the policy loss).
+// What is added up over a sequence.
 struct Sum {
     double a, b, c;
-    int64_t n : 56;
-    uint64_t kinds : 8;
+    int64_t n;
 };
 
-// Advantages above 0, below it, and others, which no limit clips: 0, and NaN (or what becomes NaN with the
-// token's weight).
-enum Kind : unsigned { kRises = 1, kFalls = 2, kLevel = 4, kBad = 8, kKinds = 15 };
-
 // The wave's sum, in every lane.  (A count below 2^53 is exact as a float64.)
-template <bool Policy>
+template <bool Three>
 __device__ __forceinline__ Sum wave_total(const Sum& t) {
-    Sum all{wave_sum(t.a), wave_sum(t.b), 0.0,
-            static_cast<int64_t>(wave_sum(static_cast<double>(t.n))), 0};
-    if constexpr (Policy) {
-        all.c = wave_sum(t.c);
-#pragma unroll
-        for (unsigned k = 1; k <= kKinds; k *= 2)
-            if (__any(t.kinds & k)) all.kinds |= k;
-    }
-    return all;
+    return {wave_sum(t.a), wave_sum(t.b), Three ? wave_sum(t.c) : 0.0,
+            static_cast<int64_t>(wave_sum(static_cast<double>(t.n)))};
 }
 
 // The sum of sequence s over its chunks, in every lane.
-template <bool Policy>
+template <bool Three>
 __device__ __forceinline__ Sum sum_of(const Sequences& q, const Sum* parts, int64_t s) {
     const int64_t lo = clamp_to(q.offsets[s], 0, q.tokens);
     const int64_t hi = clamp_to(q.offsets[s + 1], 0, q.tokens);
@@ -169,14 +156,11 @@ __device__ __forceinline__ Sum sum_of(const Sequences& q, const Sum* parts, int6
             const Sum x = parts[c + s];
             t.a += x.a;
             t.b += x.b;
-            if (Policy) {
-                t.c += x.c;
-                t.kinds |= x.kinds;
-            }
+            if (Three) t.c += x.c;
             t.n += x.n;
         }
     }
-    return wave_total<Policy>(t);
+    return wave_total<Three>(t);
 }
 
 // A chunk's tokens and a lane's place among them.
@@ -282,8 +266,8 @@ struct TokenQuad {
     }
 };
 
-// Counted tokens of a quad's places in `mask`, their kinds, their log ratios, and the weighted advantages
-// of those that a gradient flows through where the ratio is not above, and not below, its limits.
+// Counted tokens of a quad's places in `mask`, their log ratios, and the weighted advantages of those that
+// a gradient flows through where the ratio is not above, and not below, its limits.
 __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x, unsigned mask) {
     Sum t{};
 #pragma unroll
@@ -292,24 +276,47 @@ __device__ __forceinline__ Sum add_up(const PolicyParams& p, const TokenQuad& x,
         t.n += 1;
         t.a += x.log_ratio(p, e);
         const double flow = static_cast<double>(x.w[e]) * static_cast<double>(x.a[e]);
-        if (x.a[e] > 0.0f) t.b += flow;
-        if (x.a[e] < 0.0f) t.c += flow;
-        t.kinds |= x.a[e] > 0.0f ? kRises : x.a[e] < 0.0f ? kFalls : flow != flow ? kBad : kLevel;
+        if (!(x.a[e] < 0.0f)) t.b += flow;           // (a NaN goes to both)
+        if (!(x.a[e] > 0.0f)) t.c += flow;
     }
     return t;
 }
 
-__device__ __forceinline__ Ratio solve_policy(const PolicyTerms& terms, const Sum& t) {
+// Advantages above 0, below it, and others, which no limit clips: 0, and NaN (or what becomes NaN with the
+// token's weight).
+enum Kind : unsigned { kRises = 1, kFalls = 2, kLevel = 4, kBad = 8, kKinds = 15 };
+
+// Which kinds the counted tokens of sequence s are of, in every lane of a wave.
+__device__ unsigned kinds_of(const PolicyParams& p, int64_t s) {
+    const int64_t hi = clamp_to(p.seq.offsets[s + 1], 0, p.seq.tokens);
+    unsigned mine = 0, all = 0;
+    for (int64_t i = clamp_to(p.seq.offsets[s], 0, p.seq.tokens) + threadIdx.x % kWave; i < hi; i += kWave) {
+        const float w = p.weight[i], a = p.advantage[i], flow = w * a;
+        if (w != 0.0f) mine |= a > 0.0f ? kRises : a < 0.0f ? kFalls : flow != flow ? kBad : kLevel;
+    }
+#pragma unroll
+    for (unsigned k = 1; k <= kKinds; k *= 2)
+        if (__any(mine & k)) all |= k;
+    return all;
+}
+
+__device__ __forceinline__ Ratio solve_policy(const PolicyParams& p, int64_t s, const Sum& t) {
     if (t.n == 0) return {0.0, 1.0f, 0.0f};          // no token takes it
     const double share = 1.0 / static_cast<double>(t.n), d = t.a * share;
-    const bool up = !(d > terms.log_high), down = !(d < terms.log_low || d > terms.log_dual);
-    double flow = t.kinds & kBad ? __builtin_nan("") : 0.0;
+    const bool up = !(d > p.terms.log_high), down = !(d < p.terms.log_low || d > p.terms.log_dual);
+    double flow = 0.0;
     if (up) flow += t.b;
     if (down) flow += t.c;
     const float r = exp_of(d);
-    // Without a token that is not clipped there is no slope, also where r is inf.
-    if ((t.kinds & (kLevel | kBad | (up ? kRises : 0u) | (down ? kFalls : 0u))) == 0)
-        return {d, r, 0.0f};
+    // Where r is inf, or neither sum flows, it counts whether a token is there that is not clipped: without
+    // one the slope is 0, also times inf, and a NaN advantage is in it beyond every limit.  The tokens are
+    // gone through again then, which is rare: kept with every chunk's sums, the kinds cost 3 to 10 %.
+    if (r == kInf || !(up || down)) {
+        const unsigned kinds = kinds_of(p, s);
+        if ((kinds & (kLevel | kBad | (up ? kRises : 0u) | (down ? kFalls : 0u))) == 0)
+            return {d, r, 0.0f};
+        if (kinds & kBad) flow = __builtin_nan("");
+    }
     return {d, r, static_cast<float>(-static_cast<double>(r) * flow * share)};
 }
 
@@ -373,7 +380,7 @@ __device__ void policy_sums(const PolicyParams& p, int64_t wave, int64_t waves) 
 
 __device__ void policy_solve(const PolicyParams& p, int64_t wave, int64_t waves) {
     for (int64_t s = wave; s < p.seq.count; s += waves) {
-        const Ratio r = solve_policy(p.terms, sum_of<true>(p.seq, p.sums, s));
+        const Ratio r = solve_policy(p, s, sum_of<true>(p.seq, p.sums, s));
         if (threadIdx.x % kWave == 0) p.ratios[s] = r;
     }
 }
