@@ -261,15 +261,27 @@ __global__ __launch_bounds__(Threads, 4) void policy_whole_kernel(PolicyLogitsPa
 }
 
 // ------------------------------------------------------------------------------------------------
-// Rows too long for registers: first the sets of the rows' parts.
+// Rows too long for registers: first the sets of the rows' parts.  Where a row is one part, its loss is
+// worked out here (Solve): 1000 x 66000 bf16 68 us, 72 with a launch of its own for it, with entropies 74
+// and 77; 4096 x 131072 564 and 572.
 
-template <typename T, bool Entropy, bool Once>
+// Works out that a row is not counted, or has no logit for its token; its logits are not read.
+__device__ __forceinline__ bool solved_row(const PolicyLogitsParams& p, int64_t r, int64_t y, float w) {
+    if (counted_row(p, r, y, w, threadIdx.x == 0)) return false;
+    if (threadIdx.x == 0) p.scratch[r].state = y < 0 || w == 0.0f ? 1 : 2;
+    return true;
+}
+
+template <typename T, bool Entropy, bool Once, bool Solve>
 __global__ __launch_bounds__(kBlock) void policy_part_kernel(PolicyLogitsParams p) {
     __shared__ BlockScratch bs;
     const float c2 = in_log2(p.c);
-    const int64_t unit = p.unit0 + unit_of_group(), r = row_of(unit, p.splits);
-    if (p.ids[r] < 0 || p.weight[r] == 0.0f) return;   // not counted, and not read
+    const int64_t unit = p.unit0 + unit_of_group(), r = Solve ? unit : row_of(unit, p.splits);
+    const int64_t y = p.ids[r];
+    const float w = p.weight[r];
+    if (Solve ? solved_row(p, r, y, w) : y < 0 || w == 0.0f) return;
     const Row<T> row(p.x, r, p.stride, p.vocab);
+    const float token_logit = Solve ? row.at(static_cast<int>(y)) : 0.0f;
     const Part part(row, static_cast<int>(unit - r * p.splits), p.part_vecs);
     Acc acc;
     stream<kBlock, Once>(
@@ -287,7 +299,11 @@ __global__ __launch_bounds__(kBlock) void policy_part_kernel(PolicyLogitsParams 
         });
         return rest;
     });
-    if (threadIdx.x == 0) p.part_sets[unit] = make_float4(set.m, set.r, set.t, 0.0f);
+    if constexpr (Solve) {
+        if (threadIdx.x < kWave) solve_row<Entropy>(p, r, w, set, token_logit, true, p.scratch[r]);
+    } else {
+        if (threadIdx.x == 0) p.part_sets[unit] = make_float4(set.m, set.r, set.t, 0.0f);
+    }
 }
 
 // The set of a row from its parts', in every lane.
@@ -332,20 +348,17 @@ __global__ __launch_bounds__(kBlock) void policy_join_grad_kernel(PolicyLogitsPa
     write_gradient<T, Entropy>(row, out, part, raw, c2, y, sh);
 }
 
-// Others, and in place: between the two a launch that works the rows out, a wave each, from the same
-// sets, so that a token falls on the same side of a limit whatever way its row takes.
+// Others, and in place: where rows have several parts, a launch between the two that works the rows out, a
+// wave each.  All ways use the same sets, so that a token falls on the same side of a limit whichever its
+// row takes.
 
 template <typename T, bool Entropy>
 __global__ __launch_bounds__(kWave) void policy_rows_kernel(PolicyLogitsParams p) {
     const int64_t r = p.unit0 + blockIdx.x, y = p.ids[r];
     const float w = p.weight[r];
-    RowScratch& to = p.scratch[r];
-    if (!counted_row(p, r, y, w, threadIdx.x == 0)) {
-        if (threadIdx.x == 0) to.state = y < 0 || w == 0.0f ? 1 : 2;
-        return;
-    }
+    if (solved_row(p, r, y, w)) return;
     const float token_logit = Row<T>(p.x, r, p.stride, p.vocab).at(static_cast<int>(y));
-    solve_row<Entropy>(p, r, w, join_parts(p, r, in_log2(p.c)), token_logit, true, to);
+    solve_row<Entropy>(p, r, w, join_parts(p, r, in_log2(p.c)), token_logit, true, p.scratch[r]);
 }
 
 // Vectors a thread takes.  Measured, us with 1, 2 and 4, without entropies: bf16 512 x 131072 76.5, 75.3 and
@@ -408,11 +421,11 @@ WholeKernel whole_kernel(const fsdpshard_logits* x, bool entropy, bool once) {
     return {nullptr, 0};
 }
 
-// Small matrices, not in place: the gradient joins the rows' parts by itself, in two launches instead of
-// three.  Measured, us joined and apart: bf16 16 x 131072 12.1 and 14.3, 64 rows 16.4 and 17.8, 128 rows
-// 23.8 and 25.3, 192 rows 32.9 and 32.9, 256 rows 39.3 and 39.4 (with entropies 40.8 and 42.0), 256 x 70001
-// 24.7 and 26.1; fp32 32 x 131072 14.9 and 17.3, 64 rows 22.6 and 24.5, 128 rows 37.1 and 38.6, 256 rows
-// (128 MiB) 70.1 and 74.5.
+// Small matrices, not in place: the gradient joins the rows' parts by itself, without a launch for the rows.
+// From 257 rows on a row is one part, whose launch works it out.  Measured, us joined and apart: bf16 16 x
+// 131072 12.1 and 14.3, 64 rows 16.4 and 17.8, 192 rows 32.7 and 32.5 (with entropies 35.1 and 35.8), 256 rows
+// 39.0 and 39.0, 257 rows 44.3 and 41.2 (48.1 and 45.3), 512 rows 72.9 and 71 (74.6 and 76.7), 200 x 70001 21.5
+// and 23.4; fp32 64 x 131072 22.6 and 24.5, 256 rows (128 MiB) 69.7 and 73.7, 500 x 66000 70.9 and 66.8.
 constexpr int64_t kJoinRows = 256, kJoinBytes = int64_t{128} << 20;
 
 // A kernel by the matrix's type, and by whether entropies are wanted.
@@ -436,10 +449,15 @@ int launch_long(PolicyLogitsParams& p, int32_t dtype, bool entropy, bool joined,
     p.grad_vecs = grad.part_vecs;
     p.part_sets = static_cast<float4*>(workspace);
     p.scratch = reinterpret_cast<RowScratch*>(p.part_sets + p.rows * p.splits);
+    const bool solve = !joined && p.splits == 1;
     const void* kernel = long_form(dtype, entropy, [&](auto t, auto e) {
         using T = decltype(t);
-        return once ? KERNEL(policy_part_kernel<T, decltype(e)::value, true>)
-                    : KERNEL(policy_part_kernel<T, decltype(e)::value, false>);
+        constexpr bool E = decltype(e)::value;
+        if (solve)
+            return once ? KERNEL(policy_part_kernel<T, E, true, true>)
+                        : KERNEL(policy_part_kernel<T, E, false, true>);
+        return once ? KERNEL(policy_part_kernel<T, E, true, false>)
+                    : KERNEL(policy_part_kernel<T, E, false, false>);
     });
     int rc = launch_units(kernel, p.rows * p.splits, p, 0, stream);
     if (rc != FSDPSHARD_OK) return rc;
@@ -449,11 +467,13 @@ int launch_long(PolicyLogitsParams& p, int32_t dtype, bool entropy, bool joined,
         });
         return launch_units(kernel, p.rows * p.grad_splits, p, 0, stream);
     }
-    kernel = long_form(dtype, entropy, [](auto t, auto e) {
-        return KERNEL(policy_rows_kernel<decltype(t), decltype(e)::value>);
-    });
-    rc = launch_units(kernel, p.rows, p, 0, stream, kWave);
-    if (rc != FSDPSHARD_OK) return rc;
+    if (!solve) {
+        kernel = long_form(dtype, entropy, [](auto t, auto e) {
+            return KERNEL(policy_rows_kernel<decltype(t), decltype(e)::value>);
+        });
+        rc = launch_units(kernel, p.rows, p, 0, stream, kWave);
+        if (rc != FSDPSHARD_OK) return rc;
+    }
     kernel = long_form(dtype, entropy, [](auto t, auto e) {
         return KERNEL(policy_grad_kernel<decltype(t), decltype(e)::value>);
     });
