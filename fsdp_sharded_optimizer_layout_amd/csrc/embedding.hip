@@ -104,7 +104,9 @@ __device__ __forceinline__ void store_columns(T* row, const Columns& c, const fl
 
 // Groups a thread loads at once, then stores.  Measured, us with 1, 2 and 4: 16384 x 8192 bf16 84, 64 and
 // 59, 8192 x 4099 fp32 -> bf16 24, 32 (the last group has a work-group to itself) and 24, 16384 x 4096
-// bf16 -> fp32 76, 68 and 82.
+// bf16 -> fp32 76, 68 and 82.  (Results of 32 bits stay further from a copy: a group is two vectors, whose
+// stores and loads reach half of each line.  16384 tokens of 4096 columns, spread evenly: bf16 -> fp32 78 us of
+// 57 at the rate of a copy, fp32 -> fp32 99 of 73, bf16 -> bf16 44 of 37.)
 template <typename Out>
 constexpr int kLookupGroups = sizeof(Out) == 4 ? 2 : 4;
 

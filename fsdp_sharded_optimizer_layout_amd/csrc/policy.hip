@@ -1,11 +1,12 @@
 // Losses of post-training over log probabilities of packed tokens, of libfsdpshard.so on gfx950: the
 // clipped policy loss with a KL term, and the loss over pairs of sequences, with their gradients.
 //
-// Bound by launches and the latency of a few dependent loads in each: a million tokens are 36 MB, 5.5 us
-// at the rate of a copy.  Measured, us: a policy loss of 1000003 tokens 11.7 with a ratio for each token
-// and 21 in 1024 sequences (sums 9, ratios 3, outputs 11, totals 4 in a trace), a preference loss of 512
-// pairs of 2000003 tokens 17.4 (10, 4, 6); sequences of ten tokens, of which a chunk goes through 25 one
-// after the other, take 115.
+// Bound by launches and the latency of a few dependent loads in each: a million tokens with every term are
+// 36 MB, 5.5 us at the rate of a copy.  Measured, us: a policy loss of 1000003 tokens 15.7 with a ratio for
+// each token and 24.6 in 1024 sequences (in a trace, where launches do not overlap, sums 9.8, ratios 3.6,
+// outputs 11.7, totals 3.8), a preference loss of 512 pairs of 2000003 tokens 18.7 (9.7, 4.7, 5.6).  A chunk
+// goes through its sequences one after the other: a million tokens in sequences of 250, 50 and ten take 29,
+// 46 and 118, and 19, 35 and 103 in pairs.
 
 #include "policy_common.h"
 
@@ -703,9 +704,11 @@ constexpr int64_t kMaxSequences = (int64_t{1} << 31) - 1;
 constexpr int64_t kMostGroups = 4096;       // of a launch
 
 // One work-group takes calls of up to so many tokens and sequences.  Measured in a graph, us of one
-// work-group and of the launches: a policy loss with a ratio for each of 700 tokens 4.9 and 6.9, 4096 7.6
-// and 7.2, 8192 12.3 and 7.3; 700 tokens in 4 sequences 9.1 and 12.5, 4096 in 8 15.5 and 13.9, in 64 30.8
-// and 18.6; a preference loss of 2311 tokens in 8 8.5 and 9.4, 4096 in 64 24.8 and 13.9.
+// work-group and of the launches.  Policy loss, a ratio for each token: 700 tokens 5.0 and 7.0, 2560 7.2 and
+// 7.4, 3000 7.2 and 7.4, 3500 7.9 and 7.4; in 4 sequences 1000 9.3 and 12.9, 2560 12.2 and 13.5, 4096 14.2 and
+// 14.2; in 16 sequences 1000 13.7 and 17.0, 2560 16.4 and 16.0, 3000 16.7 and 15.5; in 17 1000 15.0 and 18.0,
+// 2560 17.3 and 15.5.  Preference loss: 16 sequences 2560 9.7 and 11.0, 3000 9.9 and 10.9, 4096 10.8 and 10.6;
+// 18 sequences 1000 11.0 and 12.0, 2560 11.1 and 10.1.
 constexpr int64_t kSmallTokens = 2560;
 constexpr int64_t kSmallSequences = 16;
 bool is_small(int64_t tokens, int64_t sequences) {

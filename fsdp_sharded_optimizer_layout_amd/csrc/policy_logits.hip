@@ -6,7 +6,9 @@
 // -g expm1(log p), precise also where p is near 1.  Bound by memory, and by the arithmetic of a row,
 // which overlaps the loads and stores of the three others on its CU only: 8192 x 32000 bf16 181 us with a
 // tenth of the rows not counted (5.5 TB/s), 184 to 186 with all (5.7); two 16-bit rows of 50021 a CU, 1021
-// of them 45 us.  The separate calls read the logits twice (87 + 166 us for 8192 x 32000).
+// of them 45 us; 32-bit rows, 8192 x 32000, 363 us (5.8 TB/s).  The separate calls read the logits twice (87
+// + 166 us for 8192 x 32000).  Rows too long for registers are read twice, too, those that count: 4096 x 131072
+// bf16 564 us (5.7 TB/s of what is read and written), with half of the rows not counted 383.
 
 #include "policy_common.h"
 
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(Threads, 4) void policy_whole_kernel(PolicyLogitsPa
     const auto gradient = [&](float* x, int v) {
         return row_gradient<T, Entropy>(x, c2, m, coef, tilt, v == token_vec, token_elem, token);
     };
-    // 2^u by one fused multiply-add, as in add_batch: of u' = c2 x - b, which is u - delta.  Far from 0
+    // 2^u by one fused multiply-add, as in add_batch: of u' = c2 x - b, which is u + delta.  Far from 0
     // the difference is taken first, and the row is read again.
     const float base = c2 * m, delta = __builtin_fmaf(c2, m, -base), up = exp2_fast(-delta);
     if (fabsf(base) < 0x1p20f) {

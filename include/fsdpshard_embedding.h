@@ -35,7 +35,8 @@ typedef struct fsdpshard_matrix {
 /*
  * embedding_lookup -- out[t] = scale * table[ids[t]] for every token t of out->rows.
  * An id below 0 is a position without a token and gives zeros; an id >= table->rows is not read
- * and gives NaN.  One float32 product, one rounding to out's type (scale 1 and equal types: a copy).
+ * and gives NaN.  One float32 product, one rounding to out's type (scale 1 and equal types: a copy, in
+ * which a NaN stays a NaN, not always its bits).
  *
  *   table  [vocab, dim]; vocab up to FSDPSHARD_MAX_VOCAB.  It may be a tensor's place in a flat
  *          vector: any alignment of its element
