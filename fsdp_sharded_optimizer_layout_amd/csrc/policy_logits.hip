@@ -424,10 +424,11 @@ WholeKernel whole_kernel(const fsdpshard_logits* x, bool entropy, bool once) {
 }
 
 // Small matrices, not in place: the gradient joins the rows' parts by itself, without a launch for the rows.
-// From 257 rows on a row is one part, whose launch works it out.  Measured, us joined and apart: bf16 16 x
-// 131072 12.1 and 14.3, 64 rows 16.4 and 17.8, 192 rows 32.7 and 32.5 (with entropies 35.1 and 35.8), 256 rows
-// 39.0 and 39.0, 257 rows 44.3 and 41.2 (48.1 and 45.3), 512 rows 72.9 and 71 (74.6 and 76.7), 200 x 70001 21.5
-// and 23.4; fp32 64 x 131072 22.6 and 24.5, 256 rows (128 MiB) 69.7 and 73.7, 500 x 66000 70.9 and 66.8.
+// From 257 rows on a row of up to kMaxPartVecs is one part, whose launch works it out.  Measured, us joined
+// and apart: bf16 16 x 131072 12.1 and 14.3, 64 rows 16.4 and 17.8, 192 rows 32.7 and 32.5 (with entropies
+// 35.1 and 35.8), 256 rows 39.0 and 39.0, 257 rows 44.3 and 41.2 (48.1 and 45.3), 512 rows 72.9 and 71 (74.6
+// and 76.7), 200 x 70001 21.5 and 23.4; fp32 64 x 131072 22.6 and 24.5, 256 rows (128 MiB) 69.7 and 73.7,
+// 500 x 66000 70.9 and 66.8.
 constexpr int64_t kJoinRows = 256, kJoinBytes = int64_t{128} << 20;
 
 // A kernel by the matrix's type, and by whether entropies are wanted.
@@ -438,13 +439,16 @@ const void* long_form(int32_t dtype, bool entropy, Get get) {
     });
 }
 
+int grad_loads(int32_t dtype, bool entropy) {
+    if (dtype == FSDPSHARD_FP32) return entropy ? kGradLoads<float, true> : kGradLoads<float, false>;
+    return entropy ? kGradLoads<Bf16, true> : kGradLoads<Bf16, false>;
+}
+
 int launch_long(PolicyLogitsParams& p, int32_t dtype, bool entropy, bool joined, bool once,
                 void* workspace, void* stream) {
     const Cut cut = cut_rows(p.rows, p.vocab, element_bytes(dtype));
-    const int loads = joined ? kJoinLoads
-                      : dtype != FSDPSHARD_FP32 ? (entropy ? kGradLoads<Bf16, true> : kGradLoads<Bf16, false>)
-                                                : (entropy ? kGradLoads<float, true> : kGradLoads<float, false>);
-    const Cut grad = cut_gradient(p.vocab, element_bytes(dtype), loads * kBlock);
+    const Cut grad = cut_gradient(p.vocab, element_bytes(dtype),
+                                  (joined ? kJoinLoads : grad_loads(dtype, entropy)) * kBlock);
     p.splits = cut.splits;
     p.part_vecs = cut.part_vecs;
     p.grad_splits = grad.splits;
